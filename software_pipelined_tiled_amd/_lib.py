@@ -22,6 +22,12 @@ EXPORTS = ("gemm_plan_create", "gemm_run", "gemm_run_noalloc", "gemm_plan_destro
            "gemm_select_config", "gemm_select_parts", "gemm_schedule_tile", "gemm_pipeline_protocol", "gemm_lds_chunk_offset", "gemm_probe_mfma_peak",
            "gemm_probe_copy", "gemm_probe_read", "gemm_probe_lds_read")
 
+# every entry point include/experts.h declares
+EXPERT_EXPORTS = ("experts_sort_workspace_bytes", "experts_sort", "experts_gather", "experts_combine", "experts_combine_grad",
+                  "gemm_grouped_workspace_bytes", "gemm_grouped_run", "gemm_w4_packed_bytes", "gemm_w4_pack",
+                  "gemm_w4_workspace_bytes", "gemm_w4_run")
+GEMM_GROUPED_FORWARD, GEMM_GROUPED_GRAD_A, GEMM_GROUPED_GRAD_B = 0, 1, 2
+
 
 class GemmLibraryMissing(ImportError):
     pass
@@ -46,6 +52,18 @@ class GemmConfig(ctypes.Structure):
         for k, v in d.items():
             setattr(c, k, int(v))
         return c
+
+
+class GemmGrouped(ctypes.Structure):
+    _fields_ = [("mode", ctypes.c_int), ("rows", ctypes.c_int64), ("experts", ctypes.c_int64), ("n", ctypes.c_int64),
+                ("k", ctypes.c_int64), ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("ldx", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("ldo", ctypes.c_int64), ("stride", ctypes.c_int64), ("zero_rest", ctypes.c_int)]
+
+
+class GemmW4(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("matrices", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("group", ctypes.c_int), ("has_zeros", ctypes.c_int), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64), ("zero_rest", ctypes.c_int)]
 
 
 _lib = None
@@ -97,6 +115,20 @@ def lib() -> ctypes.CDLL:
     L.gemm_probe_lds_read.argtypes = [i32, i64, vp]
     L.gemm_probe_read.restype = i32
     L.gemm_probe_read.argtypes = [vp, i64, vp]
+    for name, args in (
+            ("experts_sort_workspace_bytes", [i64, i64, P(i64)]),
+            ("experts_sort", [vp, i32, i64, i64, vp, vp, vp, vp, i64, vp]),
+            ("experts_gather", [vp, i32, i64, i64, i64, i64, vp, vp, vp, i64, i32, vp]),
+            ("experts_combine", [vp, i32, i64, i64, i64, i64, vp, vp, vp, i32, vp, i64, vp]),
+            ("experts_combine_grad", [vp, i64, vp, i32, i64, i64, i64, i64, vp, vp, vp, i32, vp, i64, vp, i32, vp]),
+            ("gemm_grouped_workspace_bytes", [P(GemmGrouped), vp, vp, P(i64)]),
+            ("gemm_grouped_run", [P(GemmGrouped), vp, vp, vp, vp, vp, i64, vp]),
+            ("gemm_w4_packed_bytes", [i64, i64, i64, i32, i32, P(i64)]),
+            ("gemm_w4_pack", [vp, vp, vp, i64, i64, i64, i32, vp, vp]),
+            ("gemm_w4_workspace_bytes", [P(GemmW4), i32, P(i64)]),
+            ("gemm_w4_run", [P(GemmW4), vp, vp, vp, vp, vp, i64, vp])):
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = i32, args
     _lib = L
     return L
 
@@ -236,3 +268,72 @@ def gemm_probe_lds_read(swizzle: int, iters: int, stream: int = 0) -> None:
 
 def gemm_probe_read(src_ptr: int, nbytes: int, stream: int = 0) -> None:
     _check(lib().gemm_probe_read(src_ptr, nbytes, stream or None), "gemm_probe_read")
+
+
+def experts_sort_workspace_bytes(slots: int, experts: int) -> int:
+    n = ctypes.c_int64()
+    _check(lib().experts_sort_workspace_bytes(slots, experts, ctypes.byref(n)), "experts_sort_workspace_bytes")
+    return n.value
+
+
+def experts_sort(ids_ptr: int, id_bits: int, slots: int, experts: int, offsets_ptr: int, order_ptr: int, rows_ptr: int,
+                 workspace_ptr: int = 0, workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(lib().experts_sort(ids_ptr or None, id_bits, slots, experts, offsets_ptr or None, order_ptr or None,
+                              rows_ptr or None, workspace_ptr or None, workspace_bytes, stream or None), "experts_sort")
+
+
+def experts_gather(x_ptr: int, dtype: int, tokens: int, top_k: int, width: int, ldx: int, rows_ptr: int, kept_ptr: int,
+                   out_ptr: int, ldo: int, zero_rest: bool, stream: int = 0) -> None:
+    _check(lib().experts_gather(x_ptr or None, dtype, tokens, top_k, width, ldx, rows_ptr or None, kept_ptr or None,
+                                out_ptr or None, ldo, int(zero_rest), stream or None), "experts_gather")
+
+
+def experts_combine(y_ptr: int, dtype: int, tokens: int, top_k: int, width: int, ldy: int, rows_ptr: int, kept_ptr: int,
+                    weights_ptr: int, weight_dtype: int, out_ptr: int, ldo: int, stream: int = 0) -> None:
+    _check(lib().experts_combine(y_ptr or None, dtype, tokens, top_k, width, ldy, rows_ptr or None, kept_ptr or None,
+                                 weights_ptr or None, weight_dtype, out_ptr or None, ldo, stream or None), "experts_combine")
+
+
+def experts_combine_grad(dout_ptr: int, lddo: int, y_ptr: int, dtype: int, tokens: int, top_k: int, width: int, ldy: int,
+                         rows_ptr: int, kept_ptr: int, weights_ptr: int, weight_dtype: int, dy_ptr: int, lddy: int,
+                         dweights_ptr: int, zero_rest: bool, stream: int = 0) -> None:
+    _check(lib().experts_combine_grad(dout_ptr or None, lddo, y_ptr or None, dtype, tokens, top_k, width, ldy,
+                                      rows_ptr or None, kept_ptr or None, weights_ptr or None, weight_dtype, dy_ptr or None,
+                                      lddy, dweights_ptr or None, int(zero_rest), stream or None), "experts_combine_grad")
+
+
+def gemm_grouped_workspace_bytes(p: GemmGrouped, x_ptr: int, y_ptr: int) -> int:
+    n = ctypes.c_int64()
+    _check(lib().gemm_grouped_workspace_bytes(ctypes.byref(p), x_ptr or None, y_ptr or None, ctypes.byref(n)),
+           "gemm_grouped_workspace_bytes")
+    return n.value
+
+
+def gemm_grouped_run(p: GemmGrouped, x_ptr: int, y_ptr: int, out_ptr: int, offsets_ptr: int, workspace_ptr: int = 0,
+                     workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(lib().gemm_grouped_run(ctypes.byref(p), x_ptr or None, y_ptr or None, out_ptr or None, offsets_ptr or None,
+                                  workspace_ptr or None, workspace_bytes, stream or None), "gemm_grouped_run")
+
+
+def gemm_w4_packed_bytes(matrices: int, n: int, k: int, group: int, has_zeros: bool) -> int:
+    b = ctypes.c_int64()
+    _check(lib().gemm_w4_packed_bytes(matrices, n, k, group, int(has_zeros), ctypes.byref(b)), "gemm_w4_packed_bytes")
+    return b.value
+
+
+def gemm_w4_pack(q_ptr: int, scales_ptr: int, zeros_ptr: int, matrices: int, n: int, k: int, group: int, packed_ptr: int,
+                 stream: int = 0) -> None:
+    _check(lib().gemm_w4_pack(q_ptr or None, scales_ptr or None, zeros_ptr or None, matrices, n, k, group,
+                              packed_ptr or None, stream or None), "gemm_w4_pack")
+
+
+def gemm_w4_workspace_bytes(p: GemmW4, has_offsets: bool) -> int:
+    n = ctypes.c_int64()
+    _check(lib().gemm_w4_workspace_bytes(ctypes.byref(p), int(has_offsets), ctypes.byref(n)), "gemm_w4_workspace_bytes")
+    return n.value
+
+
+def gemm_w4_run(p: GemmW4, x_ptr: int, packed_ptr: int, offsets_ptr: int, out_ptr: int, workspace_ptr: int = 0,
+                workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(lib().gemm_w4_run(ctypes.byref(p), x_ptr or None, packed_ptr or None, offsets_ptr or None, out_ptr or None,
+                             workspace_ptr or None, workspace_bytes, stream or None), "gemm_w4_run")

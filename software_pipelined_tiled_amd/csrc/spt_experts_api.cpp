@@ -1,0 +1,465 @@
+// Host side of include/experts.h: argument checks, the choice of a kernel, launches. Nothing here
+// allocates or synchronises, and no state outlives a call but the devices' properties.
+#include <cstring>
+#include <mutex>
+
+#include "experts.h"
+#include "spt_experts.h"
+
+namespace {
+
+constexpr int64_t kMax32 = 0x7FFFFFFF;
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxDevices = 64;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+bool is16(gemm_dtype_t d) { return d == GEMM_F16 || d == GEMM_BF16; }
+bool is_dtype(gemm_dtype_t d) { return is16(d) || d == GEMM_F32; }
+
+// Compute units of the current device; GEMM_ERR_HIP unless it is a gfx950.
+gemm_status_t device_cus(int* cu) {
+  static std::mutex mu;
+  static int known[kMaxDevices];
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess) {
+    (void)hipGetLastError();
+    return GEMM_ERR_HIP;
+  }
+  if (dev < 0 || dev >= kMaxDevices) return GEMM_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    hipDeviceProp_t prop;
+    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) {
+      (void)hipGetLastError();
+      return GEMM_ERR_HIP;
+    }
+    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return GEMM_ERR_HIP;
+    known[dev] = prop.multiProcessorCount;
+  }
+  *cu = known[dev];
+  return GEMM_OK;
+}
+
+gemm_status_t launch(const void* fn, dim3 grid, int threads, int lds, void* arg, void* stream) {
+  void* kargs[] = {arg};
+  if (hipLaunchKernel(fn, grid, dim3(threads), kargs, lds, (hipStream_t)stream) != hipSuccess) {
+    (void)hipGetLastError();
+    return GEMM_ERR_HIP;
+  }
+  return GEMM_OK;
+}
+
+int stream_grid(int64_t threads) {
+  const int64_t b = ceil_div(threads, 256);
+  return (int)(b < 1 ? 1 : (b > 8192 ? 8192 : b));
+}
+
+// ---------------------------------------------------------------------------------- sort
+// One workgroup sorts up to kSortOne slots by itself; beyond, each workgroup takes kSortBlock of them
+// (more when there would be over 256 workgroups, since each adds up every other's counts).
+constexpr int64_t kSortOne = 8192, kSortBlock = 4096;
+struct SortShape {
+  int64_t per_block, blocks;
+};
+SortShape sort_shape(int64_t slots) {
+  if (slots <= kSortOne) return {slots, 1};
+  int64_t per = round_up(ceil_div(slots, 256), 1024);
+  if (per < kSortBlock) per = kSortBlock;
+  return {per, ceil_div(slots, per)};
+}
+
+gemm_status_t check_route(gemm_dtype_t dtype, int64_t tokens, int64_t top_k, int64_t width) {
+  if (!is_dtype(dtype) || tokens < 0 || top_k < 0 || width < 0) return GEMM_ERR_INVALID;
+  if (tokens > kMax32 || top_k > kMax32 || width > kMax32 || tokens * top_k > kMax32) return GEMM_ERR_UNSUPPORTED;
+  return GEMM_OK;
+}
+
+// Threads per token: the power of two that covers the row's 16-byte chunks, at most a workgroup.
+gemm_status_t route_grid(int64_t tokens, int64_t width, int* lanes_log2, dim3* grid) {
+  const int64_t chunks = ceil_div(width, 8);
+  int l = 0;
+  while (l < 8 && ((int64_t)1 << l) < chunks) ++l;
+  const int64_t gx = ceil_div(tokens, 256 >> l), gy = ceil_div(chunks, (int64_t)1 << l);
+  if (gx * 256 > kMax32 || gy > 65535) return GEMM_ERR_UNSUPPORTED;
+  *lanes_log2 = l;
+  *grid = dim3((unsigned)gx, (unsigned)gy);
+  return GEMM_OK;
+}
+
+// ---------------------------------------------------------------------------------- grouped
+struct Operand {
+  int64_t rows, cols, ld, rows_per, stride;  // rows of a matrix per expert; stride between experts
+  bool pad;                                  // copied to the workspace
+  int64_t pad_ld, at, bytes;
+};
+struct GroupedShape {
+  Operand x, y;
+  int64_t ws;
+};
+
+gemm_status_t grouped_shape(const gemm_grouped_t* p, const void* X, const void* Y, GroupedShape* s) {
+  if (!p || p->mode < GEMM_GROUPED_FORWARD || p->mode > GEMM_GROUPED_GRAD_B) return GEMM_ERR_INVALID;
+  if (p->rows < 0 || p->experts < 0 || p->n < 0 || p->k < 0) return GEMM_ERR_INVALID;
+  if (!is_dtype(p->in_dtype) || !is_dtype(p->out_dtype)) return GEMM_ERR_INVALID;
+  if (!is16(p->in_dtype)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t lim = (int64_t)1 << 20;
+  if (p->rows > kMax32 || p->experts > kMax32 || p->n > kMax32 || p->k > kMax32) return GEMM_ERR_UNSUPPORTED;
+  const bool gb = p->mode == GEMM_GROUPED_GRAD_B;
+  const int64_t xc = p->mode == GEMM_GROUPED_FORWARD ? p->k : p->n;
+  const int64_t oc = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
+  if (p->ldx < xc || p->ldy < p->k || p->ldo < oc) return GEMM_ERR_INVALID;
+  const int64_t mat_ld = gb ? p->ldo : p->ldy;  // of the [experts, n, k] tensor
+  if (p->experts > 1 && p->n > 0 && p->stride < (p->n - 1) * mat_ld + p->k) return GEMM_ERR_INVALID;
+  if (p->ldx >= lim || p->ldy >= lim || p->ldo >= lim) return GEMM_ERR_UNSUPPORTED;
+  s->x = Operand{p->rows, xc, p->ldx, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
+  if (gb) s->y = Operand{p->rows, p->k, p->ldy, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
+  else s->y = Operand{p->experts * p->n, p->k, p->ldy, p->n > 0 ? p->n : 1, p->stride, false, 0, 0, 0};
+  s->ws = 0;
+  Operand* ops[2] = {&s->x, &s->y};
+  const void* ptr[2] = {X, Y};
+  for (int i = 0; i < 2; ++i) {
+    Operand& o = *ops[i];
+    o.pad = (uintptr_t)ptr[i] % 16 != 0 || o.cols % 8 != 0 || o.ld % 8 != 0 || o.stride % 8 != 0;
+    if (!o.pad) continue;
+    o.pad_ld = round_up(o.cols, 8);
+    o.at = s->ws;
+    o.bytes = round_up(o.rows * o.pad_ld * 2, 256);
+    s->ws += o.bytes;
+  }
+  return GEMM_OK;
+}
+
+gemm_status_t pad_operand(Operand& o, const void** ptr, char* ws, void* stream) {
+  if (!o.pad || o.rows == 0 || o.cols == 0) return GEMM_OK;
+  spt::PadArgs a;
+  a.src = (const char*)*ptr;
+  a.dst = ws + o.at;
+  a.rows = o.rows; a.ld = o.ld; a.rows_per = o.rows_per; a.stride = o.stride;
+  a.cols = (int)o.cols; a.cols_pad = (int)o.pad_ld;
+  const gemm_status_t st = launch(spt::pad_rows_fn(), dim3(stream_grid(o.rows * (o.pad_ld / 8))), 256, 0, &a, stream);
+  *ptr = a.dst;
+  o.ld = o.pad_ld;
+  if (o.stride) o.stride = o.rows_per * o.pad_ld;
+  return st;
+}
+
+// ---------------------------------------------------------------------------------- 4-bit weights
+struct W4Shape {
+  spt::W4Entry entry;
+  int64_t nblocks, row_blocks, splits, ws;
+};
+
+gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
+  if (!p || p->rows < 0 || p->matrices < 0 || p->n < 0 || p->k < 0) return GEMM_ERR_INVALID;
+  if (!is_dtype(p->dtype) || !is_dtype(p->out_dtype)) return GEMM_ERR_INVALID;
+  if (!is16(p->dtype) || (p->group != 32 && p->group != 64 && p->group != 128)) return GEMM_ERR_UNSUPPORTED;
+  if (p->ldx < p->k || p->ldo < p->n || (!grouped && p->matrices != 1)) return GEMM_ERR_INVALID;
+  const int64_t lim = (int64_t)1 << 24;
+  if (p->n > lim || p->k > lim || p->ldx >= lim / 2 || p->rows > kMax32 || p->matrices > kMax32)
+    return GEMM_ERR_UNSUPPORTED;
+  const int64_t n16 = ceil_div(p->n, 16), kb = ceil_div(p->k, 128);
+  // rows that share a matrix, on average
+  const int64_t each = p->matrices > 0 ? ceil_div(p->rows, p->matrices) : 0;
+  const int variant = each > 16 ? 2 : (each > 4 && n16 >= 1024 ? 1 : 0);
+  s->entry = spt::w4_entry(variant, p->dtype == GEMM_BF16, 128 / p->group, p->has_zeros != 0);
+  const int bm = 16 * s->entry.mt;
+  s->nblocks = ceil_div(n16, s->entry.nt);
+  s->row_blocks = grouped ? spt::max_row_blocks(p->rows, p->matrices, bm) : ceil_div(p->rows, bm);
+  if (s->row_blocks > 65535) return GEMM_ERR_UNSUPPORTED;
+  const int64_t wgs = s->nblocks * s->row_blocks;
+  // cut K when the workgroups alone would not occupy every compute unit
+  s->splits = 1;
+  if (wgs > 0 && wgs < cu) {
+    const int64_t most = kb / s->entry.waves;
+    s->splits = ceil_div(cu, wgs);
+    if (s->splits > most) s->splits = most;
+    if (s->splits < 1) s->splits = 1;
+  }
+  s->ws = s->splits > 1 ? s->splits * p->rows * p->n * 4 : 0;
+  return GEMM_OK;
+}
+
+int64_t w4_blocks(int64_t matrices, int64_t n, int64_t k) { return matrices * ceil_div(n, 16) * ceil_div(k, 128); }
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t experts_sort_workspace_bytes(int64_t slots, int64_t experts, int64_t* out) {
+  if (!out || slots < 0) return GEMM_ERR_INVALID;
+  if (experts < 1 || experts > kMaxExperts || slots > kMax32) return GEMM_ERR_UNSUPPORTED;
+  const SortShape s = sort_shape(slots);
+  *out = s.blocks > 1 ? s.blocks * (experts + 1) * 4 : 0;
+  return GEMM_OK;
+}
+
+gemm_status_t experts_sort(const void* ids, int id_bits, int64_t slots, int64_t experts, int32_t* offsets,
+                           int32_t* order, int32_t* rows, void* workspace, int64_t workspace_bytes, void* stream) {
+  int64_t need = 0;
+  gemm_status_t st = experts_sort_workspace_bytes(slots, experts, &need);
+  if (st != GEMM_OK) return st;
+  if ((id_bits != 32 && id_bits != 64) || !offsets || (slots > 0 && (!ids || !order || !rows)) ||
+      (need > 0 && (!workspace || workspace_bytes < need)))
+    return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  const SortShape s = sort_shape(slots);
+  spt::SortArgs a;
+  a.ids = ids;
+  a.id64 = id_bits == 64;
+  a.rows = (int)slots;
+  a.experts = (int)experts;
+  a.per_block = (int)s.per_block;
+  a.blocks = (int)s.blocks;
+  a.counts = (int*)workspace;
+  a.offsets = offsets;
+  a.slots = order;
+  a.rows_of = rows;
+  const int keys = (int)experts + 1;
+  if (s.blocks == 1) return launch(spt::sort_one_fn(), dim3(1), 1024, (17 * keys + 16) * 4, &a, stream);
+  st = launch(spt::sort_hist_fn(), dim3((unsigned)s.blocks), 1024, keys * 4, &a, stream);
+  if (st != GEMM_OK) return st;
+  return launch(spt::sort_place_fn(), dim3((unsigned)s.blocks), 1024, (18 * keys + 16) * 4, &a, stream);
+}
+
+gemm_status_t experts_gather(const void* x, gemm_dtype_t dtype, int64_t tokens, int64_t top_k, int64_t width,
+                             int64_t ldx, const int32_t* rows, const int32_t* kept, void* out, int64_t ldo,
+                             int zero_rest, void* stream) {
+  gemm_status_t st = check_route(dtype, tokens, top_k, width);
+  if (st != GEMM_OK) return st;
+  if (ldx < width || ldo < width) return GEMM_ERR_INVALID;
+  if (tokens == 0 || top_k == 0 || width == 0) return GEMM_OK;
+  if (!x || !rows || !kept || !out) return GEMM_ERR_INVALID;
+  spt::RouteArgs a{};
+  dim3 grid;
+  st = route_grid(tokens, width, &a.lanes_log2, &grid);
+  if (st != GEMM_OK) return st;
+  a.src = (const char*)x;
+  a.dst = (char*)out;
+  a.rows_of = rows;
+  a.kept = kept;
+  a.ld_src = ldx;
+  a.ld_dst = ldo;
+  a.tokens = (int)tokens;
+  a.top_k = (int)top_k;
+  a.width = (int)width;
+  a.zero_rest = zero_rest != 0;
+  return launch(spt::gather_fn((int)dtype), grid, 256, 0, &a, stream);
+}
+
+gemm_status_t experts_combine(const void* y, gemm_dtype_t dtype, int64_t tokens, int64_t top_k, int64_t width,
+                              int64_t ldy, const int32_t* rows, const int32_t* kept, const void* weights,
+                              gemm_dtype_t weight_dtype, void* out, int64_t ldo, void* stream) {
+  gemm_status_t st = check_route(dtype, tokens, top_k, width);
+  if (st != GEMM_OK) return st;
+  if (ldy < width || ldo < width || (weights && !is_dtype(weight_dtype))) return GEMM_ERR_INVALID;
+  if (tokens == 0 || width == 0) return GEMM_OK;
+  if (!out || !kept || (top_k > 0 && (!y || !rows))) return GEMM_ERR_INVALID;
+  spt::RouteArgs a{};
+  dim3 grid;
+  st = route_grid(tokens, width, &a.lanes_log2, &grid);
+  if (st != GEMM_OK) return st;
+  a.src = (const char*)y;
+  a.dst = (char*)out;
+  a.rows_of = rows;
+  a.kept = kept;
+  a.weights = weights;
+  a.ld_src = ldy;
+  a.ld_dst = ldo;
+  a.tokens = (int)tokens;
+  a.top_k = (int)top_k;
+  a.width = (int)width;
+  return launch(spt::combine_fn((int)dtype, weights ? (int)weight_dtype : 3), grid, 256, 0, &a, stream);
+}
+
+gemm_status_t experts_combine_grad(const void* dout, int64_t lddo, const void* y, gemm_dtype_t dtype, int64_t tokens,
+                                   int64_t top_k, int64_t width, int64_t ldy, const int32_t* rows,
+                                   const int32_t* kept, const void* weights, gemm_dtype_t weight_dtype, void* dy,
+                                   int64_t lddy, void* dweights, int zero_rest, void* stream) {
+  gemm_status_t st = check_route(dtype, tokens, top_k, width);
+  if (st != GEMM_OK) return st;
+  if (lddo < width || ldy < width || lddy < width || (weights && !is_dtype(weight_dtype))) return GEMM_ERR_INVALID;
+  if (tokens == 0 || top_k == 0) return GEMM_OK;
+  if (!rows || !kept || (width > 0 && (!dout || !y || !dy)) || (weights && !dweights)) return GEMM_ERR_INVALID;
+  if (tokens * 256 > kMax32) return GEMM_ERR_UNSUPPORTED;
+  spt::RouteArgs a{};
+  a.src = (const char*)y;
+  a.dout = (const char*)dout;
+  a.dst = (char*)dy;
+  a.rows_of = rows;
+  a.kept = kept;
+  a.weights = weights;
+  a.dweights = dweights;
+  a.ld_src = ldy;
+  a.ld_dst = lddy;
+  a.ld_dout = lddo;
+  a.tokens = (int)tokens;
+  a.top_k = (int)top_k;
+  a.width = (int)width;
+  a.zero_rest = zero_rest != 0;
+  return launch(spt::combine_grad_fn((int)dtype, weights ? (int)weight_dtype : 3), dim3((unsigned)tokens), 256, 0, &a,
+                stream);
+}
+
+gemm_status_t gemm_grouped_workspace_bytes(const gemm_grouped_t* p, const void* X, const void* Y, int64_t* out) {
+  GroupedShape s;
+  if (!out) return GEMM_ERR_INVALID;
+  const gemm_status_t st = grouped_shape(p, X, Y, &s);
+  if (st == GEMM_OK) *out = s.ws;
+  return st;
+}
+
+gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const void* Y, void* out,
+                               const int32_t* offsets, void* workspace, int64_t workspace_bytes, void* stream) {
+  GroupedShape s;
+  gemm_status_t st = grouped_shape(p, X, Y, &s);
+  if (st != GEMM_OK) return st;
+  const bool gb = p->mode == GEMM_GROUPED_GRAD_B, fwd = p->mode == GEMM_GROUPED_FORWARD;
+  const int64_t out_n = fwd ? p->n : p->k;
+  if (out_n == 0 || (gb ? p->experts == 0 || p->n == 0 : p->rows == 0)) return GEMM_OK;
+  if (!out || !offsets) return GEMM_ERR_INVALID;
+  // operands that hold at least one element have to be there
+  if ((s.x.rows > 0 && s.x.cols > 0 && !X) || (s.y.rows > 0 && s.y.cols > 0 && !Y)) return GEMM_ERR_INVALID;
+  if (s.ws > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < s.ws)) return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+
+  // few rows per expert: small row blocks, so that reading B is all there is to do
+  const int64_t each = p->experts > 0 ? ceil_div(p->rows, p->experts) : 0;
+  const int variant = !gb && each <= 32 ? 1 : 0;
+  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, variant, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
+  const int64_t tiles_m = ceil_div(p->n, entry.bm), tiles_n = ceil_div(out_n, entry.bn);
+  const int64_t units = gb ? p->experts * tiles_m * tiles_n
+                           : spt::max_row_blocks(p->rows, p->experts, entry.bm) * tiles_n;
+  const int64_t grid = units < (int64_t)cu * entry.per_cu ? units : (int64_t)cu * entry.per_cu;
+  if (units + grid > kMax32) return GEMM_ERR_UNSUPPORTED;
+
+  st = pad_operand(s.x, &X, (char*)workspace, stream);
+  if (st != GEMM_OK) return st;
+  st = pad_operand(s.y, &Y, (char*)workspace, stream);
+  if (st != GEMM_OK) return st;
+
+  spt::GroupedArgs a;
+  a.X = (const char*)X;
+  a.Y = (const char*)Y;
+  a.C = (char*)out;
+  a.offsets = offsets;
+  a.rows = (int)p->rows;
+  a.experts = (int)p->experts;
+  a.m = (int)p->n;
+  a.n = (int)out_n;
+  a.kc = (int)(fwd ? p->k : p->n);
+  a.ldx = s.x.ld;
+  a.ldy = s.y.ld;
+  a.ldc = p->ldo;
+  a.sy = s.y.stride;
+  a.sc = gb ? p->stride : 0;
+  a.tiles_m = (int)tiles_m;
+  a.tiles_n = (int)tiles_n;
+  a.group_m = 8;
+  a.grid = (int)grid;
+  a.rest = p->zero_rest != 0;
+  return launch(entry.fn, dim3((unsigned)grid), entry.threads, 0, &a, stream);
+}
+
+gemm_status_t gemm_w4_packed_bytes(int64_t matrices, int64_t n, int64_t k, int group, int has_zeros, int64_t* out) {
+  if (!out || matrices < 0 || n < 0 || k < 0) return GEMM_ERR_INVALID;
+  const int64_t lim = (int64_t)1 << 24;
+  if ((group != 32 && group != 64 && group != 128) || n > lim || k > lim || matrices > lim) return GEMM_ERR_UNSUPPORTED;
+  *out = w4_blocks(matrices, n, k) * (1024 + 16 * (128 / group) * (has_zeros ? 3 : 2));
+  return GEMM_OK;
+}
+
+gemm_status_t gemm_w4_pack(const uint8_t* q, const void* scales, const uint8_t* zeros, int64_t matrices, int64_t n,
+                           int64_t k, int group, void* packed, void* stream) {
+  int64_t bytes = 0;
+  gemm_status_t st = gemm_w4_packed_bytes(matrices, n, k, group, zeros != nullptr, &bytes);
+  if (st != GEMM_OK) return st;
+  if (bytes == 0) return GEMM_OK;
+  if (!q || !scales || !packed || (uintptr_t)packed % 16 != 0) return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  spt::W4PackArgs a;
+  a.q = q;
+  a.scales = (const unsigned short*)scales;
+  a.zeros = zeros;
+  a.packed = (char*)packed;
+  a.matrices = matrices;
+  a.n = (int)n;
+  a.k = (int)k;
+  a.group = group;
+  const int64_t blocks = w4_blocks(matrices, n, k);
+  st = launch(spt::w4_pack_fn(), dim3(stream_grid(blocks * 256)), 256, 0, &a, stream);
+  if (st != GEMM_OK) return st;
+  return launch(spt::w4_pack_groups_fn(), dim3(stream_grid(blocks * 16 * (128 / group))), 256, 0, &a, stream);
+}
+
+gemm_status_t gemm_w4_workspace_bytes(const gemm_w4_t* p, int has_offsets, int64_t* out) {
+  if (!out) return GEMM_ERR_INVALID;
+  W4Shape s;
+  int cu = 0;
+  gemm_status_t st = w4_shape(p, has_offsets != 0, 1, &s);  // the arguments first, on any host
+  if (st != GEMM_OK) return st;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  st = w4_shape(p, has_offsets != 0, cu, &s);
+  if (st == GEMM_OK) *out = s.ws;
+  return st;
+}
+
+gemm_status_t gemm_w4_run(const gemm_w4_t* p, const void* x, const void* packed, const int32_t* offsets, void* out,
+                          void* workspace, int64_t workspace_bytes, void* stream) {
+  W4Shape s;
+  int cu = 0;
+  gemm_status_t st = w4_shape(p, offsets != nullptr, 1, &s);
+  if (st != GEMM_OK) return st;
+  if (p->rows == 0 || p->n == 0) return GEMM_OK;
+  if (!out || (p->k > 0 && (!x || (p->matrices > 0 && (!packed || (uintptr_t)packed % 16 != 0))))) return GEMM_ERR_INVALID;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  st = w4_shape(p, offsets != nullptr, cu, &s);
+  if (st != GEMM_OK) return st;
+  if (s.ws > 0 && (!workspace || (uintptr_t)workspace % 4 != 0 || workspace_bytes < s.ws)) return GEMM_ERR_INVALID;
+  const int gpk = 128 / p->group;
+  const int64_t blocks = w4_blocks(p->matrices, p->n, p->k);
+  spt::W4Args a;
+  a.x = (const char*)x;
+  a.w = (const char*)packed;
+  a.scales = a.w + blocks * 1024;
+  a.zeros = a.scales + blocks * 16 * gpk * 2;
+  a.out = s.splits > 1 ? (char*)workspace : (char*)out;
+  a.offsets = offsets;
+  a.ldx = p->ldx;
+  a.ldo = p->ldo;
+  a.plane = p->rows * p->n;
+  a.rows = (int)p->rows;
+  a.experts = (int)p->matrices;
+  a.n = (int)p->n;
+  a.k = (int)p->k;
+  a.n16 = (int)ceil_div(p->n, 16);
+  a.kb = (int)ceil_div(p->k, 128);
+  a.splits = (int)s.splits;
+  a.rest = p->zero_rest != 0;
+  a.out_dtype = (int)p->out_dtype;
+  st = launch(s.entry.fn, dim3((unsigned)(s.nblocks * s.splits), (unsigned)s.row_blocks), 64 * s.entry.waves, 0, &a,
+              stream);
+  if (st != GEMM_OK || s.splits == 1) return st;
+  spt::W4ReduceArgs r;
+  r.parts = (const float*)workspace;
+  r.out = (char*)out;
+  r.kept = offsets ? offsets + p->matrices : nullptr;
+  r.ldo = p->ldo;
+  r.plane = a.plane;
+  r.rows = a.rows;
+  r.n = a.n;
+  r.splits = a.splits;
+  r.out_dtype = a.out_dtype;
+  r.rest = a.rest;
+  return launch(spt::w4_reduce_fn(), dim3(stream_grid(a.plane)), 256, 0, &r, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,268 @@
+// The experts' products over rows sorted by expert: C rows = A rows times their expert's B, and the
+// gradients of both operands, in one kernel by the side on which each operand is contiguous.
+//
+//   D[i][j] = sum over c of X[i][c] * Y[j][c]
+//   forward   X = A, Y = B[e]: both contiguous in c
+//   grad A    X = dC (contiguous in c), Y[j][c] = B[e][c][j]: contiguous in j
+//   grad B    X[i][c] = dC[c][i], Y[j][c] = A[c][j], c over the expert's rows: contiguous in i and j
+//
+// An operand that is contiguous in c is staged and read as in the dense kernels: rows of 64 c
+// (128 bytes), chunk XOR (row mod 8), one ds_read_b128 per 16 x 32 fragment. One that is contiguous
+// in i or j is staged as it lies, 64 rows of c by BM or BN columns, and turned on the way from LDS to
+// registers: ds_read_b64_tr_b16 hands each lane four c of one column (16 lanes read a 4 x 16 block),
+// two of them make a fragment, so no transposed copy of B, A or dC is written to memory. Rows past an
+// expert's last lie past its descriptor's end and read as zeros, so ragged experts need no padding in
+// grad B's sum.
+//
+// A persistent grid walks the output tiles of all experts; each unit looks its expert up from the
+// offsets (find_group), since the host does not know the counts. K-tiles of 64 stream through a ring
+// of S LDS stages by direct global->LDS loads; one barrier per K-tile.
+#include "spt_device.h"
+#include "spt_experts.h"
+
+namespace spt {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4_t;
+
+// Four c of one column per lane: lane p of each 16 supplies the address of columns 4 (p % 4) .. +3 of
+// row p / 4 and receives column p, rows 0 .. 3.
+__device__ __forceinline__ uint64_t read_tr16(const char* p) {
+  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(const lds_void_t*)p));
+}
+
+// A tile of 64 c rows x R columns: row c holds R / 8 chunks of 16 bytes, logical chunk q at physical
+// chunk q XOR tr_swz(c). A transposing read touches 64 bytes of each of four neighbouring rows; the XOR
+// moves them to the four 64-byte quarters of the 64 banks.
+template <int R>
+__device__ __forceinline__ int tr_swz(int c) {
+  return R >= 128 ? (c & 3) << 2 : (R == 64 ? ((c >> 1) & 1) << 2 : 0);
+}
+
+// MODE: kGroupedForward .. ; a WM x WN grid of waves; S stages; MINW: workgroups per CU to fit.
+template <int MODE, int BM, int BN, int WM, int WN, int S, int PER_CU, typename TIn, int OUT>
+__global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_kernel(GroupedArgs a) {
+  constexpr bool TX = MODE == kGroupedGradB, TY = MODE != kGroupedForward;
+  constexpr int W = WM * WN, BK = 64;
+  constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
+  constexpr int XB = BM * BK * 2, YB = BN * BK * 2, STAGE = XB + YB;
+  constexpr int LX = XB / 1024 / W, LY = YB / 1024 / W, LW = LX + LY;
+  static_assert(XB % (1024 * W) == 0 && YB % (1024 * W) == 0, "every wave issues the same number of loads");
+  static_assert(FM >= 1 && FN % 2 == 0 && S >= 2 && S * STAGE * PER_CU <= 160 * 1024, "tile");
+  static_assert((S - 2) * LW < 64, "vmcnt is a 6-bit counter");
+  __shared__ __attribute__((aligned(1024))) char smem[S * STAGE];
+  const unsigned lds0 = lds_addr(smem);
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int p = lane & 15, h = lane >> 4;
+  const int ldx = (int)a.ldx, ldy = (int)a.ldy, ldc = (int)a.ldc;
+  constexpr int es = OUT == 2 ? 4 : 2;
+
+  // load j of this wave: a lane's place in the operand tile. Contiguous in c: row and chunk of 8 c.
+  // Contiguous in i or j: row c and chunk of 8 columns.
+  const int n_kc = 8 * ((lane & 7) ^ swz(lane >> 3));
+  auto x_off = [&](int j) SPT_INLINE {
+    const int q = wave * LX + j;
+    if constexpr (!TX) return (unsigned)((8 * q + (lane >> 3)) * ldx + n_kc) * 2u;
+    else {
+      const int c = q * (512 / BM) + lane / (BM / 8), ch = (lane % (BM / 8)) ^ tr_swz<BM>(c);
+      return (unsigned)(c * ldx + 8 * ch) * 2u;
+    }
+  };
+  auto y_off = [&](int j) SPT_INLINE {
+    const int q = wave * LY + j;
+    if constexpr (!TY) return (unsigned)(b_row_perm(8 * q + (lane >> 3)) * ldy + n_kc) * 2u;
+    else {
+      const int c = q * (512 / BN) + lane / (BN / 8), ch = (lane % (BN / 8)) ^ tr_swz<BN>(c);
+      return (unsigned)(c * ldy + 8 * ch) * 2u;
+    }
+  };
+
+  // fragment f of k-step s. Columns of Y go to a fragment in the order of b_row_perm, so that a lane
+  // ends up with 8 consecutive output columns per fragment pair.
+  auto read_x = [&](const char* t, int s, int f) SPT_INLINE -> u32x4 {
+    if constexpr (!TX) {
+      return *(const u32x4*)(t + lds_chunk_offset(BM, wm * TM + 16 * f + p, 4 * s + h));
+    } else {
+      const int col = wm * TM + 16 * f + 4 * (p & 3);
+      uint64_t r[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = 32 * s + 8 * h + 4 * u + (p >> 2);
+        r[u] = read_tr16(t + c * (2 * BM) + (((col >> 3) ^ tr_swz<BM>(c)) << 4) + (col & 7) * 2);
+      }
+      return u32x4{(unsigned)r[0], (unsigned)(r[0] >> 32), (unsigned)r[1], (unsigned)(r[1] >> 32)};
+    }
+  };
+  auto read_y = [&](const char* t, int s, int f) SPT_INLINE -> u32x4 {
+    if constexpr (!TY) {
+      return *(const u32x4*)(t + lds_chunk_offset(BN, wn * TN + 16 * f + p, 4 * s + h));
+    } else {
+      const int col = wn * TN + 32 * (f >> 1) + 8 * (p & 3) + 4 * (f & 1);
+      uint64_t r[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = 32 * s + 8 * h + 4 * u + (p >> 2);
+        r[u] = read_tr16(t + c * (2 * BN) + (((col >> 3) ^ tr_swz<BN>(c)) << 4) + (col & 7) * 2);
+      }
+      return u32x4{(unsigned)r[0], (unsigned)(r[0] >> 32), (unsigned)r[1], (unsigned)(r[1] >> 32)};
+    }
+  };
+
+  for (int t = xcd_remap(blockIdx.x, a.grid);; t += a.grid) {
+    // this unit: output tile (row0, col0), its row and column counts, and the sum's length
+    int e, row0, rows_left, tm, tn, kc, c0 = 0;
+    if constexpr (MODE == kGroupedGradB) {
+      const int per = a.tiles_m * a.tiles_n;
+      e = t / per;
+      if (e >= a.experts) break;
+      grouped_raster(t - e * per, a.tiles_m, a.tiles_n, a.group_m, tm, tn);
+      row0 = tm * BM;
+      rows_left = a.m - row0;
+      c0 = clampi(a.offsets[e], 0, a.rows);
+      kc = clampi(a.offsets[e + 1], c0, a.rows) - c0;
+      c0 = __builtin_amdgcn_readfirstlane(c0);
+      kc = __builtin_amdgcn_readfirstlane(kc);
+    } else {
+      const GroupBlock g = find_group(a.offsets, a.experts, a.rows, BM, a.tiles_n, a.rest != 0, t);
+      if (g.e < 0) break;
+      e = g.e;
+      grouped_raster(g.local, g.blocks, a.tiles_n, a.group_m, tm, tn);
+      row0 = g.begin + tm * BM;
+      rows_left = g.end - row0;
+      kc = e == a.experts ? 0 : a.kc;  // behind the last expert: zeros
+    }
+    const int col0 = tn * BN, cols_left = a.n - col0;
+    const char* xb = a.X + (MODE == kGroupedGradB ? ((int64_t)c0 * a.ldx + row0) * 2 : (int64_t)row0 * a.ldx * 2);
+    const char* yb = a.Y + (MODE == kGroupedGradB ? ((int64_t)c0 * a.ldy + col0) * 2
+                            : MODE == kGroupedGradA ? ((int64_t)e * a.sy + col0) * 2
+                                                    : ((int64_t)e * a.sy + (int64_t)col0 * a.ldy) * 2);
+    auto issue = [&](int kt) SPT_INLINE {
+      const int k0 = kt * BK;
+      const unsigned dst = lds0 + (unsigned)(kt % S) * STAGE;
+      // K-tiles past the end read nothing and fill zeros, so every K-tile issues LW loads
+      auto rsrc = [&](bool tr, const char* base, int64_t ld, int rows, int width) SPT_INLINE {
+        const int64_t left = tr ? kc - k0 : rows;  // memory rows that may be read
+        // (memory rows hold a multiple of 8 elements, zeros past the operand's own; a chunk that the
+        // descriptor's end cut would read zeros as a whole)
+        const int64_t bytes = kc - k0 > 0 ? ((left - 1) * ld + (((tr ? width : kc) + 7) & ~7)) * 2 : 0;
+        return make_rsrc(base + (tr ? (int64_t)k0 * ld * 2 : 0), (uint64_t)(bytes > 0 ? bytes : 0));
+      };
+      const __amdgpu_buffer_rsrc_t rx = rsrc(TX, xb, a.ldx, rows_left, rows_left);
+      const __amdgpu_buffer_rsrc_t ry = rsrc(TY, yb, a.ldy, cols_left, cols_left);
+#pragma unroll
+      for (int j = 0; j < LX; ++j) {
+        const unsigned v = x_off(j);
+        dma16_unseen(rx, dst + (wave * LX + j) * 1024, TX || n_kc < kc - k0 ? v : kOOB, TX ? 0u : 2u * k0);
+      }
+#pragma unroll
+      for (int j = 0; j < LY; ++j) {
+        const unsigned v = y_off(j);
+        dma16_unseen(ry, dst + XB + (wave * LY + j) * 1024, TY || n_kc < kc - k0 ? v : kOOB, TY ? 0u : 2u * k0);
+      }
+    };
+
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int kt = (kc + BK - 1) / BK;
+    wait_vmcnt<0>();  // the previous unit's loads past its end, and its stores
+    barrier_sync();   // ... and everybody's reads of the ring
+    if (kt > 0) {
+#pragma unroll
+      for (int s = 0; s < S - 1; ++s) issue(s);
+      for (int k = 0; k < kt; ++k) {
+        wait_vmcnt<(S - 2) * LW>();  // K-tile k has landed: only later ones in flight
+        barrier_sync();              // for every wave; and K-tile k - 1 has been read by all
+        issue(k + S - 1);
+        const char* xt = smem + (k % S) * STAGE;
+        const char* yt = xt + XB;
+#pragma unroll
+        for (int s = 0; s < BK / 32; ++s) {
+          u32x4 xf[FM], yf[FN];
+#pragma unroll
+          for (int f = 0; f < FN; ++f) yf[f] = read_y(yt, s, f);
+#pragma unroll
+          for (int f = 0; f < FM; ++f) xf[f] = read_x(xt, s, f);
+#pragma unroll
+          for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) acc[i][j] = mfma16<TIn>(yf[i], xf[j], acc[i][j]);
+        }
+      }
+    }
+
+    const __amdgpu_buffer_rsrc_t rc = make_rsrc(
+        a.C + ((MODE == kGroupedGradB ? (int64_t)e * a.sc : 0) + (int64_t)row0 * a.ldc) * es,
+        ((uint64_t)(rows_left - 1) * a.ldc + a.n) * es);
+#pragma unroll
+    for (int pu = 0; pu < FN / 2; ++pu) {
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[q] = acc[2 * pu][j][q];
+          v[4 + q] = acc[2 * pu + 1][j][q];
+        }
+        const int m = wm * TM + 16 * j + p, n = col0 + wn * TN + 32 * pu + 8 * h;
+        if (rows_left >= BM && cols_left >= BN) store8<OUT, false>(v, rc, m, rows_left, n, a.n, ldc);
+        else store8<OUT, true>(v, rc, m, rows_left, n, a.n, ldc);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  wait_vmcnt<0>();  // no load may still be on its way to LDS when the workgroup ends
+}
+
+// ------------------------------------------------------------------------------ padding
+// Operands whose rows are not 16-byte aligned multiples of 8 elements are copied to rows that are,
+// the padding columns zero: the direct loads move whole 16-byte chunks.
+__global__ void __launch_bounds__(256) pad_rows_kernel(PadArgs a) {
+  typedef unsigned u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+  const int cpr = a.cols_pad / 8;
+  const int64_t total = a.rows * cpr;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / cpr;
+    const int col = (int)(i - r * cpr) * 8;
+    const char* s = a.src + ((r / a.rows_per) * a.stride + (r % a.rows_per) * a.ld + col) * 2;
+    u32x4 v = {0, 0, 0, 0};
+    if (col + 8 <= a.cols) {
+      v = *(const u32x4u*)s;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e < a.cols) v[e >> 1] |= (unsigned)((const unsigned short*)s)[e] << (16 * (e & 1));
+    }
+    *(u32x4*)(a.dst + i * 16) = v;
+  }
+}
+const void* pad_rows_fn() { return (const void*)&pad_rows_kernel; }
+
+// ------------------------------------------------------------------------------ instantiations
+template <int MODE, int BM, int BN, int WM, int WN, int S, int PER_CU>
+static GroupedEntry grouped_pick(int bf16, int out) {
+  GroupedEntry e{nullptr, BM, BN, 64 * WM * WN, PER_CU};
+#define SPT_GROUPED(TI, O) (const void*)&grouped_kernel<MODE, BM, BN, WM, WN, S, PER_CU, TI, O>
+  static const void* const fn[2][3] = {{SPT_GROUPED(_Float16, 0), SPT_GROUPED(_Float16, 1), SPT_GROUPED(_Float16, 2)},
+                                       {SPT_GROUPED(__bf16, 0), SPT_GROUPED(__bf16, 1), SPT_GROUPED(__bf16, 2)}};
+#undef SPT_GROUPED
+  e.fn = fn[bf16][out];
+  return e;
+}
+GroupedEntry grouped_entry(int mode, int variant, int bf16, int out) {
+  if (mode == kGroupedForward)
+    return variant == 0 ? grouped_pick<kGroupedForward, 128, 128, 2, 2, 2, 2>(bf16, out)
+                        : grouped_pick<kGroupedForward, 32, 64, 2, 2, 4, 3>(bf16, out);
+  if (mode == kGroupedGradA)
+    return variant == 0 ? grouped_pick<kGroupedGradA, 128, 128, 2, 2, 2, 2>(bf16, out)
+                        : grouped_pick<kGroupedGradA, 32, 64, 2, 2, 4, 3>(bf16, out);
+  return grouped_pick<kGroupedGradB, 128, 128, 2, 2, 2, 2>(bf16, out);
+}
+
+}  // namespace spt

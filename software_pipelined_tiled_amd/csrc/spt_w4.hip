@@ -1,0 +1,318 @@
+// Products with 4-bit weights and group scales:
+//   y[i][n] = sum over k of x[i][k] * (q[n][k] - z[n][k / G]) * s[n][k / G]
+// for one weight matrix, or one per expert over rows sorted by expert. q and z are 0 .. 15 (z = 8
+// where there are none), s and x 16-bit, G = 32, 64 or 128.
+//
+// Arithmetic. q - z is a whole number of at most four bits and a sign: it is exact in fp16 and in
+// bf16. So the matrix instruction takes x and q - z, every product is exact, and the sum over one
+// group stays in its fp32 accumulator; the group's scale multiplies that sum in fp32. No weight is
+// rounded, a column whose weights all equal their zero point gives exact zeros, and infinities and
+// NaN in x travel as in the formula (a group's sum of x times q - z has to stay inside fp32's range).
+//
+// What bounds it: with few rows, reading the weights (half a byte each). The packed layout gives
+// each lane 16 consecutive bytes of the stream, which are the weights of four matrix instructions
+// (32 k each) in the lane's own operand position, so a wave reads 1 KiB (16 columns x 128 k) per
+// load and nothing passes through LDS. Turning four bits into an operand costs 9 (fp16) or 17 (bf16)
+// vector instructions per 8 weights and lane; at the rate HBM delivers weights that is about a third
+// (two thirds) of the vector issue slots.
+//
+// Work split. A workgroup owns 16 * NT columns and 16 * MT rows; its waves take the 128-deep blocks
+// of K in turn and add their sums through LDS in wave order. When that leaves compute units
+// without work, K is cut over workgroups too, into fp32 planes that a second kernel adds in order.
+#include "spt_device.h"
+#include "spt_experts.h"
+
+namespace spt {
+
+// ------------------------------------------------------------------------------ layout
+// Packed words: [matrix][n/16][k/128][lane][4]. Word s of lane l holds the weights of column l % 16,
+// k = 32 s + 8 (l / 16) + 0 .. 7 of the block, element 2p in bits 4p and element 2p + 1 in bits
+// 16 + 4p, so that one mask takes a pair to the two halves of a register. Behind them the scales
+// [matrix][n/16][k/128][16][128 / G], then the zero points in the same order, a byte each.
+// Columns past N and k past K hold weight 0 with scale 0.
+__global__ void __launch_bounds__(256) w4_pack_kernel(W4PackArgs a) {
+  const int n16 = (a.n + 15) / 16, kb = (a.k + 127) / 128;
+  const int64_t words = a.matrices * n16 * kb * 256;
+  unsigned* out = (unsigned*)a.packed;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words; i += (int64_t)gridDim.x * 256) {
+    const int s = (int)(i & 3), lane = (int)(i >> 2) & 63;
+    const int64_t blk = i >> 8;
+    const int b = (int)(blk % kb);
+    const int64_t col = blk / kb;  // matrix * n16 + column block
+    const int n = (int)(col % n16) * 16 + (lane & 15), k0 = b * 128 + s * 32 + 8 * (lane >> 4);
+    const unsigned char* q = a.q + ((col / n16) * a.n + n) * (int64_t)a.k + k0;
+    unsigned w = 0;
+    if (n < a.n) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const unsigned v = k0 + e < a.k ? q[e] & 15u : 0u;
+        w |= v << (4 * (e >> 1) + 16 * (e & 1));
+      }
+    }
+    out[i] = w;
+  }
+}
+
+__global__ void __launch_bounds__(256) w4_pack_groups_kernel(W4PackArgs a) {
+  const int n16 = (a.n + 15) / 16, kb = (a.k + 127) / 128, gpk = 128 / a.group, groups = (a.k + a.group - 1) / a.group;
+  const int64_t blocks = a.matrices * n16 * kb, total = blocks * 16 * gpk;
+  unsigned short* sc = (unsigned short*)(a.packed + blocks * 1024);
+  unsigned char* zp = (unsigned char*)(sc + total);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int g = (int)(i % gpk), c = (int)(i / gpk) & 15;
+    const int64_t blk = i / (16 * gpk);
+    const int64_t col = blk / kb;
+    const int n = (int)(col % n16) * 16 + c, gr = (int)(blk % kb) * gpk + g;
+    const bool in = n < a.n && gr < groups;
+    const int64_t at = ((col / n16) * a.n + n) * (int64_t)groups + gr;
+    sc[i] = in ? a.scales[at] : (unsigned short)0;
+    if (a.zeros) zp[i] = in ? a.zeros[at] & 15 : 0;
+  }
+}
+
+// ------------------------------------------------------------------------------ four bits to operands
+// Eight weights minus their zero point as a matrix operand. A nibble placed in the low bits of the
+// fp16 pattern of 1024 (or, shifted by four, of 64) reads 1024 + q (64 + q): two pairs come out of a
+// word by a mask alone, two more after one shift.
+struct ZeroF16 {
+  unsigned c0, c1;  // -(1024 + z), -(64 + z) in both halves
+};
+struct ZeroF32 {
+  float c0, c1;
+};
+__device__ __forceinline__ unsigned and_or(unsigned v, unsigned m, unsigned o) { return (v & m) | o; }
+__device__ __forceinline__ unsigned add_f16x2(unsigned a, unsigned b) {
+  return __builtin_bit_cast(unsigned, __builtin_bit_cast(f16x2, a) + __builtin_bit_cast(f16x2, b));
+}
+__device__ __forceinline__ u32x4 unpack(unsigned w, const ZeroF16& z) {
+  u32x4 r;
+  const unsigned v = w >> 8;
+  r[0] = add_f16x2(and_or(w, 0x000F000Fu, 0x64006400u), z.c0);
+  r[1] = add_f16x2(and_or(w, 0x00F000F0u, 0x54005400u), z.c1);
+  r[2] = add_f16x2(and_or(v, 0x000F000Fu, 0x64006400u), z.c0);
+  r[3] = add_f16x2(and_or(v, 0x00F000F0u, 0x54005400u), z.c1);
+  return r;
+}
+// bf16 has no packed arithmetic: each half of the fp16 pair goes through one mixed-precision
+// multiply-add (half * 1 + c, exact) into fp32, whose upper 16 bits are the bf16 value, exact too.
+__device__ __forceinline__ unsigned minus_bf16(unsigned pair, float c) {
+  float lo, hi;
+  asm("v_fma_mix_f32 %0, %1, 1.0, %2 op_sel_hi:[1,0,0]" : "=v"(lo) : "v"(pair), "v"(c));
+  asm("v_fma_mix_f32 %0, %1, 1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(hi) : "v"(pair), "v"(c));
+  return __builtin_amdgcn_perm(__builtin_bit_cast(unsigned, hi), __builtin_bit_cast(unsigned, lo), 0x07060302u);
+}
+__device__ __forceinline__ u32x4 unpack(unsigned w, const ZeroF32& z) {
+  u32x4 r;
+  const unsigned v = w >> 8;
+  r[0] = minus_bf16(and_or(w, 0x000F000Fu, 0x64006400u), z.c0);
+  r[1] = minus_bf16(and_or(w, 0x00F000F0u, 0x54005400u), z.c1);
+  r[2] = minus_bf16(and_or(v, 0x000F000Fu, 0x64006400u), z.c0);
+  r[3] = minus_bf16(and_or(v, 0x00F000F0u, 0x54005400u), z.c1);
+  return r;
+}
+
+template <int T>
+__device__ __forceinline__ float scale_of(unsigned s) {
+  if constexpr (T == 1) return __builtin_bit_cast(float, s << 16);
+  else return (float)__builtin_bit_cast(_Float16, (unsigned short)s);
+}
+
+// out: 0 fp16, 1 bf16, 2 fp32 (the same for a whole launch)
+__device__ __forceinline__ void put_one(int out, char* p, int64_t i, float v) {
+  if (out == 2) ((float*)p)[i] = v;
+  else ((unsigned short*)p)[i] = (unsigned short)(out == 1 ? pack_bf16(v, 0.f) : pack_f16(v, 0.f));
+}
+
+// ------------------------------------------------------------------------------ the product
+// T: 0 fp16, 1 bf16 (x and scales). MT, NT: 16-row and 16-column blocks. GPK: groups per 128 k.
+// W waves. D: 128-deep blocks of weights in flight per wave.
+template <int T, int MT, int NT, int GPK, bool ZERO, int W, int D>
+__global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
+  using TIn = std::conditional_t<T == 1, __bf16, _Float16>;
+  using GroupBits = std::conditional_t<GPK == 4, uint64_t, std::conditional_t<GPK == 2, unsigned, unsigned short>>;
+  using ZeroBits = std::conditional_t<GPK == 4, unsigned, std::conditional_t<GPK == 2, unsigned short, unsigned char>>;
+  constexpr int BM = 16 * MT;
+  __shared__ float red[W][MT * NT][256];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, h = lane >> 4;
+  const int nblocks = (a.n16 + NT - 1) / NT;
+  const int nb = (int)(blockIdx.x % (unsigned)nblocks) * NT, split = (int)(blockIdx.x / (unsigned)nblocks);
+
+  int e = 0, row0 = (int)blockIdx.y * BM, rows = a.rows - row0;
+  if (a.offsets) {
+    const GroupBlock g = find_group(a.offsets, a.experts, a.rows, BM, 1, a.rest != 0, (int)blockIdx.y);
+    if (g.e < 0) return;
+    e = g.e;
+    row0 = g.begin + g.block * BM;
+    rows = g.end - row0;
+  }
+  rows = rows < BM ? rows : BM;
+  const int per = (a.kb + a.splits - 1) / a.splits;
+  const int kb0 = split * per, kb1 = e == a.experts && a.offsets ? kb0 : (kb0 + per < a.kb ? kb0 + per : a.kb);
+
+  const __amdgpu_buffer_rsrc_t rx =
+      make_rsrc(a.x + (int64_t)row0 * a.ldx * 2, ((uint64_t)(rows - 1) * a.ldx + a.k) * 2);
+  unsigned xo[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xo[i] = 16 * i + c < rows ? (unsigned)((16 * i + c) * (int)a.ldx + 8 * h) * 2u : kOOB;
+
+  const int64_t block0 = ((int64_t)e * a.n16 + nb) * a.kb;
+  const char* wp = a.w + block0 * 1024 + lane * 16;
+  const char* sp = a.scales + block0 * (16 * GPK * 2) + c * (GPK * 2);
+  const char* zp = a.zeros + block0 * (16 * GPK) + c * GPK;
+  // the workgroup's last columns may have fewer than NT blocks: the missing ones repeat the last
+  int nstep[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) nstep[j] = (nb + j < a.n16 ? j : a.n16 - 1 - nb) * a.kb;
+
+  struct Stage {
+    u32x4 q[NT];
+    GroupBits s[NT];
+    ZeroBits z[NT];
+  };
+  auto fetch = [&](Stage& st, int kb) SPT_INLINE {
+    kb = kb < kb1 ? kb : kb1 - 1;  // past the end: a block already read, not used
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int64_t b = nstep[j] + kb;
+      st.q[j] = __builtin_nontemporal_load((const u32x4*)(wp + b * 1024));
+      st.s[j] = *(const GroupBits*)(sp + b * (16 * GPK * 2));
+      if constexpr (ZERO) st.z[j] = *(const ZeroBits*)(zp + b * (16 * GPK));
+    }
+  };
+  // x of 16-row block i, matrix step s of block kb
+  auto load_x = [&](int kb, int s, int i) SPT_INLINE -> u32x4 {
+    const int k0 = kb * 128 + s * 32;
+    if (kb * 128 + 128 <= a.k) return __builtin_amdgcn_raw_buffer_load_b128(rx, xo[i], 2 * k0, 0);
+    const int left = a.k - k0 - 8 * h;  // elements of the lane's chunk that exist
+    u32x4 r = {0, 0, 0, 0};
+    if (left >= 8) {
+      r = __builtin_amdgcn_raw_buffer_load_b128(rx, xo[i], 2 * k0, 0);
+    } else {
+#pragma unroll
+      for (int m = 0; m < 7; ++m)
+        if (m < left)
+          r[m >> 1] |= (unsigned)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rx, xo[i] + 2 * m, 2 * k0, 0)
+                       << (16 * (m & 1));
+    }
+    return r;
+  };
+
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](const Stage& st, int kb) SPT_INLINE {
+    u32x4 xf[4][MT];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) xf[s][i] = load_x(kb, s, i);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int g = 0; g < GPK; ++g) {
+        const unsigned zz = ZERO ? (unsigned)(st.z[j] >> (8 * g)) & 0xFFu : 8u;
+        std::conditional_t<T == 1, ZeroF32, ZeroF16> z;
+        if constexpr (T == 1) {
+          const float f = (float)zz;
+          z = ZeroF32{-1024.f - f, -64.f - f};
+        } else {
+          const unsigned p = zz | zz << 16;
+          z = ZeroF16{0xE400E400u + p, 0xD400D400u + (p << 4)};
+        }
+        f32x4 sum[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = g * (4 / GPK); s < (g + 1) * (4 / GPK); ++s) {
+          const u32x4 wf = unpack(st.q[j][s], z);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) sum[i] = mfma16<TIn>(xf[s][i], wf, sum[i]);
+        }
+        const float sc = scale_of<T>((unsigned)(st.s[j] >> (16 * g)) & 0xFFFFu);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(sum[i][r], sc, acc[i][j][r]);
+      }
+    }
+  };
+
+  if (kb0 + wave < kb1) {
+    Stage st[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(st[d], kb0 + wave + d * W);
+    for (int kb = kb0 + wave; kb < kb1; kb += D * W) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (kb + d * W < kb1) {
+          compute(st[d], kb + d * W);
+          fetch(st[d], kb + (d + D) * W);
+        }
+      }
+    }
+  }
+
+  // the waves' sums, added in wave order
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *(f32x4*)&red[wave][i * NT + j][4 * lane] = acc[i][j];
+  __syncthreads();
+  // consecutive threads take consecutive columns
+  for (int t = threadIdx.x; t < MT * NT * 256; t += 64 * W) {
+    const int n_in = t % (16 * NT), m = t / (16 * NT);
+    const int j = n_in >> 4, i = m >> 4, src = 4 * ((n_in & 15) + 16 * ((m & 15) >> 2)) + (m & 3);
+    const int n = nb * 16 + n_in;
+    if (m >= rows || n >= a.n) continue;
+    float v = red[0][i * NT + j][src];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += red[w][i * NT + j][src];
+    if (a.splits > 1) ((float*)a.out)[split * a.plane + (int64_t)(row0 + m) * a.n + n] = v;
+    else put_one(a.out_dtype, a.out, (int64_t)(row0 + m) * a.ldo + n, v);
+  }
+}
+
+// out = the planes added in order, rounded once. With `kept`, rows from *kept on hold zeros or are
+// left alone.
+__global__ void __launch_bounds__(256) w4_reduce_kernel(W4ReduceArgs r) {
+  const int kept = r.kept && !r.rest ? clampi(*r.kept, 0, r.rows) : r.rows;
+  const int64_t total = (int64_t)kept * r.n;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    float v = r.parts[i];
+    for (int s = 1; s < r.splits; ++s) v += r.parts[s * r.plane + i];
+    const int64_t row = i / r.n;
+    put_one(r.out_dtype, r.out, row * r.ldo + (i - row * r.n), v);
+  }
+}
+
+// ------------------------------------------------------------------------------ instantiations
+template <int T, int MT, int NT, int W, int D>
+static W4Entry w4_pick_group(int gpk, bool zero) {
+  W4Entry e{nullptr, MT, NT, W};
+  if (gpk == 1) e.fn = zero ? (const void*)&w4_kernel<T, MT, NT, 1, true, W, D> : (const void*)&w4_kernel<T, MT, NT, 1, false, W, D>;
+  else if (gpk == 2) e.fn = zero ? (const void*)&w4_kernel<T, MT, NT, 2, true, W, D> : (const void*)&w4_kernel<T, MT, NT, 2, false, W, D>;
+  else e.fn = zero ? (const void*)&w4_kernel<T, MT, NT, 4, true, W, D> : (const void*)&w4_kernel<T, MT, NT, 4, false, W, D>;
+  return e;
+}
+template <int T>
+static W4Entry w4_pick(int variant, int gpk, bool zero) {
+  switch (variant) {
+    case 0: return w4_pick_group<T, 1, 1, 8, 4>(gpk, zero);
+    case 1: return w4_pick_group<T, 1, 2, 8, 4>(gpk, zero);
+    default: return w4_pick_group<T, 4, 4, 4, 2>(gpk, zero);
+  }
+}
+W4Entry w4_entry(int variant, int bf16, int gpk, bool zero) {
+  return bf16 ? w4_pick<1>(variant, gpk, zero) : w4_pick<0>(variant, gpk, zero);
+}
+const void* w4_pack_fn() { return (const void*)&w4_pack_kernel; }
+const void* w4_pack_groups_fn() { return (const void*)&w4_pack_groups_kernel; }
+const void* w4_reduce_fn() { return (const void*)&w4_reduce_kernel; }
+
+}  // namespace spt
