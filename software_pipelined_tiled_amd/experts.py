@@ -21,44 +21,70 @@ from . import _lib
 from .torch_api import dtype_code
 
 _16BIT = (torch.float16, torch.bfloat16)
+_FLOATS = (*_16BIT, torch.float32)
+_SORT_ONE = 8192  # slots that one workgroup sorts without a workspace
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 # ------------------------------------------------------------------------------------ arguments
+# These calls are a few microseconds of GPU work in a decoding loop: the checks cost what they have to,
+# messages are put together only for a refusal, and the device is switched only where it is another.
 
 def _need(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
 
 
-def _on_device(device: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None:
-            _need(t.is_cuda, f"{name} must be a device tensor")
-            _need(t.device == device, f"{name} is on {t.device}, the other operands on {device}")
+def _on_device(names: str, first: torch.Tensor, *others) -> None:
+    """Device tensors, all on the first one's device (None: an operand that is not there)."""
+    device = first.device
+    if first.is_cuda:
+        for t in others:
+            if t is not None and t.device != device:
+                break
+        else:
+            return
+    for name, t in zip(names.split(), (first, *others)):
+        if t is not None and not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other operands on {device}")
 
 
 def _matrix(name: str, t: torch.Tensor, rows: int | None = None, cols: int | None = None) -> int:
     """Checks a 2-d operand and returns its row stride."""
-    _need(t.dim() == 2, f"{name} must have two dimensions")
-    _need(rows is None or t.shape[0] == rows, f"{name} must have {rows} rows, has {t.shape[0]}")
-    _need(cols is None or t.shape[1] == cols, f"{name} must have {cols} columns, has {t.shape[1]}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
     r, c = t.shape
-    _need(c <= 1 or t.stride(1) == 1, f"{name} must have unit column stride")
+    if rows is not None and r != rows:
+        raise ValueError(f"{name} must have {rows} rows, has {r}")
+    if cols is not None and c != cols:
+        raise ValueError(f"{name} must have {cols} columns, has {c}")
+    if c > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
     if r <= 1:
         return c
-    _need(t.stride(0) >= c, f"{name} must be row-major with rows that do not overlap")
-    return t.stride(0)
+    ld = t.stride(0)
+    if ld < c:
+        raise ValueError(f"{name} must be row-major with rows that do not overlap")
+    return ld
 
 
-def _stack(name: str, t: torch.Tensor) -> tuple[int, int]:
-    """Checks a [experts, n, k] operand and returns its row and expert strides."""
-    _need(t.dim() == 3, f"{name} must have three dimensions [experts, n, k]")
+def _stack(name: str, t: torch.Tensor) -> tuple[int, int, int, int, int]:
+    """Checks a [experts, n, k] operand and returns its sizes, row stride and expert stride."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions [experts, n, k]")
     e, n, k = t.shape
-    _need(k <= 1 or t.stride(2) == 1, f"{name} must have unit stride in its last dimension")
-    _need(n <= 1 or t.stride(1) >= k, f"{name}'s rows must not overlap")
+    if k > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
     ld = t.stride(1) if n > 1 else k
-    _need(e <= 1 or n == 0 or t.stride(0) >= (n - 1) * ld + k, f"{name}'s matrices must not overlap")
-    return ld, t.stride(0) if e > 1 else n * ld
+    if ld < k:
+        raise ValueError(f"{name}'s rows must not overlap")
+    stride = t.stride(0) if e > 1 else n * ld
+    if n > 0 and stride < (n - 1) * ld + k:
+        raise ValueError(f"{name}'s matrices must not overlap")
+    return e, n, k, ld, stride
 
 
 def _rows_apart(t: torch.Tensor) -> torch.Tensor:
@@ -69,8 +95,9 @@ def _rows_apart(t: torch.Tensor) -> torch.Tensor:
 
 
 def _offsets(offsets: torch.Tensor, experts: int) -> None:
-    _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous()
-          and offsets.shape[0] == experts + 1, f"offsets must be {experts + 1} contiguous 32-bit integers")
+    if (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.shape[0] != experts + 1
+            or not offsets.is_contiguous()):
+        raise ValueError(f"offsets must be {experts + 1} contiguous 32-bit integers")
 
 
 def _type(name: str, t: torch.Tensor, kinds) -> int:
@@ -79,20 +106,37 @@ def _type(name: str, t: torch.Tensor, kinds) -> int:
     return dtype_code(t.dtype)
 
 
-def _out(out, rows, cols, dtype, device, inputs) -> tuple[torch.Tensor, bool]:
-    """The output, and whether it is new (then the rows nobody computes are zeroed)."""
+def _wants_grad(*tensors) -> bool:
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
+
+
+def _out(out, rows: int, cols: int, dtype, device) -> tuple[torch.Tensor, int, bool]:
+    """The output, its row stride, and whether it is new (then the rows nobody computes are zeroed)."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), True
-    _on_device(device, out=out)
-    _need(out.dtype == dtype, f"out must be {dtype}")
-    _matrix("out", out, rows, cols)
-    _need(not (torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (*inputs, out))),
-          "out= takes no part in autograd; call under torch.no_grad()")
-    return out, False
+        return torch.empty((rows, cols), dtype=dtype, device=device), cols, True
+    if out.device != device:
+        raise ValueError(f"out is on {out.device}, the operands on {device}")
+    if out.dtype != dtype:
+        raise ValueError(f"out must be {dtype}")
+    return out, _matrix("out", out, rows, cols), False
 
 
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _no_autograd(out, *inputs) -> None:
+    _need(not _wants_grad(out, *inputs), "out= takes no part in autograd; call under torch.no_grad()")
+
+
+def _enqueue(device: torch.device, fn, *args) -> None:
+    """fn(*args, stream) with `device` current, on its current stream."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            fn(*args, _raw_stream(index))
 
 
 def _workspace(nbytes: int, device: torch.device):
@@ -105,7 +149,6 @@ def _ptr(t) -> int:
 
 # ---------------------------------------------------------------------------- tokens by expert
 
-@dataclass(frozen=True)
 class TokenOrder:
     """A router's choices sorted by expert (made by ``sort_tokens``).
 
@@ -113,70 +156,71 @@ class TokenOrder:
     the number of kept slots. slots [tokens * top_k]: sorted position to slot (token * top_k + j).
     rows [tokens, top_k]: slot to sorted position. All 32-bit.
     """
-    offsets: torch.Tensor
-    slots: torch.Tensor
-    rows: torch.Tensor
-    num_experts: int
+    __slots__ = ("offsets", "slots", "rows", "num_experts", "tokens", "top_k", "sorted_rows", "kept_ptr")
 
-    @property
-    def tokens(self) -> int:
-        return self.rows.shape[0]
-
-    @property
-    def top_k(self) -> int:
-        return self.rows.shape[1]
-
-    def kept_ptr(self) -> int:
-        return self.offsets.data_ptr() + 4 * self.num_experts
+    def __init__(self, offsets: torch.Tensor, slots: torch.Tensor, rows: torch.Tensor, num_experts: int):
+        self.offsets, self.slots, self.rows, self.num_experts = offsets, slots, rows, num_experts
+        self.tokens, self.top_k = rows.shape
+        self.sorted_rows = self.tokens * self.top_k
+        self.kept_ptr = offsets.data_ptr() + 4 * num_experts  # where offsets[num_experts] lies
 
 
 def sort_tokens(experts: torch.Tensor, num_experts: int) -> TokenOrder:
     """Sort the slots of ``experts`` ([tokens, top_k] or [tokens] ids, 32- or 64-bit integers) by expert,
     slots of one expert in their own order. Ids outside [0, num_experts) are dropped: they sort behind
     the last expert. At most 1024 experts."""
-    if experts.dtype not in (torch.int32, torch.int64):
+    bits = 64 if experts.dtype == torch.int64 else 32
+    if bits == 32 and experts.dtype != torch.int32:
         raise TypeError(f"unsupported dtype {experts.dtype} of experts")
-    _need(experts.is_cuda, "experts must be a device tensor")
-    _need(experts.dim() in (1, 2), "experts must be [tokens, top_k] or [tokens]")
+    if not experts.is_cuda:
+        raise ValueError("experts must be a device tensor")
+    dim = experts.dim()
+    if dim != 2:
+        _need(dim == 1, "experts must be [tokens, top_k] or [tokens]")
+        experts = experts[:, None]
     num_experts = int(num_experts)
-    ids = (experts if experts.dim() == 2 else experts[:, None]).contiguous()
+    ids = experts.contiguous()
     n, dev = ids.numel(), ids.device
-    ws_bytes = _lib.experts_sort_workspace_bytes(n, num_experts)
-    with torch.cuda.device(dev):
-        offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-        slots = torch.empty(n, dtype=torch.int32, device=dev)
-        rows = torch.empty(ids.shape, dtype=torch.int32, device=dev)
-        ws = _workspace(ws_bytes, dev)
-        _lib.experts_sort(ids.data_ptr(), 8 * ids.element_size(), n, num_experts, offsets.data_ptr(), slots.data_ptr(),
-                          rows.data_ptr(), _ptr(ws), ws_bytes, _stream(dev))
+    ws_bytes = _lib.experts_sort_workspace_bytes(n, num_experts) if n > _SORT_ONE or not 0 < num_experts <= 1024 else 0
+    offsets = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
+    slots = torch.empty(n, dtype=torch.int32, device=dev)
+    rows = torch.empty(ids.shape, dtype=torch.int32, device=dev)
+    ws = _workspace(ws_bytes, dev)
+    _enqueue(dev, _lib.experts_sort, ids.data_ptr(), bits, n, num_experts, offsets.data_ptr(), slots.data_ptr(),
+             rows.data_ptr(), _ptr(ws), ws_bytes)
     return TokenOrder(offsets, slots, rows, num_experts)
 
 
 def _gather(x, order, out):
-    code = _type("x", x, (*_16BIT, torch.float32))
-    _on_device(x.device, x=x, rows=order.rows)
-    ldx = _matrix("x", x, rows=order.tokens)
-    out, fresh = _out(out, order.rows.numel(), x.shape[1], x.dtype, x.device, (x,))
-    with torch.cuda.device(x.device):
-        _lib.experts_gather(x.data_ptr(), code, order.tokens, order.top_k, x.shape[1], ldx, order.rows.data_ptr(),
-                            order.kept_ptr(), out.data_ptr(), _matrix("out", out), fresh, _stream(x.device))
+    code = _type("x", x, _FLOATS)
+    _on_device("x order", x, order.rows)
+    ldx = _matrix("x", x, order.tokens)
+    width, dev = x.shape[1], x.device
+    out, ldo, fresh = _out(out, order.sorted_rows, width, x.dtype, dev)
+    _enqueue(dev, _lib.experts_gather, x.data_ptr(), code, order.tokens, order.top_k, width, ldx, order.rows.data_ptr(),
+             order.kept_ptr, out.data_ptr(), ldo, fresh)
     return out
 
 
+def _router_weights(weights, order):
+    """The weights, contiguous, and their type's code."""
+    if weights is None:
+        return None, 0
+    code = _type("weights", weights, _FLOATS)
+    if weights.shape != order.rows.shape:
+        raise ValueError(f"weights must be {tuple(order.rows.shape)}")
+    return weights.contiguous(), code
+
+
 def _combine(y, order, weights, out):
-    code = _type("y", y, (*_16BIT, torch.float32))
-    _on_device(y.device, y=y, rows=order.rows, weights=weights)
-    ldy = _matrix("y", y, rows=order.rows.numel())
-    wcode = 0
-    if weights is not None:
-        wcode = _type("weights", weights, (*_16BIT, torch.float32))
-        _need(tuple(weights.shape) == tuple(order.rows.shape), f"weights must be {tuple(order.rows.shape)}")
-        weights = weights.contiguous()
-    out, _ = _out(out, order.tokens, y.shape[1], y.dtype, y.device, (y, weights))
-    with torch.cuda.device(y.device):
-        _lib.experts_combine(y.data_ptr(), code, order.tokens, order.top_k, y.shape[1], ldy, order.rows.data_ptr(),
-                             order.kept_ptr(), _ptr(weights), wcode, out.data_ptr(), _matrix("out", out),
-                             _stream(y.device))
+    code = _type("y", y, _FLOATS)
+    _on_device("y order weights", y, order.rows, weights)
+    ldy = _matrix("y", y, order.sorted_rows)
+    weights, wcode = _router_weights(weights, order)
+    width, dev = y.shape[1], y.device
+    out, ldo, _ = _out(out, order.tokens, width, y.dtype, dev)
+    _enqueue(dev, _lib.experts_combine, y.data_ptr(), code, order.tokens, order.top_k, width, ldy, order.rows.data_ptr(),
+             order.kept_ptr, _ptr(weights), wcode, out.data_ptr(), ldo)
     return out
 
 
@@ -189,23 +233,17 @@ def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, order: TokenOrder,
                       weights: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
     """Gradients of ``combine_rows`` for y and the weights (None without weights), in their types. Rows
     and weights of dropped slots get zeros."""
-    code = _type("y", y, (*_16BIT, torch.float32))
-    dev = y.device
-    _on_device(dev, y=y, dout=dout, rows=order.rows, weights=weights)
-    _need(dout.dtype == y.dtype, f"dout must be {y.dtype}")
-    ldy = _matrix("y", y, rows=order.rows.numel())
-    lddo = _matrix("dout", dout, rows=order.tokens, cols=y.shape[1])
-    wcode, dw = 0, None
-    if weights is not None:
-        wcode = _type("weights", weights, (*_16BIT, torch.float32))
-        _need(tuple(weights.shape) == tuple(order.rows.shape), f"weights must be {tuple(order.rows.shape)}")
-        weights = weights.detach().contiguous()
-        dw = torch.empty(order.rows.shape, dtype=weights.dtype, device=dev)
-    dy = torch.empty(y.shape, dtype=y.dtype, device=dev)
-    with torch.cuda.device(dev):
-        _lib.experts_combine_grad(dout.data_ptr(), lddo, y.data_ptr(), code, order.tokens, order.top_k, y.shape[1], ldy,
-                                  order.rows.data_ptr(), order.kept_ptr(), _ptr(weights), wcode, dy.data_ptr(),
-                                  y.shape[1], _ptr(dw), True, _stream(dev))
+    code = _type("y", y, _FLOATS)
+    _on_device("y dout order weights", y, dout, order.rows, weights)
+    _need(dout.dtype == y.dtype, "dout must have y's dtype")
+    width, dev = y.shape[1] if y.dim() == 2 else 0, y.device
+    ldy = _matrix("y", y, order.sorted_rows)
+    lddo = _matrix("dout", dout, order.tokens, width)
+    weights, wcode = _router_weights(weights, order)
+    dw = torch.empty(order.rows.shape, dtype=weights.dtype, device=dev) if weights is not None else None
+    dy = torch.empty((order.sorted_rows, width), dtype=y.dtype, device=dev)
+    _enqueue(dev, _lib.experts_combine_grad, dout.data_ptr(), lddo, y.data_ptr(), code, order.tokens, order.top_k, width,
+             ldy, order.rows.data_ptr(), order.kept_ptr, _ptr(weights), wcode, dy.data_ptr(), width, _ptr(dw), True)
     return dy, dw
 
 
@@ -239,59 +277,69 @@ class _Combine(torch.autograd.Function):
 def gather_rows(x: torch.Tensor, order: TokenOrder, out: torch.Tensor | None = None) -> torch.Tensor:
     """Token rows x [tokens, width] in the order's sorted rows [tokens * top_k, width]. Rows at dropped
     positions are zeros in a new tensor, and left as they were in ``out``."""
-    return _Gather.apply(x, order) if out is None else _gather(x, order, out)
+    if out is not None:
+        _no_autograd(out, x)
+    elif _wants_grad(x):
+        return _Gather.apply(x, order)
+    return _gather(x, order, out)
 
 
 def combine_rows(y: torch.Tensor, order: TokenOrder, weights: torch.Tensor | None = None,
                  out: torch.Tensor | None = None) -> torch.Tensor:
     """Each token's weighted sum of its kept sorted rows: y [tokens * top_k, width], weights [tokens,
     top_k] (fp32 or 16-bit; None: ones). Summed in fp32 in the slots' order, rounded once to y's type."""
-    return _Combine.apply(y, order, weights) if out is None else _combine(y, order, weights, out)
+    if out is not None:
+        _no_autograd(out, y, weights)
+    elif _wants_grad(y, weights):
+        return _Combine.apply(y, order, weights)
+    return _combine(y, order, weights, out)
 
 
 # --------------------------------------------------------------------------- experts' products
 
 def _grouped_run(mode, x, y, out, offsets, rows, experts, n, k, ldx, ldy, ldo, stride, fresh):
-    p = _lib.GemmGrouped(mode=mode, rows=rows, experts=experts, n=n, k=k, in_dtype=dtype_code(x.dtype),
-                         out_dtype=dtype_code(out.dtype), ldx=ldx, ldy=ldy, ldo=ldo, stride=stride, zero_rest=int(fresh))
-    ws_bytes = _lib.gemm_grouped_workspace_bytes(p, x.data_ptr(), y.data_ptr())
-    with torch.cuda.device(x.device):
-        ws = _workspace(ws_bytes, x.device)
-        _lib.gemm_grouped_run(p, x.data_ptr(), y.data_ptr(), out.data_ptr(), offsets.data_ptr(), _ptr(ws), ws_bytes,
-                              _stream(x.device))
+    p = _lib.GemmGrouped(mode, rows, experts, n, k, dtype_code(x.dtype), dtype_code(out.dtype), ldx, ldy, ldo, stride,
+                         fresh)
+    xp, yp = x.data_ptr(), y.data_ptr()
+    ws_bytes = _lib.gemm_grouped_workspace_bytes(p, xp, yp)
+    ws = _workspace(ws_bytes, x.device)
+    _enqueue(x.device, _lib.gemm_grouped_run, p, xp, yp, out.data_ptr(), offsets.data_ptr(), _ptr(ws), ws_bytes)
     return out
+
+
+def _result_type(out_dtype, out, default):
+    dtype = out_dtype or (default if out is None else out.dtype)
+    dtype_code(dtype)
+    return dtype
 
 
 def _grouped_forward(A, B, offsets, out_dtype, out):
     _type("A", A, _16BIT)
-    _need(B.dtype == A.dtype, f"B must be {A.dtype}")
-    _on_device(A.device, A=A, B=B, offsets=offsets)
-    ldb, stride = _stack("B", B)
-    E, N, K = B.shape
-    lda = _matrix("A", A, cols=K)
+    _need(B.dtype == A.dtype, "B must have A's dtype")
+    _on_device("A B offsets", A, B, offsets)
+    E, N, K, ldb, stride = _stack("B", B)
+    lda = _matrix("A", A, None, K)
     _offsets(offsets, E)
-    dtype = out.dtype if out is not None and out_dtype is None else out_dtype or A.dtype
-    dtype_code(dtype)
-    C, fresh = _out(out, A.shape[0], N, dtype, A.device, (A, B))
-    return _grouped_run(_lib.GEMM_GROUPED_FORWARD, A, B, C, offsets, A.shape[0], E, N, K, lda, ldb, _matrix("out", C),
-                        stride, fresh)
+    rows = A.shape[0]
+    C, ldc, fresh = _out(out, rows, N, _result_type(out_dtype, out, A.dtype), A.device)
+    return _grouped_run(_lib.GEMM_GROUPED_FORWARD, A, B, C, offsets, rows, E, N, K, lda, ldb, ldc, stride, fresh)
 
 
 def grouped_matmul_grad_a(dC: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
                           out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of ``grouped_matmul`` for A: dA[i] = dC[i]·B[e] for expert e's rows i, in dC's type. Rows behind
     the last expert: zeros in a new tensor, left as they were in ``out``."""
-    dC, B = dC.detach(), B.detach()
     _type("dC", dC, _16BIT)
-    _need(B.dtype == dC.dtype, f"B must be {dC.dtype}")
-    _on_device(dC.device, dC=dC, B=B, offsets=offsets)
-    ldb, stride = _stack("B", B)
-    E, N, K = B.shape
-    lddc = _matrix("dC", dC, cols=N)
+    _need(B.dtype == dC.dtype, "B must have dC's dtype")
+    _on_device("dC B offsets", dC, B, offsets)
+    E, N, K, ldb, stride = _stack("B", B)
+    lddc = _matrix("dC", dC, None, N)
     _offsets(offsets, E)
-    dA, fresh = _out(out, dC.shape[0], K, dC.dtype, dC.device, ())
-    return _grouped_run(_lib.GEMM_GROUPED_GRAD_A, dC, B, dA, offsets, dC.shape[0], E, N, K, lddc, ldb, _matrix("out", dA),
-                        stride, fresh)
+    rows = dC.shape[0]
+    if out is not None:
+        _no_autograd(out)
+    dA, lda, fresh = _out(out, rows, K, dC.dtype, dC.device)
+    return _grouped_run(_lib.GEMM_GROUPED_GRAD_A, dC, B, dA, offsets, rows, E, N, K, lddc, ldb, lda, stride, fresh)
 
 
 def grouped_matmul_grad_b(dC: torch.Tensor, A: torch.Tensor, offsets: torch.Tensor,
@@ -299,20 +347,18 @@ def grouped_matmul_grad_b(dC: torch.Tensor, A: torch.Tensor, offsets: torch.Tens
     """Gradient of ``grouped_matmul`` for B, [experts, n, k]: dB[e] = sum over expert e's rows i of
     dC[i]ᵀ·A[i], in A's type or ``out_dtype`` (fp32 for a main copy of the weights); zeros for an expert
     without rows."""
-    dC, A = dC.detach(), A.detach()
     _type("A", A, _16BIT)
-    _need(dC.dtype == A.dtype, f"dC must be {A.dtype}")
-    _on_device(A.device, dC=dC, A=A, offsets=offsets)
+    _need(dC.dtype == A.dtype, "dC must have A's dtype")
+    _on_device("A dC offsets", A, dC, offsets)
     _need(offsets.dim() == 1 and offsets.shape[0] >= 1, "offsets must be [experts + 1]")
     E = offsets.shape[0] - 1
     _offsets(offsets, E)
-    lddc = _matrix("dC", dC, rows=A.shape[0])
     lda = _matrix("A", A)
-    N, K = dC.shape[1], A.shape[1]
-    dtype = out_dtype or A.dtype
-    dtype_code(dtype)
-    dB = torch.empty((E, N, K), dtype=dtype, device=A.device)
-    return _grouped_run(_lib.GEMM_GROUPED_GRAD_B, dC, A, dB, offsets, A.shape[0], E, N, K, lddc, lda, K, N * K, True)
+    rows, K = A.shape
+    lddc = _matrix("dC", dC, rows)
+    N = dC.shape[1]
+    dB = torch.empty((E, N, K), dtype=_result_type(out_dtype, None, A.dtype), device=A.device)
+    return _grouped_run(_lib.GEMM_GROUPED_GRAD_B, dC, A, dB, offsets, rows, E, N, K, lddc, lda, K, N * K, True)
 
 
 class _Grouped(torch.autograd.Function):
@@ -336,7 +382,9 @@ def grouped_matmul(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out_
     """C[i] = A[i]·B[e]ᵀ for expert e's rows offsets[e] <= i < offsets[e + 1]: A [rows, k] and B [experts, n, k]
     fp16 or bf16, fp32 sums, C in A's type or ``out_dtype``. ``offsets``: 32-bit, on the device (a
     ``TokenOrder``'s). Rows behind the last expert are zeros in a new tensor, left as they were in ``out``."""
-    if out is None:
+    if out is not None:
+        _no_autograd(out, A, B)
+    elif _wants_grad(A, B):
         return _Grouped.apply(A, B, offsets, out_dtype)
     return _grouped_forward(A, B, offsets, out_dtype, out)
 
@@ -364,7 +412,7 @@ def pack_w4(q: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = 
     shape, or None for z = 8. group_size 32, 64 or 128."""
     _need(q.dtype == torch.uint8 and q.dim() in (2, 3), "q must be [n, k] or [experts, n, k] bytes")
     _type("scales", scales, _16BIT)
-    _on_device(q.device, q=q, scales=scales, zeros=zeros)
+    _on_device("q scales zeros", q, scales, zeros)
     group_size = int(group_size)
     _need(group_size in (32, 64, 128), "group_size must be 32, 64 or 128")
     n, k = q.shape[-2:]
@@ -373,12 +421,11 @@ def pack_w4(q: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = 
     _need(zeros is None or (zeros.dtype == torch.uint8 and tuple(zeros.shape) == shape), f"zeros must be bytes {shape}")
     matrices = q.shape[0] if q.dim() == 3 else 1
     nbytes = _lib.gemm_w4_packed_bytes(matrices, n, k, group_size, zeros is not None)
-    with torch.cuda.device(q.device):
-        q, scales = q.contiguous(), scales.detach().contiguous()
-        zeros = zeros.contiguous() if zeros is not None else None
-        packed = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        _lib.gemm_w4_pack(q.data_ptr(), scales.data_ptr(), _ptr(zeros), matrices, n, k, group_size, packed.data_ptr(),
-                          _stream(q.device))
+    q, scales = q.contiguous(), scales.detach().contiguous()
+    zeros = zeros.contiguous() if zeros is not None else None
+    packed = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    _enqueue(q.device, _lib.gemm_w4_pack, q.data_ptr(), scales.data_ptr(), _ptr(zeros), matrices, n, k, group_size,
+             packed.data_ptr())
     return W4Weight(packed, matrices, q.dim() == 3, n, k, group_size, zeros is not None, scales.dtype)
 
 
@@ -388,27 +435,26 @@ def w4_matmul(x: torch.Tensor, w: W4Weight, offsets: torch.Tensor | None = None,
     offsets[e] <= i < offsets[e + 1] of a weight packed from [experts, n, k]. x in the scales' type; no weight
     is rounded, sums are fp32. No gradient. Rows behind the last expert are zeros in a new tensor, left as they
     were in ``out``."""
-    _type("x", x, _16BIT)
-    _need(x.dtype == w.dtype, f"x must be {w.dtype}, the scales' type")
-    _on_device(x.device, x=x, weight=w.packed, offsets=offsets)
-    _need((offsets is not None) == w.stacked,
-          "offsets go with a weight packed from [experts, n, k], and only with one")
-    _need(not (torch.is_grad_enabled() and x.requires_grad), "w4_matmul has no gradient; call under torch.no_grad()")
-    ldx = _matrix("x", x, cols=w.k)
+    code = _type("x", x, _16BIT)
+    _need(x.dtype == w.dtype, "x must have the dtype of the scales")
+    _on_device("x weight offsets", x, w.packed, offsets)
+    _need((offsets is not None) == w.stacked, "offsets go with a weight packed from [experts, n, k], and only with one")
+    _need(not _wants_grad(x, out), "w4_matmul has no gradient; call under torch.no_grad()")
+    ldx = _matrix("x", x, None, w.k)
     if offsets is not None:
         _offsets(offsets, w.matrices)
-    dtype = out.dtype if out is not None and out_dtype is None else out_dtype or x.dtype
-    dtype_code(dtype)
-    out, fresh = _out(out, x.shape[0], w.n, dtype, x.device, ())
-    p = _lib.GemmW4(rows=x.shape[0], matrices=w.matrices, n=w.n, k=w.k, group=w.group_size,
-                    has_zeros=int(w.has_zeros), dtype=dtype_code(x.dtype), out_dtype=dtype_code(dtype), ldx=ldx,
-                    ldo=_matrix("out", out), zero_rest=int(fresh))
-    with torch.cuda.device(x.device):
-        ws_bytes = _lib.gemm_w4_workspace_bytes(p, offsets is not None)
-        ws = _workspace(ws_bytes, x.device)
-        _lib.gemm_w4_run(p, x.data_ptr(), w.packed.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(ws), ws_bytes,
-                         _stream(x.device))
+    rows, dev = x.shape[0], x.device
+    dtype = _result_type(out_dtype, out, x.dtype)
+    out, ldo, fresh = _out(out, rows, w.n, dtype, dev)
+    p = _lib.GemmW4(rows, w.matrices, w.n, w.k, w.group_size, w.has_zeros, code, dtype_code(dtype), ldx, ldo, fresh)
+    _enqueue(dev, _w4_run, p, x, w.packed, offsets, out)
     return out
+
+
+def _w4_run(p, x, packed, offsets, out, stream):
+    ws_bytes = _lib.gemm_w4_workspace_bytes(p, offsets is not None)
+    ws = _workspace(ws_bytes, x.device)
+    _lib.gemm_w4_run(p, x.data_ptr(), packed.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(ws), ws_bytes, stream)
 
 
 # --------------------------------------------------------------------------------- all together
