@@ -183,7 +183,7 @@ struct W4Entry {
   const void* fn;
   int mt, nt, waves;  // 16-row and 16-column blocks of a workgroup, and its waves
 };
-// variant 0: up to 16 rows; 1: up to 16 rows, two column blocks; 2: 64 rows. gpk: groups per 128 k
+// variant 0 .. 2: 16 rows by 16, 32 or 64 columns; 3: 32 rows by 64; 4: 64 rows by 64. gpk: groups per 128 k
 W4Entry w4_entry(int variant, int bf16, int gpk, bool zero);
 const void* w4_pack_fn();
 const void* w4_pack_groups_fn();

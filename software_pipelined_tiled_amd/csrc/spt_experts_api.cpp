@@ -159,9 +159,14 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
   if (p->n > lim || p->k > lim || p->ldx >= lim / 2 || p->rows > kMax32 || p->matrices > kMax32)
     return GEMM_ERR_UNSUPPORTED;
   const int64_t n16 = ceil_div(p->n, 16), kb = ceil_div(p->k, 128);
-  // rows that share a matrix, on average
+  // Rows that share a matrix, on average, decide how many 16-row blocks a workgroup takes, and the
+  // number of 16-column blocks how many of those. More columns a workgroup reuse each load of x, fewer
+  // keep every compute unit busy. One row of 8192 x 8192 (512 column blocks): 2 columns 9.6 us, 1 11.1,
+  // 4 13.8; 16 rows of 28672 x 8192: 4 columns 35 us, 2 43, 1 58; one row of 1024 x 8192: 1 column 6.3
+  // us, 2 6.8. 64 rows of 8192 x 8192: 32-row workgroups 23 us, 64-row ones 27; 512 rows: 159 and 139 us.
   const int64_t each = p->matrices > 0 ? ceil_div(p->rows, p->matrices) : 0;
-  const int variant = each > 16 ? 2 : (each > 4 && n16 >= 1024 ? 1 : 0);
+  const int64_t cols = n16 * (each <= 16 ? (p->rows < p->matrices ? p->rows : p->matrices) : 1);
+  const int variant = each > 64 ? 4 : each > 16 ? 3 : cols < 384 ? 0 : cols < 1536 || each <= 2 ? 1 : 2;
   s->entry = spt::w4_entry(variant, p->dtype == GEMM_BF16, 128 / p->group, p->has_zeros != 0);
   const int bm = 16 * s->entry.mt;
   s->nblocks = ceil_div(n16, s->entry.nt);

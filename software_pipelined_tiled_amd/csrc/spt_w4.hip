@@ -167,13 +167,16 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
 #pragma unroll
   for (int j = 0; j < NT; ++j) nstep[j] = (nb + j < a.n16 ? j : a.n16 - 1 - nb) * a.kb;
 
+  // A block's loads. Loads complete in the order they were issued, so x travels in the same stage as
+  // the weights it meets: loaded when needed, it would stand behind the weights of the stages to come,
+  // and every block would wait for all of them.
   struct Stage {
     u32x4 q[NT];
+    u32x4 x[4][MT];
     GroupBits s[NT];
     ZeroBits z[NT];
   };
-  auto fetch = [&](Stage& st, int kb) SPT_INLINE {
-    kb = kb < kb1 ? kb : kb1 - 1;  // past the end: a block already read, not used
+  auto fetch_w = [&](Stage& st, int kb) SPT_INLINE {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int64_t b = nstep[j] + kb;
@@ -182,22 +185,35 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
       if constexpr (ZERO) st.z[j] = *(const ZeroBits*)(zp + b * (16 * GPK));
     }
   };
-  // x of 16-row block i, matrix step s of block kb
-  auto load_x = [&](int kb, int s, int i) SPT_INLINE -> u32x4 {
-    const int k0 = kb * 128 + s * 32;
-    if (kb * 128 + 128 <= a.k) return __builtin_amdgcn_raw_buffer_load_b128(rx, xo[i], 2 * k0, 0);
-    const int left = a.k - k0 - 8 * h;  // elements of the lane's chunk that exist
-    u32x4 r = {0, 0, 0, 0};
-    if (left >= 8) {
-      r = __builtin_amdgcn_raw_buffer_load_b128(rx, xo[i], 2 * k0, 0);
-    } else {
+  auto fetch = [&](Stage& st, int kb) SPT_INLINE {
+    fetch_w(st, kb);
 #pragma unroll
-      for (int m = 0; m < 7; ++m)
-        if (m < left)
-          r[m >> 1] |= (unsigned)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rx, xo[i] + 2 * m, 2 * k0, 0)
-                       << (16 * (m & 1));
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) st.x[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, xo[i], 2 * (kb * 128 + s * 32), 0);
+  };
+  // the last block of a K that is no multiple of 128: chunks of x past K are zeros, one that K cuts is
+  // put together from its elements
+  auto fetch_cut = [&](Stage& st, int kb) SPT_INLINE {
+    fetch_w(st, kb);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int k0 = kb * 128 + s * 32, left = a.k - k0 - 8 * h;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        u32x4 r = {0, 0, 0, 0};
+        if (left >= 8) {
+          r = __builtin_amdgcn_raw_buffer_load_b128(rx, xo[i], 2 * k0, 0);
+        } else {
+#pragma unroll
+          for (int m = 0; m < 7; ++m)
+            if (m < left)
+              r[m >> 1] |= (unsigned)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rx, xo[i] + 2 * m, 2 * k0, 0)
+                           << (16 * (m & 1));
+        }
+        st.x[s][i] = r;
+      }
     }
-    return r;
   };
 
   f32x4 acc[MT][NT];
@@ -206,12 +222,7 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](const Stage& st, int kb) SPT_INLINE {
-    u32x4 xf[4][MT];
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-      for (int i = 0; i < MT; ++i) xf[s][i] = load_x(kb, s, i);
+  auto compute = [&](const Stage& st) SPT_INLINE {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
@@ -232,7 +243,7 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
         for (int s = g * (4 / GPK); s < (g + 1) * (4 / GPK); ++s) {
           const u32x4 wf = unpack(st.q[j][s], z);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) sum[i] = mfma16<TIn>(xf[s][i], wf, sum[i]);
+          for (int i = 0; i < MT; ++i) sum[i] = mfma16<TIn>(st.x[s][i], wf, sum[i]);
         }
         const float sc = scale_of<T>((unsigned)(st.s[j] >> (16 * g)) & 0xFFFFu);
 #pragma unroll
@@ -243,19 +254,43 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
     }
   };
 
-  if (kb0 + wave < kb1) {
+  const int kb_full = kb1 < (a.k >> 7) ? kb1 : a.k >> 7;  // blocks below it lie inside K
+  // Block i of this wave is block kb0 + wave + i * W. The steady loop loads in the same order whatever
+  // happens, so that a block's wait leaves the loads of the D - 1 blocks behind it in flight; the last
+  // blocks, which load no more, are computed apart. (A load under a condition inside the loop makes every
+  // wait a wait for all.)
+  const int mine = kb_full - kb0 - wave > 0 ? (kb_full - kb0 - wave + W - 1) / W : 0;
+  if (mine > 0) {
+    auto at = [&](int i) SPT_INLINE { return kb0 + wave + (i < mine ? i : mine - 1) * W; };
     Stage st[D];
 #pragma unroll
-    for (int d = 0; d < D; ++d) fetch(st[d], kb0 + wave + d * W);
-    for (int kb = kb0 + wave; kb < kb1; kb += D * W) {
+    for (int d = 0; d < D; ++d) {
+      fetch(st[d], at(d));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    int i = 0;
+    for (; i + 2 * D <= mine; i += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (kb + d * W < kb1) {
-          compute(st[d], kb + d * W);
-          fetch(st[d], kb + (d + D) * W);
-        }
+        compute(st[d]);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch(st[d], at(i + D + d));
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (i + d < mine) compute(st[d]);
+      if (i + D + d < mine) fetch(st[d], at(i + D + d));
+    }
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d)
+      if (i + D + d < mine) compute(st[d]);
+  }
+  if (kb_full < kb1 && kb_full >= kb0 && (kb_full - kb0) % W == wave) {
+    Stage st;
+    fetch_cut(st, kb_full);
+    compute(st);
   }
 
   // the waves' sums, added in wave order
@@ -304,8 +339,10 @@ template <int T>
 static W4Entry w4_pick(int variant, int gpk, bool zero) {
   switch (variant) {
     case 0: return w4_pick_group<T, 1, 1, 8, 4>(gpk, zero);
-    case 1: return w4_pick_group<T, 1, 2, 8, 4>(gpk, zero);
-    default: return w4_pick_group<T, 4, 4, 4, 2>(gpk, zero);
+    case 1: return w4_pick_group<T, 1, 2, 8, 2>(gpk, zero);
+    case 2: return w4_pick_group<T, 1, 4, 8, 2>(gpk, zero);
+    case 3: return w4_pick_group<T, 2, 4, 8, 1>(gpk, zero);
+    default: return w4_pick_group<T, 4, 4, 4, 1>(gpk, zero);
   }
 }
 W4Entry w4_entry(int variant, int bf16, int gpk, bool zero) {
