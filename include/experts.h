@@ -90,6 +90,7 @@ typedef struct {
   gemm_dtype_t out_dtype; /* F16, BF16 or F32 */
   int64_t ldx, ldy, ldo, stride;
   int zero_rest; /* FORWARD, GRAD_A: zero the output rows behind the last expert, else leave them */
+  int tile;      /* rows of an output tile: 0 for the library's choice, else 32 (not GRAD_B), 128 or 256 */
 } gemm_grouped_t;
 
 /*

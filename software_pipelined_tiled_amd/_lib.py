@@ -57,7 +57,8 @@ class GemmConfig(ctypes.Structure):
 class GemmGrouped(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int), ("rows", ctypes.c_int64), ("experts", ctypes.c_int64), ("n", ctypes.c_int64),
                 ("k", ctypes.c_int64), ("in_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int), ("ldx", ctypes.c_int64),
-                ("ldy", ctypes.c_int64), ("ldo", ctypes.c_int64), ("stride", ctypes.c_int64), ("zero_rest", ctypes.c_int)]
+                ("ldy", ctypes.c_int64), ("ldo", ctypes.c_int64), ("stride", ctypes.c_int64), ("zero_rest", ctypes.c_int),
+                ("tile", ctypes.c_int)]
 
 
 class GemmW4(ctypes.Structure):

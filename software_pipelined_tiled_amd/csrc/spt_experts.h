@@ -38,7 +38,8 @@ __device__ __forceinline__ GroupBlock find_group(const int* __restrict__ offsets
   GroupBlock g;
   g.e = -1;
   g.begin = g.end = g.block = g.blocks = g.local = 0;
-  const int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+  int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+  asm volatile("" : "+v"(lane));  // lane addresses are made here, not kept in registers across a caller's loop
   const int groups = rest ? E + 1 : E;
   int left = u;  // units still to skip
   for (int base = 0; base < groups; base += 64) {
@@ -142,8 +143,9 @@ struct GroupedEntry {
   const void* fn;
   int bm, bn, threads, per_cu;
 };
-// variant 0: large tiles, 1: small row blocks (not grad B)
-GroupedEntry grouped_entry(int mode, int variant, int bf16, int out);
+// tile: rows of an output tile, 32 (not grad B), 128 or 256
+GroupedEntry grouped_entry(int mode, int tile, int bf16, int out);
+GroupedEntry grouped_pp_entry(int mode, int bf16, int out);
 
 // ------------------------------------------------------------------------------ 4-bit weights
 struct W4PackArgs {

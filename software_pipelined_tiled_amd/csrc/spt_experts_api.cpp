@@ -102,7 +102,8 @@ gemm_status_t grouped_shape(const gemm_grouped_t* p, const void* X, const void* 
   if (!p || p->mode < GEMM_GROUPED_FORWARD || p->mode > GEMM_GROUPED_GRAD_B) return GEMM_ERR_INVALID;
   if (p->rows < 0 || p->experts < 0 || p->n < 0 || p->k < 0) return GEMM_ERR_INVALID;
   if (!is_dtype(p->in_dtype) || !is_dtype(p->out_dtype)) return GEMM_ERR_INVALID;
-  if (!is16(p->in_dtype)) return GEMM_ERR_UNSUPPORTED;
+  if (p->tile != 0 && p->tile != 32 && p->tile != 128 && p->tile != 256) return GEMM_ERR_INVALID;
+  if (!is16(p->in_dtype) || (p->tile == 32 && p->mode == GEMM_GROUPED_GRAD_B)) return GEMM_ERR_UNSUPPORTED;
   const int64_t lim = (int64_t)1 << 20;
   if (p->rows > kMax32 || p->experts > kMax32 || p->n > kMax32 || p->k > kMax32) return GEMM_ERR_UNSUPPORTED;
   const bool gb = p->mode == GEMM_GROUPED_GRAD_B;
@@ -128,6 +129,24 @@ gemm_status_t grouped_shape(const gemm_grouped_t* p, const void* X, const void* 
     s->ws += o.bytes;
   }
   return GEMM_OK;
+}
+
+// Rows of an output tile. Few rows per expert: 32, so that reading B is all there is to do. Else the
+// tile with the shorter time: rounds of tiles over the compute units, times K-tiles (and about two more
+// for the stores), times what a K-tile costs a compute unit.
+int grouped_tile(const gemm_grouped_t* p, int cu) {
+  const bool gb = p->mode == GEMM_GROUPED_GRAD_B;
+  const int64_t e = p->experts > 0 ? p->experts : 1;
+  const int64_t each = ceil_div(p->rows, e);
+  if (!gb && each <= 32) return 32;
+  const int64_t out_n = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
+  const double kt = (double)ceil_div(gb ? each : p->mode == GEMM_GROUPED_FORWARD ? p->k : p->n, 64) + 2;
+  auto cost = [&](int bm, int64_t slots, double per_k_tile) {
+    // an expert's last row block is half full on average
+    const int64_t rb = gb ? e * ceil_div(p->n, bm) : (2 * p->rows + e * bm) / (2 * bm) + 1;
+    return (double)ceil_div(rb * ceil_div(out_n, bm), slots) * kt * per_k_tile;
+  };
+  return cost(256, cu, 1.5) <= cost(128, 2 * (int64_t)cu, 1.1) ? 256 : 128;
 }
 
 gemm_status_t pad_operand(Operand& o, const void** ptr, char* ws, void* stream) {
@@ -332,10 +351,8 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   st = device_cus(&cu);
   if (st != GEMM_OK) return st;
 
-  // few rows per expert: small row blocks, so that reading B is all there is to do
-  const int64_t each = p->experts > 0 ? ceil_div(p->rows, p->experts) : 0;
-  const int variant = !gb && each <= 32 ? 1 : 0;
-  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, variant, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
+  const int tile = p->tile ? p->tile : grouped_tile(p, cu);
+  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, tile, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
   const int64_t tiles_m = ceil_div(p->n, entry.bm), tiles_n = ceil_div(out_n, entry.bn);
   const int64_t units = gb ? p->experts * tiles_m * tiles_n
                            : spt::max_row_blocks(p->rows, p->experts, entry.bm) * tiles_n;

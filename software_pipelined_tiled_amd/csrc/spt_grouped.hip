@@ -9,8 +9,7 @@
 // An operand that is contiguous in c is staged and read as in the dense kernels: rows of 64 c
 // (128 bytes), chunk XOR (row mod 8), one ds_read_b128 per 16 x 32 fragment. One that is contiguous
 // in i or j is staged as it lies, 64 rows of c by BM or BN columns, and turned on the way from LDS to
-// registers: ds_read_b64_tr_b16 hands each lane four c of one column (16 lanes read a 4 x 16 block),
-// two of them make a fragment, so no transposed copy of B, A or dC is written to memory. Rows past an
+// registers (spt_transpose.h), so no transposed copy of B, A or dC is written to memory. Rows past an
 // expert's last lie past its descriptor's end and read as zeros, so ragged experts need no padding in
 // grad B's sum.
 //
@@ -19,25 +18,9 @@
 // of S LDS stages by direct global->LDS loads; one barrier per K-tile.
 #include "spt_device.h"
 #include "spt_experts.h"
+#include "spt_transpose.h"
 
 namespace spt {
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4 lds_s16x4_t;
-
-// Four c of one column per lane: lane p of each 16 supplies the address of columns 4 (p % 4) .. +3 of
-// row p / 4 and receives column p, rows 0 .. 3.
-__device__ __forceinline__ uint64_t read_tr16(const char* p) {
-  return __builtin_bit_cast(uint64_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)(const lds_void_t*)p));
-}
-
-// A tile of 64 c rows x R columns: row c holds R / 8 chunks of 16 bytes, logical chunk q at physical
-// chunk q XOR tr_swz(c). A transposing read touches 64 bytes of each of four neighbouring rows; the XOR
-// moves them to the four 64-byte quarters of the 64 banks.
-template <int R>
-__device__ __forceinline__ int tr_swz(int c) {
-  return R >= 128 ? (c & 3) << 2 : (R == 64 ? ((c >> 1) & 1) << 2 : 0);
-}
 
 // MODE: kGroupedForward .. ; a WM x WN grid of waves; S stages; MINW: workgroups per CU to fit.
 template <int MODE, int BM, int BN, int WM, int WN, int S, int PER_CU, typename TIn, int OUT>
@@ -67,7 +50,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
     const int q = wave * LX + j;
     if constexpr (!TX) return (unsigned)((8 * q + (lane >> 3)) * ldx + n_kc) * 2u;
     else {
-      const int c = q * (512 / BM) + lane / (BM / 8), ch = (lane % (BM / 8)) ^ tr_swz<BM>(c);
+      const int c = q * (512 / BM) + lane / (BM / 8), ch = (lane % (BM / 8)) ^ (2 * tr_swz<BM>(c));
       return (unsigned)(c * ldx + 8 * ch) * 2u;
     }
   };
@@ -75,40 +58,20 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
     const int q = wave * LY + j;
     if constexpr (!TY) return (unsigned)(b_row_perm(8 * q + (lane >> 3)) * ldy + n_kc) * 2u;
     else {
-      const int c = q * (512 / BN) + lane / (BN / 8), ch = (lane % (BN / 8)) ^ tr_swz<BN>(c);
+      const int c = q * (512 / BN) + lane / (BN / 8), ch = (lane % (BN / 8)) ^ (2 * tr_swz<BN>(c));
       return (unsigned)(c * ldy + 8 * ch) * 2u;
     }
   };
 
-  // fragment f of k-step s. Columns of Y go to a fragment in the order of b_row_perm, so that a lane
-  // ends up with 8 consecutive output columns per fragment pair.
+  // fragment f of k-step s. Rows of Y that are contiguous in c are staged in the order of b_row_perm, so
+  // that a lane ends up with 8 consecutive output columns per fragment pair.
   auto read_x = [&](const char* t, int s, int f) SPT_INLINE -> u32x4 {
-    if constexpr (!TX) {
-      return *(const u32x4*)(t + lds_chunk_offset(BM, wm * TM + 16 * f + p, 4 * s + h));
-    } else {
-      const int col = wm * TM + 16 * f + 4 * (p & 3);
-      uint64_t r[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c = 32 * s + 8 * h + 4 * u + (p >> 2);
-        r[u] = read_tr16(t + c * (2 * BM) + (((col >> 3) ^ tr_swz<BM>(c)) << 4) + (col & 7) * 2);
-      }
-      return u32x4{(unsigned)r[0], (unsigned)(r[0] >> 32), (unsigned)r[1], (unsigned)(r[1] >> 32)};
-    }
+    if constexpr (!TX) return *(const u32x4*)(t + lds_chunk_offset(BM, wm * TM + 16 * f + p, 4 * s + h));
+    else return tr_frag<2 * BM>(t + tr_offset<BM>(32 * s + 8 * h + (p >> 2), (wm * TM + 16 * f) / 16) + 8 * (p & 3));
   };
   auto read_y = [&](const char* t, int s, int f) SPT_INLINE -> u32x4 {
-    if constexpr (!TY) {
-      return *(const u32x4*)(t + lds_chunk_offset(BN, wn * TN + 16 * f + p, 4 * s + h));
-    } else {
-      const int col = wn * TN + 32 * (f >> 1) + 8 * (p & 3) + 4 * (f & 1);
-      uint64_t r[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int c = 32 * s + 8 * h + 4 * u + (p >> 2);
-        r[u] = read_tr16(t + c * (2 * BN) + (((col >> 3) ^ tr_swz<BN>(c)) << 4) + (col & 7) * 2);
-      }
-      return u32x4{(unsigned)r[0], (unsigned)(r[0] >> 32), (unsigned)r[1], (unsigned)(r[1] >> 32)};
-    }
+    if constexpr (!TY) return *(const u32x4*)(t + lds_chunk_offset(BN, wn * TN + 16 * f + p, 4 * s + h));
+    else return tr_frag<2 * BN>(t + tr_offset<BN>(32 * s + 8 * h + (p >> 2), (wn * TN + 16 * f) / 16) + 8 * (p & 3));
   };
 
   for (int t = xcd_remap(blockIdx.x, a.grid);; t += a.grid) {
@@ -205,12 +168,16 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
         float v[8];
+        if constexpr (TY) {
+          pair_columns(acc[2 * pu][j], acc[2 * pu + 1][j], v);
+        } else {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[q] = acc[2 * pu][j][q];
-          v[4 + q] = acc[2 * pu + 1][j][q];
+          for (int q = 0; q < 4; ++q) {
+            v[q] = acc[2 * pu][j][q];
+            v[4 + q] = acc[2 * pu + 1][j][q];
+          }
         }
-        const int m = wm * TM + 16 * j + p, n = col0 + wn * TN + 32 * pu + 8 * h;
+        const int m = wm * TM + 16 * j + p, n = col0 + wn * TN + 32 * pu + (TY ? pair_column(lane) : 8 * h);
         if (rows_left >= BM && cols_left >= BN) store8<OUT, false>(v, rc, m, rows_left, n, a.n, ldc);
         else store8<OUT, true>(v, rc, m, rows_left, n, a.n, ldc);
         __builtin_amdgcn_sched_barrier(0);
@@ -255,13 +222,14 @@ static GroupedEntry grouped_pick(int bf16, int out) {
   e.fn = fn[bf16][out];
   return e;
 }
-GroupedEntry grouped_entry(int mode, int variant, int bf16, int out) {
+GroupedEntry grouped_entry(int mode, int tile, int bf16, int out) {
+  if (tile == 256) return grouped_pp_entry(mode, bf16, out);
   if (mode == kGroupedForward)
-    return variant == 0 ? grouped_pick<kGroupedForward, 128, 128, 2, 2, 2, 2>(bf16, out)
-                        : grouped_pick<kGroupedForward, 32, 64, 2, 2, 4, 3>(bf16, out);
+    return tile == 128 ? grouped_pick<kGroupedForward, 128, 128, 2, 2, 2, 2>(bf16, out)
+                       : grouped_pick<kGroupedForward, 32, 64, 2, 2, 4, 3>(bf16, out);
   if (mode == kGroupedGradA)
-    return variant == 0 ? grouped_pick<kGroupedGradA, 128, 128, 2, 2, 2, 2>(bf16, out)
-                        : grouped_pick<kGroupedGradA, 32, 64, 2, 2, 4, 3>(bf16, out);
+    return tile == 128 ? grouped_pick<kGroupedGradA, 128, 128, 2, 2, 2, 2>(bf16, out)
+                       : grouped_pick<kGroupedGradA, 32, 64, 2, 2, 4, 3>(bf16, out);
   return grouped_pick<kGroupedGradB, 128, 128, 2, 2, 2, 2>(bf16, out);
 }
 

@@ -297,9 +297,9 @@ def combine_rows(y: torch.Tensor, order: TokenOrder, weights: torch.Tensor | Non
 
 # --------------------------------------------------------------------------- experts' products
 
-def _grouped_run(mode, x, y, out, offsets, rows, experts, n, k, ldx, ldy, ldo, stride, fresh):
+def _grouped_run(mode, x, y, out, offsets, rows, experts, n, k, ldx, ldy, ldo, stride, fresh, tile):
     p = _lib.GemmGrouped(mode, rows, experts, n, k, dtype_code(x.dtype), dtype_code(out.dtype), ldx, ldy, ldo, stride,
-                         fresh)
+                         fresh, tile)
     xp, yp = x.data_ptr(), y.data_ptr()
     ws_bytes = _lib.gemm_grouped_workspace_bytes(p, xp, yp)
     ws = _workspace(ws_bytes, x.device)
@@ -313,7 +313,7 @@ def _result_type(out_dtype, out, default):
     return dtype
 
 
-def _grouped_forward(A, B, offsets, out_dtype, out):
+def _grouped_forward(A, B, offsets, out_dtype, out, tile):
     _type("A", A, _16BIT)
     _need(B.dtype == A.dtype, "B must have A's dtype")
     _on_device("A B offsets", A, B, offsets)
@@ -322,11 +322,12 @@ def _grouped_forward(A, B, offsets, out_dtype, out):
     _offsets(offsets, E)
     rows = A.shape[0]
     C, ldc, fresh = _out(out, rows, N, _result_type(out_dtype, out, A.dtype), A.device)
-    return _grouped_run(_lib.GEMM_GROUPED_FORWARD, A, B, C, offsets, rows, E, N, K, lda, ldb, ldc, stride, fresh)
+    return _grouped_run(_lib.GEMM_GROUPED_FORWARD, A, B, C, offsets, rows, E, N, K, lda, ldb, ldc, stride, fresh,
+                        tile)
 
 
-def grouped_matmul_grad_a(dC: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor,
-                          out: torch.Tensor | None = None) -> torch.Tensor:
+def grouped_matmul_grad_a(dC: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
+                          tile: int = 0) -> torch.Tensor:
     """Gradient of ``grouped_matmul`` for A: dA[i] = dC[i]·B[e] for expert e's rows i, in dC's type. Rows behind
     the last expert: zeros in a new tensor, left as they were in ``out``."""
     _type("dC", dC, _16BIT)
@@ -339,11 +340,12 @@ def grouped_matmul_grad_a(dC: torch.Tensor, B: torch.Tensor, offsets: torch.Tens
     if out is not None:
         _no_autograd(out)
     dA, lda, fresh = _out(out, rows, K, dC.dtype, dC.device)
-    return _grouped_run(_lib.GEMM_GROUPED_GRAD_A, dC, B, dA, offsets, rows, E, N, K, lddc, ldb, lda, stride, fresh)
+    return _grouped_run(_lib.GEMM_GROUPED_GRAD_A, dC, B, dA, offsets, rows, E, N, K, lddc, ldb, lda, stride, fresh,
+                        tile)
 
 
 def grouped_matmul_grad_b(dC: torch.Tensor, A: torch.Tensor, offsets: torch.Tensor,
-                          out_dtype: torch.dtype | None = None) -> torch.Tensor:
+                          out_dtype: torch.dtype | None = None, tile: int = 0) -> torch.Tensor:
     """Gradient of ``grouped_matmul`` for B, [experts, n, k]: dB[e] = sum over expert e's rows i of
     dC[i]ᵀ·A[i], in A's type or ``out_dtype`` (fp32 for a main copy of the weights); zeros for an expert
     without rows."""
@@ -358,14 +360,15 @@ def grouped_matmul_grad_b(dC: torch.Tensor, A: torch.Tensor, offsets: torch.Tens
     lddc = _matrix("dC", dC, rows)
     N = dC.shape[1]
     dB = torch.empty((E, N, K), dtype=_result_type(out_dtype, None, A.dtype), device=A.device)
-    return _grouped_run(_lib.GEMM_GROUPED_GRAD_B, dC, A, dB, offsets, rows, E, N, K, lddc, lda, K, N * K, True)
+    return _grouped_run(_lib.GEMM_GROUPED_GRAD_B, dC, A, dB, offsets, rows, E, N, K, lddc, lda, K, N * K, True,
+                        tile)
 
 
 class _Grouped(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, A, B, offsets, out_dtype):
+    def forward(ctx, A, B, offsets, out_dtype, tile):
         ctx.save_for_backward(A, B, offsets)
-        return _grouped_forward(A, B, offsets, out_dtype, None)
+        return _grouped_forward(A, B, offsets, out_dtype, None, tile)
 
     @staticmethod
     @once_differentiable
@@ -374,19 +377,20 @@ class _Grouped(torch.autograd.Function):
         dC = _rows_apart(dC.to(A.dtype))  # the products take 16-bit operands of one type
         dA = grouped_matmul_grad_a(dC, B, offsets) if ctx.needs_input_grad[0] else None
         dB = grouped_matmul_grad_b(dC, A, offsets) if ctx.needs_input_grad[1] else None
-        return dA, dB, None, None
+        return dA, dB, None, None, None
 
 
 def grouped_matmul(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out_dtype: torch.dtype | None = None,
-                   out: torch.Tensor | None = None) -> torch.Tensor:
+                   out: torch.Tensor | None = None, tile: int = 0) -> torch.Tensor:
     """C[i] = A[i]·B[e]ᵀ for expert e's rows offsets[e] <= i < offsets[e + 1]: A [rows, k] and B [experts, n, k]
     fp16 or bf16, fp32 sums, C in A's type or ``out_dtype``. ``offsets``: 32-bit, on the device (a
-    ``TokenOrder``'s). Rows behind the last expert are zeros in a new tensor, left as they were in ``out``."""
+    ``TokenOrder``'s). Rows behind the last expert are zeros in a new tensor, left as they were in ``out``.
+    ``tile``: rows of an output tile, 0 for the library's choice, else 32, 128 or 256 (the same values)."""
     if out is not None:
         _no_autograd(out, A, B)
     elif _wants_grad(A, B):
-        return _Grouped.apply(A, B, offsets, out_dtype)
-    return _grouped_forward(A, B, offsets, out_dtype, out)
+        return _Grouped.apply(A, B, offsets, out_dtype, tile)
+    return _grouped_forward(A, B, offsets, out_dtype, out, tile)
 
 
 # ------------------------------------------------------------------------------- 4-bit weights

@@ -210,12 +210,12 @@ def plain_grouped(mode, x, y, bounds, experts, n, k):
     return ref, tot
 
 
-def call_grouped(mode, x, y, off, out_dtype=None):
+def call_grouped(mode, x, y, off, out_dtype=None, tile=0):
     if mode == "f":
-        return spt.grouped_matmul(x, y, off, out_dtype=out_dtype)
+        return spt.grouped_matmul(x, y, off, out_dtype=out_dtype, tile=tile)
     if mode == "a":
-        return spt.grouped_matmul_grad_a(x, y, off)
-    return spt.grouped_matmul_grad_b(x, y, off, out_dtype=out_dtype)
+        return spt.grouped_matmul_grad_a(x, y, off, tile=tile)
+    return spt.grouped_matmul_grad_b(x, y, off, out_dtype=out_dtype, tile=tile)
 
 
 def operands(mode, rows, experts, n, k, make):
@@ -255,6 +255,10 @@ def test_grouped_exact(counts, rest, n, k, mode, dtype):
     for extra, start in ((8, 0), (3, 1)):
         got2 = call_grouped(mode, padded(x, extra, start), padded(y, extra, start), off, F32)
         assert torch.equal(got2, got), (extra, start)
+    # every tile, and 16-bit outputs (the sums are below 2^24, rounded once)
+    for tile in (32, 128, 256)[mode == "b":]:
+        assert torch.equal(call_grouped(mode, x, y, off, F32, tile), got), tile
+        assert torch.equal(call_grouped(mode, x, y, off, dtype, tile), got.to(dtype)), tile
 
 
 @pytest.mark.parametrize("mode", ["f", "a", "b"])
@@ -269,6 +273,27 @@ def test_grouped_real(counts, rest, n, k, mode, dtype, out_dtype):
     length = {"f": k, "a": n, "b": max(counts)}[mode]
     close(got, ref, tot, length, dtype if mode == "a" else out_dtype)
     assert torch.equal(call_grouped(mode, x, y, off, out_dtype), got)  # the same bits every time
+    for tile in (32, 128, 256)[mode == "b":]:
+        close(call_grouped(mode, x, y, off, out_dtype, tile), ref, tot, length, dtype if mode == "a" else out_dtype)
+
+
+# tiles a workgroup takes one after another, each with one to three K-tiles: units, stores and loads of
+# neighbouring tiles meet in every phase; empty experts in grad B are one K-tile of zeros
+@pytest.mark.parametrize("mode", ["f", "a", "b"])
+@pytest.mark.parametrize("length", [8, 64, 72, 136, 200])
+@pytest.mark.parametrize("tile", [128, 256])
+def test_grouped_many_tiles_of_short_sums(mode, length, tile):
+    if mode == "b":
+        counts, rest, n, k = [length, 0, length + 1, 3] * 4, 5, 1100, 2000
+    else:
+        counts, rest = [600, 0, 1, 257, 900, 0, 255], 300
+        n, k = (2600, length) if mode == "f" else (length, 2600)
+    off = offsets_of(counts)
+    x, y = operands(mode, sum(counts) + rest, len(counts), n, k, lambda s, seed: ints(s, BF16, seed))
+    ref, _ = plain_grouped(mode, x, y, off.tolist(), len(counts), n, k)
+    for out_dtype in (F32, BF16):
+        got = call_grouped(mode, x, y, off, out_dtype, tile)
+        assert torch.equal(got, ref.to(got.dtype)), out_dtype
 
 
 @pytest.mark.parametrize("mode", ["f", "a"])

@@ -100,7 +100,8 @@ def grouped(**change):
     (dict(stride=0, experts=1), OK), (dict(rows=2**31), UNSUPPORTED), (dict(ldx=2**20), UNSUPPORTED),
     (dict(ldy=2**20, stride=2**26), UNSUPPORTED), (dict(ldo=2**20), UNSUPPORTED),
     (dict(mode=1, ldx=31, ldo=48), INVALID), (dict(mode=1, ldx=32, ldo=47), INVALID), (dict(mode=1, ldx=32, ldo=48), OK),
-    (dict(mode=2, ldx=32, ldo=47), INVALID), (dict(mode=2, ldx=32, ldo=48), OK)])
+    (dict(mode=2, ldx=32, ldo=47), INVALID), (dict(mode=2, ldx=32, ldo=48), OK),
+    (dict(tile=64), INVALID), (dict(tile=32), OK), (dict(tile=32, mode=2, ldx=32, ldo=48), UNSUPPORTED), (dict(tile=256), OK)])
 def test_grouped_shapes(change, status):
     n = ctypes.c_int64()
     assert spt.lib().gemm_grouped_workspace_bytes(ctypes.byref(grouped(**change)), A, A, ctypes.byref(n)) == status
