@@ -11,6 +11,7 @@ namespace {
 constexpr int64_t kMax32 = 0x7FFFFFFF;
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxDevices = 64;
+constexpr int kCus = 256;  // the MI355X's, for choices that must not depend on the device in use
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
@@ -94,42 +95,10 @@ struct Operand {
   int64_t pad_ld, at, bytes;
 };
 struct GroupedShape {
+  int tile;
   Operand x, y;
   int64_t ws;
 };
-
-gemm_status_t grouped_shape(const gemm_grouped_t* p, const void* X, const void* Y, GroupedShape* s) {
-  if (!p || p->mode < GEMM_GROUPED_FORWARD || p->mode > GEMM_GROUPED_GRAD_B) return GEMM_ERR_INVALID;
-  if (p->rows < 0 || p->experts < 0 || p->n < 0 || p->k < 0) return GEMM_ERR_INVALID;
-  if (!is_dtype(p->in_dtype) || !is_dtype(p->out_dtype)) return GEMM_ERR_INVALID;
-  if (p->tile != 0 && p->tile != 32 && p->tile != 128 && p->tile != 256) return GEMM_ERR_INVALID;
-  if (!is16(p->in_dtype) || (p->tile == 32 && p->mode == GEMM_GROUPED_GRAD_B)) return GEMM_ERR_UNSUPPORTED;
-  const int64_t lim = (int64_t)1 << 20;
-  if (p->rows > kMax32 || p->experts > kMax32 || p->n > kMax32 || p->k > kMax32) return GEMM_ERR_UNSUPPORTED;
-  const bool gb = p->mode == GEMM_GROUPED_GRAD_B;
-  const int64_t xc = p->mode == GEMM_GROUPED_FORWARD ? p->k : p->n;
-  const int64_t oc = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
-  if (p->ldx < xc || p->ldy < p->k || p->ldo < oc) return GEMM_ERR_INVALID;
-  const int64_t mat_ld = gb ? p->ldo : p->ldy;  // of the [experts, n, k] tensor
-  if (p->experts > 1 && p->n > 0 && p->stride < (p->n - 1) * mat_ld + p->k) return GEMM_ERR_INVALID;
-  if (p->ldx >= lim || p->ldy >= lim || p->ldo >= lim) return GEMM_ERR_UNSUPPORTED;
-  s->x = Operand{p->rows, xc, p->ldx, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
-  if (gb) s->y = Operand{p->rows, p->k, p->ldy, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
-  else s->y = Operand{p->experts * p->n, p->k, p->ldy, p->n > 0 ? p->n : 1, p->stride, false, 0, 0, 0};
-  s->ws = 0;
-  Operand* ops[2] = {&s->x, &s->y};
-  const void* ptr[2] = {X, Y};
-  for (int i = 0; i < 2; ++i) {
-    Operand& o = *ops[i];
-    o.pad = (uintptr_t)ptr[i] % 16 != 0 || o.cols % 8 != 0 || o.ld % 8 != 0 || o.stride % 8 != 0;
-    if (!o.pad) continue;
-    o.pad_ld = round_up(o.cols, 8);
-    o.at = s->ws;
-    o.bytes = round_up(o.rows * o.pad_ld * 2, 256);
-    s->ws += o.bytes;
-  }
-  return GEMM_OK;
-}
 
 // Rows of an output tile. Few rows per expert: 32, so that reading B is all there is to do. Else the
 // tile with the shorter time: rounds of tiles over the compute units, times K-tiles (and about two more
@@ -147,6 +116,42 @@ int grouped_tile(const gemm_grouped_t* p, int cu) {
     return (double)ceil_div(rb * ceil_div(out_n, bm), slots) * kt * per_k_tile;
   };
   return cost(256, cu, 1.5) <= cost(128, 2 * (int64_t)cu, 1.1) ? 256 : 128;
+}
+
+gemm_status_t grouped_shape(const gemm_grouped_t* p, int cu, const void* X, const void* Y, GroupedShape* s) {
+  if (!p || p->mode < GEMM_GROUPED_FORWARD || p->mode > GEMM_GROUPED_GRAD_B) return GEMM_ERR_INVALID;
+  if (p->rows < 0 || p->experts < 0 || p->n < 0 || p->k < 0) return GEMM_ERR_INVALID;
+  if (!is_dtype(p->in_dtype) || !is_dtype(p->out_dtype)) return GEMM_ERR_INVALID;
+  if (p->tile != 0 && p->tile != 32 && p->tile != 128 && p->tile != 256) return GEMM_ERR_INVALID;
+  if (!is16(p->in_dtype) || (p->tile == 32 && p->mode == GEMM_GROUPED_GRAD_B)) return GEMM_ERR_UNSUPPORTED;
+  const int64_t lim = (int64_t)1 << 20;
+  if (p->rows > kMax32 || p->experts > kMax32 || p->n > kMax32 || p->k > kMax32) return GEMM_ERR_UNSUPPORTED;
+  const bool gb = p->mode == GEMM_GROUPED_GRAD_B;
+  const int64_t xc = p->mode == GEMM_GROUPED_FORWARD ? p->k : p->n;
+  const int64_t oc = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
+  if (p->ldx < xc || p->ldy < p->k || p->ldo < oc) return GEMM_ERR_INVALID;
+  const int64_t mat_ld = gb ? p->ldo : p->ldy;  // of the [experts, n, k] tensor
+  if (p->experts > 1 && p->n > 0 && p->stride < (p->n - 1) * mat_ld + p->k) return GEMM_ERR_INVALID;
+  if (p->ldx >= lim || p->ldy >= lim || p->ldo >= lim) return GEMM_ERR_UNSUPPORTED;
+  s->x = Operand{p->rows, xc, p->ldx, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
+  if (gb) s->y = Operand{p->rows, p->k, p->ldy, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
+  else s->y = Operand{p->experts * p->n, p->k, p->ldy, p->n > 0 ? p->n : 1, p->stride, false, 0, 0, 0};
+  const int tile = p->tile ? p->tile : grouped_tile(p, cu);
+  s->tile = tile;
+  s->ws = 0;
+  Operand* ops[2] = {&s->x, &s->y};
+  const void* ptr[2] = {X, Y};
+  for (int i = 0; i < 2; ++i) {
+    Operand& o = *ops[i];
+    // the 256-row tiles load whole 16-byte chunks of rows that are multiples of them
+    o.pad = tile == 256 && ((uintptr_t)ptr[i] % 16 != 0 || o.cols % 8 != 0 || o.ld % 8 != 0 || o.stride % 8 != 0);
+    if (!o.pad) continue;
+    o.pad_ld = round_up(o.cols, 8);
+    o.at = s->ws;
+    o.bytes = round_up(o.rows * o.pad_ld * 2, 256);
+    s->ws += o.bytes;
+  }
+  return GEMM_OK;
 }
 
 gemm_status_t pad_operand(Operand& o, const void** ptr, char* ws, void* stream) {
@@ -330,7 +335,7 @@ gemm_status_t experts_combine_grad(const void* dout, int64_t lddo, const void* y
 gemm_status_t gemm_grouped_workspace_bytes(const gemm_grouped_t* p, const void* X, const void* Y, int64_t* out) {
   GroupedShape s;
   if (!out) return GEMM_ERR_INVALID;
-  const gemm_status_t st = grouped_shape(p, X, Y, &s);
+  const gemm_status_t st = grouped_shape(p, kCus, X, Y, &s);
   if (st == GEMM_OK) *out = s.ws;
   return st;
 }
@@ -338,7 +343,7 @@ gemm_status_t gemm_grouped_workspace_bytes(const gemm_grouped_t* p, const void* 
 gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const void* Y, void* out,
                                const int32_t* offsets, void* workspace, int64_t workspace_bytes, void* stream) {
   GroupedShape s;
-  gemm_status_t st = grouped_shape(p, X, Y, &s);
+  gemm_status_t st = grouped_shape(p, kCus, X, Y, &s);
   if (st != GEMM_OK) return st;
   const bool gb = p->mode == GEMM_GROUPED_GRAD_B, fwd = p->mode == GEMM_GROUPED_FORWARD;
   const int64_t out_n = fwd ? p->n : p->k;
@@ -351,8 +356,7 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   st = device_cus(&cu);
   if (st != GEMM_OK) return st;
 
-  const int tile = p->tile ? p->tile : grouped_tile(p, cu);
-  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, tile, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
+  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, s.tile, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
   const int64_t tiles_m = ceil_div(p->n, entry.bm), tiles_n = ceil_div(out_n, entry.bn);
   const int64_t units = gb ? p->experts * tiles_m * tiles_n
                            : spt::max_row_blocks(p->rows, p->experts, entry.bm) * tiles_n;

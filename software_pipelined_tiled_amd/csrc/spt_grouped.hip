@@ -13,6 +13,13 @@
 // expert's last lie past its descriptor's end and read as zeros, so ragged experts need no padding in
 // grad B's sum.
 //
+// Operands may start at any element and have rows of any length: a 16-byte load takes any byte offset. A
+// chunk that reaches past the end of a row contiguous in c holds the next row's elements, which the last
+// K-tile masks in both operands (0 * NaN is NaN); past the end of a row contiguous in i or j they meet only
+// columns that are not stored. The descriptor's check drops a dword that is not wholly inside: with an odd
+// row length it ends one element further, or, where that would lie past the operand itself, that one
+// element is put into LDS by hand.
+//
 // A persistent grid walks the output tiles of all experts; each unit looks its expert up from the
 // offsets (find_group), since the host does not know the counts. K-tiles of 64 stream through a ring
 // of S LDS stages by direct global->LDS loads; one barrier per K-tile.
@@ -102,19 +109,26 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
     const char* yb = a.Y + (MODE == kGroupedGradB ? ((int64_t)c0 * a.ldy + col0) * 2
                             : MODE == kGroupedGradA ? ((int64_t)e * a.sy + col0) * 2
                                                     : ((int64_t)e * a.sy + (int64_t)col0 * a.ldy) * 2);
+    // Odd row lengths: the descriptor ends one element further (more = 1), but in the tile that holds the
+    // operand's very last element (patch). In whole-number arithmetic, which stays in scalar registers.
+    auto at_most_1 = [](int v) SPT_INLINE { return v < 1 ? (v < 0 ? 0 : v) : 1; };
+    const int x_behind = MODE == kGroupedGradB ? a.rows - c0 - kc : a.rows - row0 - rows_left;
+    const int y_behind = MODE == kGroupedGradB ? a.rows - c0 - kc : a.experts - 1 - e;
+    const int x_more = (TX ? rows_left : kc) & (at_most_1(x_behind) | at_most_1(rows_left - BM));
+    const int y_more = (TY ? cols_left : kc) & (at_most_1(y_behind) | at_most_1(cols_left - BN));
+    const bool x_patch = ((TX ? rows_left : kc) & 1) != x_more, y_patch = ((TY ? cols_left : kc) & 1) != y_more;
     auto issue = [&](int kt) SPT_INLINE {
       const int k0 = kt * BK;
       const unsigned dst = lds0 + (unsigned)(kt % S) * STAGE;
       // K-tiles past the end read nothing and fill zeros, so every K-tile issues LW loads
-      auto rsrc = [&](bool tr, const char* base, int64_t ld, int rows, int width) SPT_INLINE {
-        const int64_t left = tr ? kc - k0 : rows;  // memory rows that may be read
-        // (memory rows hold a multiple of 8 elements, zeros past the operand's own; a chunk that the
-        // descriptor's end cut would read zeros as a whole)
-        const int64_t bytes = kc - k0 > 0 ? ((left - 1) * ld + (((tr ? width : kc) + 7) & ~7)) * 2 : 0;
-        return make_rsrc(base + (tr ? (int64_t)k0 * ld * 2 : 0), (uint64_t)(bytes > 0 ? bytes : 0));
+      auto rsrc = [&](bool tr, const char* base, int64_t ld, int rows, int width, int odd) SPT_INLINE {
+        const int some = kc > k0;
+        const int64_t left = some ? (tr ? kc - k0 : rows) : 1;  // memory rows that may be read
+        const int64_t bytes = ((left - 1) * ld + width + odd) * 2 * some;
+        return make_rsrc(base + (tr ? (int64_t)k0 * ld * 2 : 0), (uint64_t)bytes);
       };
-      const __amdgpu_buffer_rsrc_t rx = rsrc(TX, xb, a.ldx, rows_left, rows_left);
-      const __amdgpu_buffer_rsrc_t ry = rsrc(TY, yb, a.ldy, cols_left, cols_left);
+      const __amdgpu_buffer_rsrc_t rx = rsrc(TX, xb, a.ldx, rows_left, TX ? rows_left : kc, x_more);
+      const __amdgpu_buffer_rsrc_t ry = rsrc(TY, yb, a.ldy, cols_left, TY ? cols_left : kc, y_more);
 #pragma unroll
       for (int j = 0; j < LX; ++j) {
         const unsigned v = x_off(j);
@@ -134,30 +148,77 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
       for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     const int kt = (kc + BK - 1) / BK;
+    // K-tile k's products, from its stage. kCut: the K-tile reaches past kc, whose elements from there on are
+    // masked in operands contiguous in c.
+    auto products = [&](int k, auto cut_c) SPT_INLINE {
+      constexpr bool kCut = decltype(cut_c)::value;
+      const char* xt = smem + (k % S) * STAGE;
+      const char* yt = xt + XB;
+#pragma unroll
+      for (int s = 0; s < BK / 32; ++s) {
+        u32x4 xf[FM], yf[FN];
+#pragma unroll
+        for (int f = 0; f < FN; ++f) yf[f] = read_y(yt, s, f);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) xf[f] = read_x(xt, s, f);
+        if constexpr (kCut) {
+          const int left = kc - k * BK - 32 * s - 8 * h;  // elements of the lane's eight that exist
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const unsigned keep = left >= 2 * w + 2 ? ~0u : (left == 2 * w + 1 ? 0xFFFFu : 0u);
+            if constexpr (!TY) {
+#pragma unroll
+              for (int f = 0; f < FN; ++f) yf[f][w] &= keep;
+            }
+            if constexpr (!TX) {
+#pragma unroll
+              for (int f = 0; f < FM; ++f) xf[f][w] &= keep;
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int j = 0; j < FM; ++j) acc[i][j] = mfma16<TIn>(yf[i], xf[j], acc[i][j]);
+      }
+    };
+    // an operand's very last element, which no load reaches (see the top), into its place in stage `st`
+    auto patch = [&](int st) SPT_INLINE {
+      const int c = kc - 1 - (kt - 1) * BK;
+      char* xt = smem + st * STAGE;
+      if (x_patch && threadIdx.x == 0) {
+        const int r = rows_left - 1;
+        const int64_t at = TX ? (int64_t)(kc - 1) * a.ldx + r : (int64_t)r * a.ldx + kc - 1;
+        const int o = TX ? tr_offset<TX ? BM : 128>(c, r >> 4) + 2 * (r & 15) : lds_chunk_offset(BM, r, c >> 3) + 2 * (c & 7);
+        *(unsigned short*)(xt + o) = *(const unsigned short*)(xb + 2 * at);
+      }
+      if (y_patch && threadIdx.x == 64) {
+        const int r = cols_left - 1;
+        const int64_t at = TY ? (int64_t)(kc - 1) * a.ldy + r : (int64_t)r * a.ldy + kc - 1;
+        // rows contiguous in c are staged in b_row_perm's order: LDS row 16 h + 4 g + i holds row 8 g + 4 h + i
+        const int lr = (r & ~31) + 16 * ((r >> 2) & 1) + 4 * ((r >> 3) & 3) + (r & 3);
+        const int o = TY ? tr_offset<BN>(c, r >> 4) + 2 * (r & 15) : lds_chunk_offset(BN, lr, c >> 3) + 2 * (c & 7);
+        *(unsigned short*)(xt + XB + o) = *(const unsigned short*)(yb + 2 * at);
+      }
+      wait_lgkmcnt0();
+      barrier_sync();
+    };
     wait_vmcnt<0>();  // the previous unit's loads past its end, and its stores
     barrier_sync();   // ... and everybody's reads of the ring
     if (kt > 0) {
 #pragma unroll
       for (int s = 0; s < S - 1; ++s) issue(s);
-      for (int k = 0; k < kt; ++k) {
+      for (int k = 0; k < kt - 1; ++k) {
         wait_vmcnt<(S - 2) * LW>();  // K-tile k has landed: only later ones in flight
         barrier_sync();              // for every wave; and K-tile k - 1 has been read by all
         issue(k + S - 1);
-        const char* xt = smem + (k % S) * STAGE;
-        const char* yt = xt + XB;
-#pragma unroll
-        for (int s = 0; s < BK / 32; ++s) {
-          u32x4 xf[FM], yf[FN];
-#pragma unroll
-          for (int f = 0; f < FN; ++f) yf[f] = read_y(yt, s, f);
-#pragma unroll
-          for (int f = 0; f < FM; ++f) xf[f] = read_x(xt, s, f);
-#pragma unroll
-          for (int i = 0; i < FN; ++i)
-#pragma unroll
-            for (int j = 0; j < FM; ++j) acc[i][j] = mfma16<TIn>(yf[i], xf[j], acc[i][j]);
-        }
+        products(k, std::false_type{});
       }
+      wait_vmcnt<(S - 2) * LW>();
+      barrier_sync();
+      if (x_patch || y_patch) patch((kt - 1) % S);
+      if ((!TX || !TY) && (kc & 7)) products(kt - 1, std::true_type{});
+      else products(kt - 1, std::false_type{});
     }
 
     const __amdgpu_buffer_rsrc_t rc = make_rsrc(
