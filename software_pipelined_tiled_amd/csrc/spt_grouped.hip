@@ -53,6 +53,9 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
   // load j of this wave: a lane's place in the operand tile. Contiguous in c: row and chunk of 8 c.
   // Contiguous in i or j: row c and chunk of 8 columns.
   const int n_kc = 8 * ((lane & 7) ^ swz(lane >> 3));
+  // Y's row in LDS row r. 16-bit outputs: b_row_perm, so that a lane ends up with 8 consecutive output
+  // columns per fragment pair, 16 bytes. fp32 outputs: as they lie; four consecutive columns are 16 bytes.
+  auto y_row = [](int r) SPT_INLINE { return OUT == 2 ? r : b_row_perm(r); };
   auto x_off = [&](int j) SPT_INLINE {
     const int q = wave * LX + j;
     if constexpr (!TX) return (unsigned)((8 * q + (lane >> 3)) * ldx + n_kc) * 2u;
@@ -63,15 +66,14 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
   };
   auto y_off = [&](int j) SPT_INLINE {
     const int q = wave * LY + j;
-    if constexpr (!TY) return (unsigned)(b_row_perm(8 * q + (lane >> 3)) * ldy + n_kc) * 2u;
+    if constexpr (!TY) return (unsigned)(y_row(8 * q + (lane >> 3)) * ldy + n_kc) * 2u;
     else {
       const int c = q * (512 / BN) + lane / (BN / 8), ch = (lane % (BN / 8)) ^ (2 * tr_swz<BN>(c));
       return (unsigned)(c * ldy + 8 * ch) * 2u;
     }
   };
 
-  // fragment f of k-step s. Rows of Y that are contiguous in c are staged in the order of b_row_perm, so
-  // that a lane ends up with 8 consecutive output columns per fragment pair.
+  // fragment f of k-step s
   auto read_x = [&](const char* t, int s, int f) SPT_INLINE -> u32x4 {
     if constexpr (!TX) return *(const u32x4*)(t + lds_chunk_offset(BM, wm * TM + 16 * f + p, 4 * s + h));
     else return tr_frag<2 * BM>(t + tr_offset<BM>(32 * s + 8 * h + (p >> 2), (wm * TM + 16 * f) / 16) + 8 * (p & 3));
@@ -195,8 +197,8 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
       if (y_patch && threadIdx.x == 64) {
         const int r = cols_left - 1;
         const int64_t at = TY ? (int64_t)(kc - 1) * a.ldy + r : (int64_t)r * a.ldy + kc - 1;
-        // rows contiguous in c are staged in b_row_perm's order: LDS row 16 h + 4 g + i holds row 8 g + 4 h + i
-        const int lr = (r & ~31) + 16 * ((r >> 2) & 1) + 4 * ((r >> 3) & 3) + (r & 3);
+        // b_row_perm's LDS row of row 8 g + 4 h + i is 16 h + 4 g + i
+        const int lr = OUT == 2 ? r : (r & ~31) + 16 * ((r >> 2) & 1) + 4 * ((r >> 3) & 3) + (r & 3);
         const int o = TY ? tr_offset<BN>(c, r >> 4) + 2 * (r & 15) : lds_chunk_offset(BN, lr, c >> 3) + 2 * (c & 7);
         *(unsigned short*)(xt + XB + o) = *(const unsigned short*)(yb + 2 * at);
       }
@@ -224,10 +226,24 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
     const __amdgpu_buffer_rsrc_t rc = make_rsrc(
         a.C + ((MODE == kGroupedGradB ? (int64_t)e * a.sc : 0) + (int64_t)row0 * a.ldc) * es,
         ((uint64_t)(rows_left - 1) * a.ldc + a.n) * es);
-#pragma unroll
-    for (int pu = 0; pu < FN / 2; ++pu) {
+    const bool full = rows_left >= BM && cols_left >= BN;
+    if constexpr (OUT == 2) {
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+          const int m = wm * TM + 16 * j + p, n = col0 + wn * TN + 16 * i + 4 * h;
+          if (full) store4_f32<false>(acc[i][j], rc, m, rows_left, n, a.n, ldc);
+          else store4_f32<true>(acc[i][j], rc, m, rows_left, n, a.n, ldc);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      continue;
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+#pragma unroll
+      for (int pu = 0; pu < FN / 2; ++pu) {
         float v[8];
         if constexpr (TY) {
           pair_columns(acc[2 * pu][j], acc[2 * pu + 1][j], v);
@@ -239,7 +255,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
           }
         }
         const int m = wm * TM + 16 * j + p, n = col0 + wn * TN + 32 * pu + (TY ? pair_column(lane) : 8 * h);
-        if (rows_left >= BM && cols_left >= BN) store8<OUT, false>(v, rc, m, rows_left, n, a.n, ldc);
+        if (full) store8<OUT, false>(v, rc, m, rows_left, n, a.n, ldc);
         else store8<OUT, true>(v, rc, m, rows_left, n, a.n, ldc);
         __builtin_amdgcn_sched_barrier(0);
       }

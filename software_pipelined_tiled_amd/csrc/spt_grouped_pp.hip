@@ -127,6 +127,12 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
   };
   auto valid = [&](const Cursor& c) SPT_INLINE { return c.tl.t >= 0; };
 
+  // Y's row in LDS row r, where Y is contiguous in c. 16-bit outputs: b_row_perm128. fp32 outputs: in each 64
+  // rows, LDS row 16 f + c holds row 4 c + f, so that a lane holds four consecutive columns per four
+  // fragments, 16 bytes, and a quarter-wave 256.
+  auto y_row = [](int r) SPT_INLINE {
+    return OUT == 2 ? (r & ~63) + 4 * (r & 15) + ((r >> 4) & 3) : b_row_perm128(r);
+  };
   struct OpLoads {
     __amdgpu_buffer_rsrc_t r;
     unsigned v0, lds, soff;  // v0: the lane's offset; contiguous in i or j: of its row alone
@@ -150,7 +156,7 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
       o.soff = 0;
     } else {
       o.r = x ? c.rx : c.ry;
-      const int row = x ? lrow : b_row_perm128(lrow);
+      const int row = x ? lrow : y_row(lrow);
       o.v0 = lane_kc < c.tl.kc - k0 ? (unsigned)(row * o.ld + lane_kc) * 2u : kOOB;
       o.soff = 2u * k0;
     }
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
       dma16_unseen(o.r, o.lds + j * 1024, xor_add_in_place(2u * tcol, 64u * (j & 1) + 128u * (j >> 2), o.v0),
                    (unsigned)(2 * q * o.ld) * 2u);
     } else {
-      const int row = x ? 8 * q : b_row_perm128(8 * q);
+      const int row = x ? 8 * q : y_row(8 * q);
       dma16_unseen(o.r, o.lds + j * 1024, add_in_place(o.v0, (unsigned)(row * o.ld) * 2u), o.soff);
     }
   };
@@ -276,8 +282,10 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
   };
 
   // ------------------------------------------------------------------------ stores
-  // Forward: store s is row 4 (l/16) + s%4 of X block s/4, columns 8 (l%16) .. +7. Gradients: store s is
-  // row l%16 of X block s%4, eight columns of Y block pair s/4.
+  // 16-bit outputs, 16 stores of eight columns. Forward: store s is row 4 (l/16) + s%4 of X block s/4, columns
+  // 8 (l%16) .. +7. Gradients: row l%16 of X block s/4, Y block pair s%4. fp32 outputs, 32 stores of four
+  // columns: half s%2 of a row (forward), or Y block s%8 (gradients). The stores that fill one 128-byte line
+  // follow each other: four apart, grad B ran 5 % (16-bit) and 12 % (fp32) slower.
   auto epilogue = [&](const PpUnit& in, auto reads_c, int p) SPT_INLINE {
     constexpr bool kReads = decltype(reads_c)::value;
     const int e = __builtin_amdgcn_readfirstlane(in.e), row0 = __builtin_amdgcn_readfirstlane(in.row0);
@@ -288,25 +296,39 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
                   ((uint64_t)(rows_left - 1) * args.ldc + args.n) * es);
     const int ln = (int)opaque_u32((unsigned)lane);
     const int m_lane = TY ? m_base + ln % 16 : m_base + 4 * (ln / 16);
-    const int n_lane = col0 + TN * wn + (TY ? pair_column(ln) : 8 * (ln % 16));
+    const int n_lane = col0 + TN * wn + (OUT == 2 ? 4 * (TY ? ln / 16 : ln % 16) : TY ? pair_column(ln) : 8 * (ln % 16));
     const unsigned voff = (unsigned)(m_lane * ldc + n_lane) * (unsigned)es;
+    constexpr int kPolicy = TY ? 0 : kStoreNonTemporal;
     auto stores = [&](auto edge_c) SPT_INLINE {
       constexpr bool kEdge = decltype(edge_c)::value;
       Bases b{};
       if constexpr (kReads) b = frag_bases(p);
-      constexpr int NS = 16;
+      constexpr int NS = OUT == 2 ? 32 : 16;
       static_for<NS>([&](auto s_c) {
         constexpr int st = decltype(s_c)::value;
-        constexpr int dm = TY ? 16 * (st % 4) : 16 * (st / 4) + st % 4, dn = TY ? 32 * (st / 4) : 0;
-        float vv[8];
-        if constexpr (TY) {
-          pair_columns(acc[2 * (st / 4)][st % 4], acc[2 * (st / 4) + 1][st % 4], vv);
-        } else {
+        if constexpr (OUT == 2) {
+          constexpr int j = st / 8, e = st / 2 % 4, half = st % 2;  // e, half: forward
+          constexpr int dm = TY ? 16 * j : 16 * j + e, dn = TY ? 16 * (st % 8) : 64 * half;
+          f32x4 v;
+          if constexpr (TY) v = acc[st % 8][j];
+          else {
 #pragma unroll
-          for (int f = 0; f < 8; ++f) vv[f] = acc[f][st / 4][st % 4];
+            for (int f = 0; f < 4; ++f) v[f] = acc[4 * half + f][j][e];
+          }
+          if constexpr (kEdge) store4_f32<true>(v, rc, m_lane + dm, rows_left, n_lane + dn, args.n, ldc);
+          else __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, voff, (unsigned)((dm * ldc + dn) * es), kPolicy);
+        } else {
+          constexpr int dm = TY ? 16 * (st / 4) : 16 * (st / 4) + st % 4, dn = TY ? 32 * (st % 4) : 0;
+          float vv[8];
+          if constexpr (TY) {
+            pair_columns(acc[2 * (st % 4)][st / 4], acc[2 * (st % 4) + 1][st / 4], vv);
+          } else {
+#pragma unroll
+            for (int f = 0; f < 8; ++f) vv[f] = acc[f][st / 4][st % 4];
+          }
+          if constexpr (kEdge) store8<OUT, true>(vv, rc, m_lane + dm, rows_left, n_lane + dn, args.n, ldc);
+          else store8_at<OUT, kPolicy>(vv, rc, voff, (unsigned)((dm * ldc + dn) * es));
         }
-        if constexpr (kEdge) store8<OUT, true>(vv, rc, m_lane + dm, rows_left, n_lane + dn, args.n, ldc);
-        else store8_at<OUT, TY ? 0 : kStoreNonTemporal>(vv, rc, voff, (unsigned)((dm * ldc + dn) * es));
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (kReads) {
           static_for<NR>([&](auto r_c) {

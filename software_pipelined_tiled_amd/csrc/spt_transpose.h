@@ -72,4 +72,23 @@ __device__ __forceinline__ void pair_columns(const f32x4& lo, const f32x4& hi, f
 }
 __device__ __forceinline__ int pair_column(int lane) { return 16 * ((lane >> 4) & 1) + 8 * (lane >> 5); }
 
+// Four consecutive fp32 outputs at row m (relative to the descriptor's first), column n. Lanes whose
+// columns follow each other write 64 or 256 contiguous bytes per store; the eight columns a lane holds for a
+// 16-bit output would be two stores with 16-byte gaps, at half the rate. EDGE as in store8.
+template <bool EDGE>
+__device__ __forceinline__ void store4_f32(const f32x4& v, __amdgpu_buffer_rsrc_t rc, int m, int rows_left, int n, int N,
+                                           int ldc) {
+  if (EDGE && (m >= rows_left || n >= N)) return;
+  const unsigned off = (unsigned)(m * ldc + n) * 4u;
+  if (!EDGE || n + 4 <= N) {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rc, off, 0, 0);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float f = v[e];
+      if (n + e < N) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, f), rc, off + 4u * e, 0, 0);
+    }
+  }
+}
+
 }  // namespace spt
