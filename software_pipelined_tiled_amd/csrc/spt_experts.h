@@ -129,6 +129,7 @@ struct GroupedArgs {
   int group_m;
   int grid;
   int rest;              // zero the output rows behind the last expert
+  int nt;                // gradients, 256-row tiles: non-temporal stores
 };
 
 struct PadArgs {

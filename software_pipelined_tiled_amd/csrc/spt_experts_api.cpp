@@ -388,6 +388,10 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   a.group_m = 8;
   a.grid = (int)grid;
   a.rest = p->zero_rest != 0;
+  // Short sums write as fast as HBM takes it, and non-temporal stores are taken faster (8190 rows, 16
+  // experts, 4096 x 2048: fp32 258 -> 224 us, bf16 188 -> 159); among long ones they only leave the caches
+  // (16384 rows, 8 experts, 8192 x 4096: 886 -> 917).
+  a.nt = (gb ? ceil_div(p->rows, p->experts) : a.kc) < 1024;
   return launch(entry.fn, dim3((unsigned)grid), entry.threads, 0, &a, stream);
 }
 

@@ -298,9 +298,10 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
     const int m_lane = TY ? m_base + ln % 16 : m_base + 4 * (ln / 16);
     const int n_lane = col0 + TN * wn + (OUT == 2 ? 4 * (TY ? ln / 16 : ln % 16) : TY ? pair_column(ln) : 8 * (ln % 16));
     const unsigned voff = (unsigned)(m_lane * ldc + n_lane) * (unsigned)es;
-    constexpr int kPolicy = TY ? 0 : kStoreNonTemporal;
-    auto stores = [&](auto edge_c) SPT_INLINE {
-      constexpr bool kEdge = decltype(edge_c)::value;
+    // 0: interior, non-temporal; 1: interior, default policy; 2: edge tile, masked per element
+    auto stores = [&](auto mode_c) SPT_INLINE {
+      constexpr bool kEdge = decltype(mode_c)::value == 2;
+      constexpr int kPolicy = decltype(mode_c)::value == 0 ? kStoreNonTemporal : 0;
       Bases b{};
       if constexpr (kReads) b = frag_bases(p);
       constexpr int NS = OUT == 2 ? 32 : 16;
@@ -338,8 +339,9 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
       });
       if constexpr (kReads) wait_lgkmcnt0();
     };
-    if (rows_left >= BM && cols_left >= BN) stores(std::false_type{});
-    else stores(std::true_type{});
+    if (rows_left < BM || cols_left < BN) stores(std::integral_constant<int, 2>{});
+    else if (!TY || args.nt) stores(std::integral_constant<int, 0>{});
+    else stores(std::integral_constant<int, 1>{});
   };
   using t_ = std::true_type;
   using f_ = std::false_type;
