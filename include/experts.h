@@ -96,9 +96,9 @@ typedef struct {
 /*
  * fp32 sums, rounded once. GRAD_B writes every expert's gradient, zeros for one without rows. The
  * sums run in a fixed order: results do not change from run to run.
- *   The kernels load 16-byte chunks; an operand whose base, row length, leading dimension or expert
- * stride is not a multiple of 16 bytes is first copied to padded rows in the workspace. The output
- * needs only its element's alignment.
+ *   Any element alignment and row length will do. The 256-row tiles want whole 16-byte chunks: where they
+ * are chosen, an operand whose base, row length, leading dimension or expert stride is not a multiple of
+ * 16 bytes is first copied to padded rows in the workspace.
  * Errors: GEMM_ERR_INVALID (null pointer, bad enum, negative size, ld or stride too small, workspace
  *         too small), GEMM_ERR_UNSUPPORTED (types; rows beyond 2^31 - 1; more than 2^31 - 1 output
  *         tiles; a leading dimension of 2^20 elements or more), GEMM_ERR_HIP.

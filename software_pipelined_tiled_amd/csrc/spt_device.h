@@ -90,6 +90,16 @@ __device__ __forceinline__ void dma16_unseen(__amdgpu_buffer_rsrc_t r, unsigned 
                : "memory", "m0");
 }
 
+// The same with the non-temporal hint, for an operand whose every byte one workgroup reads once.
+__device__ __forceinline__ void dma16_unseen_stream(__amdgpu_buffer_rsrc_t r, unsigned lds, unsigned voffset,
+                                                    unsigned soffset) {
+  const unsigned m0 = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen nt lds"
+               :
+               : "s"(m0), "v"(voffset), "s"(r), "s"(soffset)
+               : "memory", "m0");
+}
+
 // v + c (c wave-uniform), computed where it is written: the compiler may not hoist it, so a loop
 // that issues many loads keeps one temporary instead of one precomputed register per load.
 __device__ __forceinline__ unsigned add_in_place(unsigned v, unsigned c) {

@@ -144,8 +144,8 @@ struct GroupedEntry {
   const void* fn;
   int bm, bn, threads, per_cu;
 };
-// tile: rows of an output tile, 32 (not grad B), 128 or 256
-GroupedEntry grouped_entry(int mode, int tile, int bf16, int out);
+// tile: rows of an output tile, 32 (not grad B), 128 or 256; deep: the 32-row tile's longer ring, Y streamed
+GroupedEntry grouped_entry(int mode, int tile, bool deep, int bf16, int out);
 GroupedEntry grouped_pp_entry(int mode, int bf16, int out);
 
 // ------------------------------------------------------------------------------ 4-bit weights

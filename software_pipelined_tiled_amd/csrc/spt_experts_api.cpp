@@ -101,9 +101,10 @@ struct GroupedShape {
 };
 
 // Rows of an output tile. Few rows per expert: 32, so that reading B is all there is to do. Else the
-// tile with the shorter time: rounds of tiles over the compute units, times K-tiles (and about two more
-// for the stores), times what a K-tile costs a compute unit.
-int grouped_tile(const gemm_grouped_t* p, int cu) {
+// tile with the shorter time in us: rounds of tiles over the compute units, times K-tiles (and about two
+// more for the stores), times what a K-tile takes. 256-row tiles copy an operand that is off 16 bytes
+// first; 128-row tiles load it as it lies, a tenth slower.
+int grouped_tile(const gemm_grouped_t* p, int cu, const Operand* const (&ops)[2], const bool (&off)[2]) {
   const bool gb = p->mode == GEMM_GROUPED_GRAD_B;
   const int64_t e = p->experts > 0 ? p->experts : 1;
   const int64_t each = ceil_div(p->rows, e);
@@ -115,7 +116,10 @@ int grouped_tile(const gemm_grouped_t* p, int cu) {
     const int64_t rb = gb ? e * ceil_div(p->n, bm) : (2 * p->rows + e * bm) / (2 * bm) + 1;
     return (double)ceil_div(rb * ceil_div(out_n, bm), slots) * kt * per_k_tile;
   };
-  return cost(256, cu, 1.5) <= cost(128, 2 * (int64_t)cu, 1.1) ? 256 : 128;
+  double copy = 0;
+  for (int i = 0; i < 2; ++i)
+    if (off[i]) copy += 3 + (double)ops[i]->rows * (double)ops[i]->cols * 4 / 4.5e6;  // read and written at 4.5 TB/s
+  return cost(256, cu, 1.5) + copy <= cost(128, 2 * (int64_t)cu, copy > 0 ? 1.2 : 1.1) ? 256 : 128;
 }
 
 gemm_status_t grouped_shape(const gemm_grouped_t* p, int cu, const void* X, const void* Y, GroupedShape* s) {
@@ -136,15 +140,16 @@ gemm_status_t grouped_shape(const gemm_grouped_t* p, int cu, const void* X, cons
   s->x = Operand{p->rows, xc, p->ldx, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
   if (gb) s->y = Operand{p->rows, p->k, p->ldy, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
   else s->y = Operand{p->experts * p->n, p->k, p->ldy, p->n > 0 ? p->n : 1, p->stride, false, 0, 0, 0};
-  const int tile = p->tile ? p->tile : grouped_tile(p, cu);
-  s->tile = tile;
   s->ws = 0;
-  Operand* ops[2] = {&s->x, &s->y};
+  Operand* const ops[2] = {&s->x, &s->y};
   const void* ptr[2] = {X, Y};
+  bool off[2];  // not in rows of whole 16-byte chunks
+  for (int i = 0; i < 2; ++i)
+    off[i] = (uintptr_t)ptr[i] % 16 != 0 || ops[i]->cols % 8 != 0 || ops[i]->ld % 8 != 0 || ops[i]->stride % 8 != 0;
+  s->tile = p->tile ? p->tile : grouped_tile(p, cu, {ops[0], ops[1]}, off);
   for (int i = 0; i < 2; ++i) {
     Operand& o = *ops[i];
-    // the 256-row tiles load whole 16-byte chunks of rows that are multiples of them
-    o.pad = tile == 256 && ((uintptr_t)ptr[i] % 16 != 0 || o.cols % 8 != 0 || o.ld % 8 != 0 || o.stride % 8 != 0);
+    o.pad = s->tile == 256 && off[i];
     if (!o.pad) continue;
     o.pad_ld = round_up(o.cols, 8);
     o.at = s->ws;
@@ -356,7 +361,14 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   st = device_cus(&cu);
   if (st != GEMM_OK) return st;
 
-  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, s.tile, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
+  // 32-row tiles: with at most two of them for every compute unit, two workgroups with six stages in flight
+  // (64 rows, 8 experts, 4096^2: 44 us against 57 with three of four stages); with more, a third workgroup
+  // saves a round (200 rows: 59 against 77). The hint keeps B, which is read once then, out of the caches;
+  // without 16-byte rows neighbouring loads share lines, and it costs (2044 columns: 56 us against 49).
+  const int64_t blocks = p->rows / 32 + (p->experts < p->rows ? p->experts : p->rows);
+  const bool deep = s.tile == 32 && blocks * ceil_div(out_n, 64) <= 2 * (int64_t)cu && (uintptr_t)Y % 16 == 0 &&
+                    p->k % 8 == 0 && p->ldy % 8 == 0;
+  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, s.tile, deep, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
   const int64_t tiles_m = ceil_div(p->n, entry.bm), tiles_n = ceil_div(out_n, entry.bn);
   const int64_t units = gb ? p->experts * tiles_m * tiles_n
                            : spt::max_row_blocks(p->rows, p->experts, entry.bm) * tiles_n;

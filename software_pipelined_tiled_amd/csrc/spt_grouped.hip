@@ -29,8 +29,9 @@
 
 namespace spt {
 
-// MODE: kGroupedForward .. ; a WM x WN grid of waves; S stages; MINW: workgroups per CU to fit.
-template <int MODE, int BM, int BN, int WM, int WN, int S, int PER_CU, typename TIn, int OUT>
+// MODE: kGroupedForward .. ; a WM x WN grid of waves; S stages; PER_CU: workgroups per CU to fit; STREAM: Y
+// loaded with the non-temporal hint.
+template <int MODE, int BM, int BN, int WM, int WN, int S, int PER_CU, bool STREAM, typename TIn, int OUT>
 __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_kernel(GroupedArgs a) {
   constexpr bool TX = MODE == kGroupedGradB, TY = MODE != kGroupedForward;
   constexpr int W = WM * WN, BK = 64;
@@ -139,7 +140,9 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
 #pragma unroll
       for (int j = 0; j < LY; ++j) {
         const unsigned v = y_off(j);
-        dma16_unseen(ry, dst + XB + (wave * LY + j) * 1024, TY || n_kc < kc - k0 ? v : kOOB, TY ? 0u : 2u * k0);
+        const unsigned at = dst + XB + (wave * LY + j) * 1024, voff = TY || n_kc < kc - k0 ? v : kOOB;
+        if constexpr (STREAM) dma16_unseen_stream(ry, at, voff, TY ? 0u : 2u * k0);
+        else dma16_unseen(ry, at, voff, TY ? 0u : 2u * k0);
       }
     };
 
@@ -289,23 +292,25 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(PadArgs a) {
 const void* pad_rows_fn() { return (const void*)&pad_rows_kernel; }
 
 // ------------------------------------------------------------------------------ instantiations
-template <int MODE, int BM, int BN, int WM, int WN, int S, int PER_CU>
+template <int MODE, int BM, int BN, int WM, int WN, int S, int PER_CU, bool STREAM = false>
 static GroupedEntry grouped_pick(int bf16, int out) {
   GroupedEntry e{nullptr, BM, BN, 64 * WM * WN, PER_CU};
-#define SPT_GROUPED(TI, O) (const void*)&grouped_kernel<MODE, BM, BN, WM, WN, S, PER_CU, TI, O>
+#define SPT_GROUPED(TI, O) (const void*)&grouped_kernel<MODE, BM, BN, WM, WN, S, PER_CU, STREAM, TI, O>
   static const void* const fn[2][3] = {{SPT_GROUPED(_Float16, 0), SPT_GROUPED(_Float16, 1), SPT_GROUPED(_Float16, 2)},
                                        {SPT_GROUPED(__bf16, 0), SPT_GROUPED(__bf16, 1), SPT_GROUPED(__bf16, 2)}};
 #undef SPT_GROUPED
   e.fn = fn[bf16][out];
   return e;
 }
-GroupedEntry grouped_entry(int mode, int tile, int bf16, int out) {
+GroupedEntry grouped_entry(int mode, int tile, bool deep, int bf16, int out) {
   if (tile == 256) return grouped_pp_entry(mode, bf16, out);
   if (mode == kGroupedForward)
     return tile == 128 ? grouped_pick<kGroupedForward, 128, 128, 2, 2, 2, 2>(bf16, out)
+           : deep      ? grouped_pick<kGroupedForward, 32, 64, 2, 2, 6, 2, true>(bf16, out)
                        : grouped_pick<kGroupedForward, 32, 64, 2, 2, 4, 3>(bf16, out);
   if (mode == kGroupedGradA)
     return tile == 128 ? grouped_pick<kGroupedGradA, 128, 128, 2, 2, 2, 2>(bf16, out)
+           : deep      ? grouped_pick<kGroupedGradA, 32, 64, 2, 2, 6, 2, true>(bf16, out)
                        : grouped_pick<kGroupedGradA, 32, 64, 2, 2, 4, 3>(bf16, out);
   return grouped_pick<kGroupedGradB, 128, 128, 2, 2, 2, 2>(bf16, out);
 }

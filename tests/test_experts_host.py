@@ -108,18 +108,22 @@ def test_grouped_shapes(change, status):
 
 
 def test_grouped_workspace_is_for_operands_off_sixteen_bytes():
+    # only the 256-row tiles copy an operand; the others load any alignment
     def ws(x=A, y=A, **change):
-        return _lib.gemm_grouped_workspace_bytes(grouped(**change), x, y)
+        return _lib.gemm_grouped_workspace_bytes(grouped(**{"tile": 256, **change}), x, y)
     assert ws() == 0
     assert ws(x=A + 2) == 64 * 48 * 2                      # A copied
+    assert ws(x=A + 2, tile=128) == ws(x=A + 2, tile=32) == 0
     assert ws(y=A + 8) == 4 * 32 * 48 * 2                  # B copied
     assert ws(ldx=50) == 64 * 48 * 2
     assert ws(k=45, ldx=45, ldy=45, stride=32 * 45) == (64 + 4 * 32) * 48 * 2  # rows of 45 padded to 48
     assert ws(mode=2, ldx=33, n=33, ldo=48, stride=33 * 48) == 64 * 40 * 2
+    # the library's choice: a large B is not copied for a few rows
+    assert ws(tile=0, rows=5000, experts=64, n=1409, k=2044, ldx=2044, ldy=2044, ldo=1409, stride=1409 * 2044) == 0
 
 
 def test_grouped_run_refusals():
-    L, p = spt.lib(), grouped()
+    L, p = spt.lib(), grouped(tile=256)
     assert L.gemm_grouped_run(None, A, A, A, A, None, 0, None) == INVALID
     assert L.gemm_grouped_run(ctypes.byref(p), None, A, A, A, None, 0, None) == INVALID
     assert L.gemm_grouped_run(ctypes.byref(p), A, None, A, A, None, 0, None) == INVALID
