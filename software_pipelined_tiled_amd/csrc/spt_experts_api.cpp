@@ -188,26 +188,38 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
   if (p->n > lim || p->k > lim || p->ldx >= lim / 2 || p->rows > kMax32 || p->matrices > kMax32)
     return GEMM_ERR_UNSUPPORTED;
   const int64_t n16 = ceil_div(p->n, 16), kb = ceil_div(p->k, 128);
-  // Rows that share a matrix, on average, decide how many 16-row blocks a workgroup takes, and the
-  // number of 16-column blocks how many of those. More columns a workgroup reuse each load of x, fewer
-  // keep every compute unit busy. One row of 8192 x 8192 (512 column blocks): 2 columns 9.6 us, 1 11.1,
-  // 4 13.8; 16 rows of 28672 x 8192: 4 columns 35 us, 2 43, 1 58; one row of 1024 x 8192: 1 column 6.3
-  // us, 2 6.8. 64 rows of 8192 x 8192: 32-row workgroups 23 us, 64-row ones 27; 512 rows: 159 and 139 us.
-  const int64_t each = p->matrices > 0 ? ceil_div(p->rows, p->matrices) : 0;
-  const int64_t cols = n16 * (each <= 16 ? (p->rows < p->matrices ? p->rows : p->matrices) : 1);
-  const int variant = each > 64 ? 4 : each > 16 ? 3 : cols < 384 ? 0 : cols < 1536 || each <= 2 ? 1 : 2;
+  // The kernel goes by the work: u 16 x 16 blocks of output. Few: one wave's K slices of one column block or
+  // two, straight from memory, which spreads best; from about 1000 blocks on the waves share x in LDS, in
+  // tiles that grow with u (short sums of few rows: fewer K parts, variant 6: 256 rows over 16 experts of 4096 x
+  // 2048 20.6 us against 27.1). us with bf16, G = 128, for variants 0 .. 5:
+  //   8192 x 8192, 1 row (u 512, weights bound)   13.0  10.3  12.9  14.2  15.6  18.8
+  //   4096 x 4096, 1 row (u 256)                   5.0   6.8   8.5   9.5  10.0  12.0
+  //   8192 x 8192, 32 rows (u 1024)               34.1  21.2  17.3  18.2  18.6  21.0
+  //   4096 x 4096, 128 rows (u 2048)              33.4  20.4  16.6  13.6  17.2  19.4
+  //   4096 x 4096, 256 rows (u 4096)              63.4  36.9  30.2  24.8  20.5  24.9
+  //   8192 x 8192, 512 rows (u 16384)            486.5 284.8 226.1 169.8 124.8  99.6
+  const int64_t each = p->matrices > 0 ? ceil_div(p->rows, p->matrices) : 0;  // rows that share a matrix, on average
+  const int64_t used = p->rows < p->matrices ? p->rows : p->matrices;
+  const int64_t u = n16 * used * ceil_div(each, 16);
+  const int variant = u <= 256               ? 0
+                      : u <= 768 || each <= 4   ? 1
+                      : each <= 16 && kb <= 16  ? 6
+                      : u <= 1100 || each <= 16 ? 2
+                      : u <= 3584               ? 3
+                      : u <= 8000               ? 4
+                                                : 5;
   s->entry = spt::w4_entry(variant, p->dtype == GEMM_BF16, 128 / p->group, p->has_zeros != 0);
   const int bm = 16 * s->entry.mt;
   s->nblocks = ceil_div(n16, s->entry.nt);
   s->row_blocks = grouped ? spt::max_row_blocks(p->rows, p->matrices, bm) : ceil_div(p->rows, bm);
   if (s->row_blocks > 65535) return GEMM_ERR_UNSUPPORTED;
   const int64_t wgs = s->nblocks * s->row_blocks;
-  // cut K when the workgroups alone would not occupy every compute unit
+  // Cut K when the workgroups alone leave compute units idle, into as many parts as still run at once: one
+  // workgroup more than compute units is a second round.
   s->splits = 1;
   if (wgs > 0 && wgs < cu) {
     const int64_t most = kb / s->entry.waves;
-    s->splits = ceil_div(cu, wgs);
-    if (s->splits > most) s->splits = most;
+    s->splits = cu / wgs < most ? cu / wgs : most;
     if (s->splits < 1) s->splits = 1;
   }
   s->ws = s->splits > 1 ? s->splits * p->rows * p->n * 4 : 0;

@@ -112,9 +112,42 @@ __device__ __forceinline__ u32x4 unpack(unsigned w, const ZeroF32& z) {
 }
 
 template <int T>
+__device__ __forceinline__ auto zero_of(unsigned z) {
+  if constexpr (T == 1) {
+    const float f = (float)z;
+    return ZeroF32{-1024.f - f, -64.f - f};
+  } else {
+    const unsigned p = z | z << 16;
+    return ZeroF16{0xE400E400u + p, 0xD400D400u + (p << 4)};
+  }
+}
+template <int T>
 __device__ __forceinline__ float scale_of(unsigned s) {
   if constexpr (T == 1) return __builtin_bit_cast(float, s << 16);
   else return (float)__builtin_bit_cast(_Float16, (unsigned short)s);
+}
+
+constexpr int kLoadNonTemporal = 2;  // cache policy: the weights are read once
+
+// B bytes (1, 2, 4 or 8) of a lane
+template <int B>
+__device__ __forceinline__ auto load_groups(__amdgpu_buffer_rsrc_t r, int voff, int soff) {
+  if constexpr (B == 8) return __builtin_bit_cast(uint64_t, __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0));
+  else if constexpr (B == 4) return __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+  else if constexpr (B == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, voff, soff, 0);
+  else return __builtin_amdgcn_raw_buffer_load_b8(r, voff, soff, 0);
+}
+
+// The lane's chunk of eight x at byte offset voff + soff, of which `left` exist; the rest are zeros. A chunk
+// that K cuts is put together from its elements, eight loads at once and no branch (one behind the other
+// they made the last block take longer than all others).
+__device__ __forceinline__ u32x4 load_cut(__amdgpu_buffer_rsrc_t r, unsigned voff, int soff, int left, bool whole) {
+  if (whole) return __builtin_amdgcn_raw_buffer_load_b128(r, left > 0 ? voff : kOOB, soff, 0);
+  unsigned v[8];
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+    v[m] = (unsigned short)__builtin_amdgcn_raw_buffer_load_b16(r, m < left ? voff + 2 * m : kOOB, soff, 0);
+  return u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
 }
 
 // out: 0 fp16, 1 bf16, 2 fp32 (the same for a whole launch)
@@ -158,10 +191,13 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
 #pragma unroll
   for (int i = 0; i < MT; ++i) xo[i] = 16 * i + c < rows ? (unsigned)((16 * i + c) * (int)a.ldx + 8 * h) * 2u : kOOB;
 
+  // The weights from this wave's first column block on. A block's offset is wave-uniform and rides in the
+  // load's scalar offset: 64-bit lane addresses would cost vector instructions at every load.
   const int64_t block0 = ((int64_t)e * a.n16 + nb) * a.kb;
-  const char* wp = a.w + block0 * 1024 + lane * 16;
-  const char* sp = a.scales + block0 * (16 * GPK * 2) + c * (GPK * 2);
-  const char* zp = a.zeros + block0 * (16 * GPK) + c * GPK;
+  const uint64_t blocks = (uint64_t)(a.n16 - nb < NT ? a.n16 - nb : NT) * a.kb;
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + block0 * 1024, blocks * 1024);
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.scales + block0 * (32 * GPK), blocks * (32 * GPK));
+  const __amdgpu_buffer_rsrc_t rz = make_rsrc(a.zeros + block0 * (16 * GPK), blocks * (16 * GPK));
   // the workgroup's last columns may have fewer than NT blocks: the missing ones repeat the last
   int nstep[NT];
 #pragma unroll
@@ -179,10 +215,10 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
   auto fetch_w = [&](Stage& st, int kb) SPT_INLINE {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int64_t b = nstep[j] + kb;
-      st.q[j] = __builtin_nontemporal_load((const u32x4*)(wp + b * 1024));
-      st.s[j] = *(const GroupBits*)(sp + b * (16 * GPK * 2));
-      if constexpr (ZERO) st.z[j] = *(const ZeroBits*)(zp + b * (16 * GPK));
+      const int b = nstep[j] + kb;
+      st.q[j] = __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16, b * 1024, kLoadNonTemporal);
+      st.s[j] = load_groups<2 * GPK>(rs, c * (2 * GPK), b * (32 * GPK));
+      if constexpr (ZERO) st.z[j] = (ZeroBits)load_groups<GPK>(rz, c * GPK, b * (16 * GPK));
     }
   };
   auto fetch = [&](Stage& st, int kb) SPT_INLINE {
@@ -192,27 +228,14 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) st.x[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rx, xo[i], 2 * (kb * 128 + s * 32), 0);
   };
-  // the last block of a K that is no multiple of 128: chunks of x past K are zeros, one that K cuts is
-  // put together from its elements
+  // the last block of a K that is no multiple of 128
   auto fetch_cut = [&](Stage& st, int kb) SPT_INLINE {
     fetch_w(st, kb);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int k0 = kb * 128 + s * 32, left = a.k - k0 - 8 * h;
+      const int k0 = kb * 128 + s * 32;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        u32x4 r = {0, 0, 0, 0};
-        if (left >= 8) {
-          r = __builtin_amdgcn_raw_buffer_load_b128(rx, xo[i], 2 * k0, 0);
-        } else {
-#pragma unroll
-          for (int m = 0; m < 7; ++m)
-            if (m < left)
-              r[m >> 1] |= (unsigned)(unsigned short)__builtin_amdgcn_raw_buffer_load_b16(rx, xo[i] + 2 * m, 2 * k0, 0)
-                           << (16 * (m & 1));
-        }
-        st.x[s][i] = r;
-      }
+      for (int i = 0; i < MT; ++i) st.x[s][i] = load_cut(rx, xo[i], 2 * k0, a.k - k0 - 8 * h, (a.k & 7) == 0);
     }
   };
 
@@ -227,15 +250,7 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int g = 0; g < GPK; ++g) {
-        const unsigned zz = ZERO ? (unsigned)(st.z[j] >> (8 * g)) & 0xFFu : 8u;
-        std::conditional_t<T == 1, ZeroF32, ZeroF16> z;
-        if constexpr (T == 1) {
-          const float f = (float)zz;
-          z = ZeroF32{-1024.f - f, -64.f - f};
-        } else {
-          const unsigned p = zz | zz << 16;
-          z = ZeroF16{0xE400E400u + p, 0xD400D400u + (p << 4)};
-        }
+        const auto z = zero_of<T>(ZERO ? (unsigned)(st.z[j] >> (8 * g)) & 0xFFu : 8u);
         f32x4 sum[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -313,6 +328,198 @@ __global__ void __launch_bounds__(64 * W) w4_kernel(W4Args a) {
   }
 }
 
+// The same product with more rows: the waves of a workgroup split its columns (WN) and the blocks of K
+// (WK), and share x. An x fragment costs as much of the load path as a wave's whole block of weights, so
+// each is loaded once for WN waves, a block ahead, into registers and from there into one of two LDS
+// buffers, in the order the matrix instruction wants it (lane-contiguous, no bank conflicts).
+template <int T, int MT, int NT, int WN, int WK, int GPK, bool ZERO>
+__global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
+  using TIn = std::conditional_t<T == 1, __bf16, _Float16>;
+  using GroupBits = std::conditional_t<GPK == 4, uint64_t, std::conditional_t<GPK == 2, unsigned, unsigned short>>;
+  using ZeroBits = std::conditional_t<GPK == 4, unsigned, std::conditional_t<GPK == 2, unsigned short, unsigned char>>;
+  constexpr int BM = 16 * MT, W = WN * WK;
+  constexpr int NX = 4 * MT / WN;  // x fragments a wave loads per block
+  constexpr int XBUF = WK * 4 * MT * 1024, RED = W * MT * NT * 1024;
+  static_assert(4 * MT % WN == 0, "the waves of a block load the same number of fragments");
+  __shared__ __attribute__((aligned(16))) char lds[2 * XBUF > RED ? 2 * XBUF : RED];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wk = wave / WN, wn = wave % WN;
+  const int c = lane & 15, h = lane >> 4;
+  const int nblocks = (a.n16 + NT * WN - 1) / (NT * WN);
+  const int col16 = (int)(blockIdx.x % (unsigned)nblocks) * (NT * WN), split = (int)(blockIdx.x / (unsigned)nblocks);
+  const int nb = col16 + wn * NT < a.n16 ? col16 + wn * NT : a.n16 - 1;  // this wave's first column block
+
+  int e = 0, row0 = (int)blockIdx.y * BM, rows = a.rows - row0;
+  if (a.offsets) {
+    const GroupBlock g = find_group(a.offsets, a.experts, a.rows, BM, 1, a.rest != 0, (int)blockIdx.y);
+    if (g.e < 0) return;
+    e = g.e;
+    row0 = g.begin + g.block * BM;
+    rows = g.end - row0;
+  }
+  rows = rows < BM ? rows : BM;
+  const bool none = a.offsets && e == a.experts;  // rows behind the last expert: zeros
+  const int per = (a.kb + a.splits - 1) / a.splits;
+  const int kb0 = split * per, kb1 = none ? kb0 : (kb0 + per < a.kb ? kb0 + per : a.kb);
+  const int kb_full = kb1 < (a.k >> 7) ? kb1 : a.k >> 7;
+
+  const __amdgpu_buffer_rsrc_t rx =
+      make_rsrc(a.x + (int64_t)row0 * a.ldx * 2, ((uint64_t)(rows - 1) * a.ldx + a.k) * 2);
+  // fragment i of this wave: matrix step f / MT, rows 16 (f % MT) .., f = wn * NX + i
+  unsigned xo[NX];
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    const int f = wn * NX + i, m = 16 * (f % MT) + c;
+    xo[i] = m < rows ? (unsigned)(m * (int)a.ldx + 32 * (f / MT) + 8 * h) * 2u : kOOB;
+  }
+  auto x_at = [&](int buf, int w, int f) SPT_INLINE { return lds + buf * XBUF + (w * 4 * MT + f) * 1024 + 16 * lane; };
+
+  // The weights from this wave's first column block on. A block's offset is wave-uniform and rides in the
+  // load's scalar offset: 64-bit lane addresses would cost vector instructions at every load.
+  const int64_t block0 = ((int64_t)e * a.n16 + nb) * a.kb;
+  const uint64_t blocks = (uint64_t)(a.n16 - nb < NT ? a.n16 - nb : NT) * a.kb;
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(a.w + block0 * 1024, blocks * 1024);
+  const __amdgpu_buffer_rsrc_t rs = make_rsrc(a.scales + block0 * (32 * GPK), blocks * (32 * GPK));
+  const __amdgpu_buffer_rsrc_t rz = make_rsrc(a.zeros + block0 * (16 * GPK), blocks * (16 * GPK));
+  int nstep[NT];  // column blocks past the last repeat it
+#pragma unroll
+  for (int j = 0; j < NT; ++j) nstep[j] = (nb + j < a.n16 ? j : a.n16 - 1 - nb) * a.kb;
+
+  struct Stage {
+    u32x4 q[NT];
+    GroupBits s[NT];
+    ZeroBits z[NT];
+  };
+  auto fetch_w = [&](Stage& st, int kb) SPT_INLINE {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int b = nstep[j] + kb;
+      st.q[j] = __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16, b * 1024, kLoadNonTemporal);
+      st.s[j] = load_groups<2 * GPK>(rs, c * (2 * GPK), b * (32 * GPK));
+      if constexpr (ZERO) st.z[j] = (ZeroBits)load_groups<GPK>(rz, c * GPK, b * (16 * GPK));
+    }
+  };
+
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // one block of weights with x from LDS buffer `buf`
+  auto compute = [&](const Stage& st, int buf, int w) SPT_INLINE {
+#pragma unroll
+    for (int g = 0; g < GPK; ++g) {
+      constexpr int SPG = 4 / GPK;  // matrix steps per group
+      u32x4 xf[SPG][MT];
+#pragma unroll
+      for (int s = 0; s < SPG; ++s)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) xf[s][i] = *(const u32x4*)x_at(buf, w, (g * SPG + s) * MT + i);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const auto z = zero_of<T>(ZERO ? (unsigned)(st.z[j] >> (8 * g)) & 0xFFu : 8u);
+        f32x4 sum[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < SPG; ++s) {
+          const u32x4 wf = unpack(st.q[j][g * SPG + s], z);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) sum[i] = mfma16<TIn>(xf[s][i], wf, sum[i]);
+        }
+        const float sc = scale_of<T>((unsigned)(st.s[j] >> (16 * g)) & 0xFFFFu);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(sum[i][r], sc, acc[i][j][r]);
+      }
+    }
+  };
+
+  const int n = kb_full - kb0 > 0 ? (kb_full - kb0 + WK - 1) / WK : 0;  // rounds of WK blocks
+  if (n > 0) {
+    // past the end: the last block again, loaded and not used, so that every round issues the same loads
+    auto block = [&](int i) SPT_INLINE {
+      const int b = kb0 + i * WK + wk;
+      return b < kb_full ? b : kb_full - 1;
+    };
+    u32x4 xs[NX];
+    auto fetch_x = [&](int i) SPT_INLINE {
+#pragma unroll
+      for (int f = 0; f < NX; ++f) xs[f] = __builtin_amdgcn_raw_buffer_load_b128(rx, xo[f], 2 * 128 * block(i), 0);
+    };
+    auto put_x = [&](int buf) SPT_INLINE {
+#pragma unroll
+      for (int f = 0; f < NX; ++f) *(u32x4*)x_at(buf, wk, wn * NX + f) = xs[f];
+    };
+    Stage st[2];
+    fetch_x(0);
+    fetch_w(st[0], block(0));
+    __builtin_amdgcn_sched_barrier(0);
+    put_x(0);
+    fetch_x(1);
+    fetch_w(st[1], block(1));
+    wait_lgkmcnt0();
+    barrier_sync();
+    for (int i = 0; i < n; i += 2) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        put_x(d ^ 1);  // round i + d + 1; its buffer was read in the round before this one
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_x(i + d + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        if (kb0 + (i + d) * WK + wk < kb_full) compute(st[d], d, wk);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_w(st[d], block(i + d + 2));
+        wait_lgkmcnt0();
+        barrier_sync();
+      }
+    }
+  }
+  if (kb_full < kb1 && kb_full >= kb0) {
+    // the last block of a K that is no multiple of 128, for the waves of K part 0
+    Stage st;
+    fetch_w(st, kb_full);
+    barrier_sync();
+    if (wk == 0) {
+#pragma unroll
+      for (int f = 0; f < NX; ++f) {
+        const int left = a.k - kb_full * 128 - 32 * ((wn * NX + f) / MT) - 8 * h;
+        const u32x4 r = load_cut(rx, xo[f], 2 * 128 * kb_full, left, (a.k & 7) == 0);
+        *(u32x4*)x_at(0, 0, wn * NX + f) = r;
+      }
+    }
+    wait_lgkmcnt0();
+    barrier_sync();
+    if (wk == 0) compute(st, 0, 0);
+  }
+
+  // the K parts' sums, added in their order; consecutive threads take consecutive columns
+  wait_lgkmcnt0();
+  barrier_sync();  // the buffers have been read
+  float* red = (float*)lds;
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) *(f32x4*)&red[((wk * MT + i) * WN * NT + wn * NT + j) * 256 + 4 * lane] = acc[i][j];
+  __syncthreads();
+  constexpr int COLS = 16 * NT * WN;
+  for (int t = threadIdx.x; t < BM * COLS; t += 64 * W) {
+    const int n_in = t % COLS, m = t / COLS;
+    const int col = col16 * 16 + n_in;
+    if (m >= rows || col >= a.n) continue;
+    const int at = ((m >> 4) * WN * NT + (n_in >> 4)) * 256 + 4 * ((n_in & 15) + 16 * ((m & 15) >> 2)) + (m & 3);
+    float v = red[at];
+#pragma unroll
+    for (int w = 1; w < WK; ++w) v += red[at + w * MT * WN * NT * 256];
+    if (a.splits > 1) ((float*)a.out)[split * a.plane + (int64_t)(row0 + m) * a.n + col] = v;
+    else put_one(a.out_dtype, a.out, (int64_t)(row0 + m) * a.ldo + col, v);
+  }
+}
+
 // out = the planes added in order, rounded once. With `kept`, rows from *kept on hold zeros or are
 // left alone.
 __global__ void __launch_bounds__(256) w4_reduce_kernel(W4ReduceArgs r) {
@@ -335,14 +542,24 @@ static W4Entry w4_pick_group(int gpk, bool zero) {
   else e.fn = zero ? (const void*)&w4_kernel<T, MT, NT, 4, true, W, D> : (const void*)&w4_kernel<T, MT, NT, 4, false, W, D>;
   return e;
 }
+template <int T, int MT, int NT, int WN, int WK>
+static W4Entry w4_pick_rows(int gpk, bool zero) {
+  W4Entry e{nullptr, MT, NT * WN, WN * WK};
+  if (gpk == 1) e.fn = zero ? (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 1, true> : (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 1, false>;
+  else if (gpk == 2) e.fn = zero ? (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 2, true> : (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 2, false>;
+  else e.fn = zero ? (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 4, true> : (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 4, false>;
+  return e;
+}
 template <int T>
 static W4Entry w4_pick(int variant, int gpk, bool zero) {
   switch (variant) {
     case 0: return w4_pick_group<T, 1, 1, 8, 4>(gpk, zero);
     case 1: return w4_pick_group<T, 1, 2, 8, 2>(gpk, zero);
-    case 2: return w4_pick_group<T, 1, 4, 8, 2>(gpk, zero);
-    case 3: return w4_pick_group<T, 2, 4, 8, 1>(gpk, zero);
-    default: return w4_pick_group<T, 4, 4, 4, 1>(gpk, zero);
+    case 2: return w4_pick_rows<T, 1, 1, 4, 4>(gpk, zero);
+    case 3: return w4_pick_rows<T, 2, 1, 4, 4>(gpk, zero);
+    case 4: return w4_pick_rows<T, 2, 2, 4, 2>(gpk, zero);
+    case 6: return w4_pick_rows<T, 1, 2, 4, 2>(gpk, zero);
+    default: return w4_pick_rows<T, 4, 2, 4, 2>(gpk, zero);
   }
 }
 W4Entry w4_entry(int variant, int bf16, int gpk, bool zero) {
