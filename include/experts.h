@@ -33,7 +33,7 @@ extern "C" {
  *   order   [slots]         sorted position -> slot
  *   rows    [slots]         slot -> sorted position, a permutation; the slot is kept exactly when its
  *                           position is below offsets[experts]
- * One kernel up to 8192 slots, two beyond (the workspace holds the workgroups' counts).
+ * One kernel up to 4096 slots, two beyond (the workspace holds the workgroups' counts).
  * Errors: GEMM_ERR_INVALID (sizes negative, a null pointer, id_bits not 32 or 64, workspace missing),
  *         GEMM_ERR_UNSUPPORTED (experts not in 1 .. 1024, slots beyond 2^31 - 1), GEMM_ERR_HIP.
  */

@@ -57,9 +57,10 @@ int stream_grid(int64_t threads) {
 }
 
 // ---------------------------------------------------------------------------------- sort
-// One workgroup sorts up to kSortOne slots by itself; beyond, each workgroup takes kSortBlock of them
+// One workgroup sorts up to kSortOne slots by itself (4096 slots of 64 experts: 6.7 us in one launch, 6.9 in
+// two; 8192: 10.5 against 6.9); beyond, each workgroup takes kSortBlock of them
 // (more when there would be over 256 workgroups, since each adds up every other's counts).
-constexpr int64_t kSortOne = 8192, kSortBlock = 4096;
+constexpr int64_t kSortOne = 4096, kSortBlock = 1024;
 struct SortShape {
   int64_t per_block, blocks;
 };
@@ -377,7 +378,8 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   // (64 rows, 8 experts, 4096^2: 44 us against 57 with three of four stages); with more, a third workgroup
   // saves a round (200 rows: 59 against 77). The hint keeps B, which is read once then, out of the caches;
   // without 16-byte rows neighbouring loads share lines, and it costs (2044 columns: 56 us against 49).
-  const int64_t blocks = p->rows / 32 + (p->experts < p->rows ? p->experts : p->rows);
+  const int64_t used = p->experts < p->rows ? p->experts : p->rows;
+  const int64_t blocks = used + (p->rows > 16 * used ? (p->rows - 16 * used) / 32 : 0);  // about
   const bool deep = s.tile == 32 && blocks * ceil_div(out_n, 64) <= 2 * (int64_t)cu && (uintptr_t)Y % 16 == 0 &&
                     p->k % 8 == 0 && p->ldy % 8 == 0;
   const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, s.tile, deep, p->in_dtype == GEMM_BF16, (int)p->out_dtype);

@@ -22,7 +22,7 @@ from .torch_api import dtype_code
 
 _16BIT = (torch.float16, torch.bfloat16)
 _FLOATS = (*_16BIT, torch.float32)
-_SORT_ONE = 8192  # slots that one workgroup sorts without a workspace
+_SORT_ONE = 4096  # slots that one workgroup sorts without a workspace
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 

@@ -73,8 +73,8 @@ def offsets_of(counts):
 # ------------------------------------------------------------------------------------------- sort
 
 @pytest.mark.parametrize("tokens,top_k,experts", [
-    (0, 2, 4), (1, 1, 1), (1, 8, 8), (63, 1, 3), (16, 4, 8), (65, 1, 64), (1000, 8, 127), (1024, 8, 128),
-    (8193, 1, 255), (4097, 6, 64), (5000, 2, 1), (9001, 3, 1024), (100003, 3, 8), (300000, 1, 511), (1 << 17, 8, 256)])
+    (0, 2, 4), (1, 1, 1), (1, 8, 8), (63, 1, 3), (16, 4, 8), (65, 1, 64), (1000, 8, 127), (1024, 4, 128), (1024, 8, 128),
+    (4096, 1, 255), (4097, 1, 255), (4097, 6, 64), (5000, 2, 1), (9001, 3, 1024), (100003, 3, 8), (300000, 1, 511), (1 << 17, 8, 256)])
 @pytest.mark.parametrize("dtype,skew", [(torch.int64, False), (torch.int32, True)])
 def test_sort(tokens, top_k, experts, dtype, skew):
     ids = ids_of(tokens, top_k, experts, tokens + experts, dtype=dtype, skew=skew)

@@ -32,7 +32,7 @@ def test_enum_values_match_the_header():
 
 
 @pytest.mark.parametrize("slots,experts,want", [
-    (0, 1, 0), (8192, 8, 0), (8193, 8, 3 * 9 * 4), (1 << 20, 1024, 256 * 1025 * 4), (2**31 - 1, 4, None)])
+    (0, 1, 0), (4096, 8, 0), (4097, 8, 5 * 9 * 4), (1 << 20, 1024, 256 * 1025 * 4), (2**31 - 1, 4, None)])
 def test_sort_workspace(slots, experts, want):
     got = spt._lib.experts_sort_workspace_bytes(slots, experts)
     if want is not None:
