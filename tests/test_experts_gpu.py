@@ -398,7 +398,9 @@ def w4_dense(q, s, z, group):
 
 
 W4_SHAPES = [(1, 1, 1), (1, 16, 128), (2, 17, 31), (5, 100, 33), (16, 64, 256), (17, 48, 1000), (1, 1024, 4096), (33, 40, 520),
-             (64, 130, 384), (65, 257, 129), (200, 96, 640), (3, 2056, 8190), (16, 16400, 256)]
+             (64, 130, 384), (65, 257, 129), (200, 96, 640), (3, 2056, 8190), (16, 16400, 256),
+             # one shape for each kernel the choice goes to as the output grows, with blocks of K that K cuts
+             (2, 4160, 200), (15, 17500, 2201), (40, 8000, 303), (130, 9000, 300), (300, 8001, 517), (70, 24000, 120)]
 
 
 @pytest.mark.parametrize("rows,n,k", W4_SHAPES)
@@ -422,8 +424,8 @@ def test_w4_exact_and_real(rows, n, k, dtype, group, zeros):
 
 
 @pytest.mark.parametrize("counts,rest", [([1, 0, 2, 0], 0), ([3, 0, 20, 1, 64, 0, 7, 9], 5), ([0, 0], 3), ([70, 130, 0, 1], 0),
-                                        ([1] * 70, 2)])
-@pytest.mark.parametrize("n,k", [(48, 384), (257, 1023), (2000, 128)])
+                                        ([1] * 70, 2), ([29, 31, 0, 40] * 5, 1), ([100, 0, 130, 1] * 5, 9)])
+@pytest.mark.parametrize("n,k", [(48, 384), (257, 1023), (2000, 128), (1000, 2100)])
 @pytest.mark.parametrize("dtype,group,zeros", [(BF16, 128, False), (F16, 32, True)])
 def test_w4_experts(counts, rest, n, k, dtype, group, zeros):
     e, rows = len(counts), sum(counts) + rest
@@ -653,6 +655,62 @@ def test_side_streams_at_once():
         for r in runs:
             for a, e in zip(r, w):
                 assert torch.equal(a, e)
+
+
+# ------------------------------------------------------------------------------- contents gone wrong
+
+@pytest.mark.parametrize("off", [[5, 2, 40, 10], [-7, 30, 30, 1000], [0, 0, 0, -1], [60, 50, 40, 30],
+                                 [2**31 - 1, -(2**31), 7, 2**30]])
+def test_wrong_offsets_stay_inside_the_operands(off):
+    # offsets are clamped to the operands: the results mean nothing, but nothing else is touched
+    rows, n, k = 50, 72, 88
+    guard = 64
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    x, b = ints((rows, k), BF16, 131), ints((3, n, k), BF16, 132)
+    dc = ints((rows, n), BF16, 133)
+    q, s, z = w4_parts((3, n), k, 32, BF16, True, 134)
+    w = spt.pack_w4(q, s, z, 32)
+    for tile in (32, 128, 256):
+        c = torch.full((rows + 2 * guard, n), 7.0, dtype=BF16, device="cuda")
+        spt.grouped_matmul(x, b, offsets, out=c[guard:-guard], tile=tile)
+        a = torch.full((rows + 2 * guard, k), 7.0, dtype=BF16, device="cuda")
+        spt.grouped_matmul_grad_a(dc, b, offsets, out=a[guard:-guard], tile=tile)
+        for t in (c, a):
+            assert (t[:guard] == 7).all() and (t[-guard:] == 7).all()
+        if tile != 32:
+            assert spt.grouped_matmul_grad_b(dc, x, offsets, tile=tile).shape == (3, n, k)
+    c = torch.full((rows + 2 * guard, n), 7.0, dtype=BF16, device="cuda")
+    spt.w4_matmul(x, w, offsets, out=c[guard:-guard])
+    assert (c[:guard] == 7).all() and (c[-guard:] == 7).all()
+
+
+def test_wrong_positions_stay_inside_the_operands():
+    order = spt.sort_tokens(ids_of(20, 2, 3, 141), 3)
+    order.rows.copy_(torch.tensor([-5, 1000, 2**31 - 1, -(2**31), 39, 40, 3, 3] * 5, dtype=torch.int32).view(20, 2))
+    x = ints((20, 24), F16, 142)
+    out = torch.full((40 + 128, 24), 7.0, dtype=F16, device="cuda")
+    spt.gather_rows(x, order, out=out[64:-64])
+    assert (out[:64] == 7).all() and (out[-64:] == 7).all()
+    y = ints((40, 24), F16, 143)
+    assert spt.combine_rows(y, order).shape == (20, 24)
+    dy, dw = spt.combine_rows_grad(x, y, order, torch.ones((20, 2), device="cuda"))
+    assert dy.shape == y.shape and dw[0].eq(0).all()
+
+
+def test_no_slots_and_no_tokens():
+    order = spt.sort_tokens(torch.zeros((5, 0), dtype=torch.int64, device="cuda"), 3)
+    x = ints((5, 16), F16, 151)
+    assert order.offsets.eq(0).all() and spt.gather_rows(x, order).shape == (0, 16)
+    assert spt.combine_rows(x[:0], order).eq(0).all() and spt.gather_rows_grad(x[:0], order).shape == (5, 16)
+    order = spt.sort_tokens(torch.zeros((0, 2), dtype=torch.int32, device="cuda"), 3)
+    assert spt.combine_rows(x[:0], order, torch.zeros((0, 2), device="cuda")).shape == (0, 16)
+    b = ints((3, 8, 16), F16, 152)
+    assert spt.routed_matmul(x[:0], b, torch.zeros((0, 2), dtype=torch.int64, device="cuda")).shape == (0, 8)
+    ids = torch.full((5, 2), -1, dtype=torch.int64, device="cuda")  # every slot dropped
+    w = torch.ones((5, 2), device="cuda", requires_grad=True)
+    out = spt.routed_matmul(x, b, ids, w)
+    out.sum().backward()
+    assert out.eq(0).all() and w.grad.eq(0).all()
 
 
 # --------------------------------------------------------------------------------------- refusals
