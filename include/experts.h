@@ -100,7 +100,7 @@ typedef struct {
  * are chosen, an operand whose base, row length, leading dimension or expert stride is not a multiple of
  * 16 bytes is first copied to padded rows in the workspace.
  * Errors: GEMM_ERR_INVALID (null pointer, bad enum, negative size, ld or stride too small, workspace
- *         too small), GEMM_ERR_UNSUPPORTED (types; rows beyond 2^31 - 1; more than 2^31 - 1 output
+ *         too small), GEMM_ERR_UNSUPPORTED (types; rows beyond 2^31 - 1; more than 2^24 output
  *         tiles; a leading dimension of 2^20 elements or more), GEMM_ERR_HIP.
  */
 gemm_status_t gemm_grouped_workspace_bytes(const gemm_grouped_t* p, const void* X, const void* Y, int64_t* out);

@@ -49,7 +49,7 @@ __device__ __forceinline__ GroupBlock find_group(const int* __restrict__ offsets
       b = clampi(offsets[l], 0, rows);
       en = l < E ? clampi(offsets[l + 1], b, rows) : rows;
     }
-    const int nb = (en - b + bm - 1) / bm;
+    const int nb = (int)((unsigned)(en - b + bm - 1) / (unsigned)bm);
     int s = nb * per;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {

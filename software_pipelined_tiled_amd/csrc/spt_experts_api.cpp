@@ -10,6 +10,9 @@ namespace {
 
 constexpr int64_t kMax32 = 0x7FFFFFFF;
 constexpr int kMaxExperts = 1024;
+// Output tiles of a grouped product: 64 experts' counts add up in 32 bits whatever the offsets hold. Of the
+// smallest tiles these are 2^35 elements.
+constexpr int64_t kMaxUnits = (int64_t)1 << 24;
 constexpr int kMaxDevices = 64;
 constexpr int kCus = 256;  // the MI355X's, for choices that must not depend on the device in use
 
@@ -330,7 +333,7 @@ gemm_status_t experts_combine_grad(const void* dout, int64_t lddo, const void* y
   if (lddo < width || ldy < width || lddy < width || (weights && !is_dtype(weight_dtype))) return GEMM_ERR_INVALID;
   if (tokens == 0 || top_k == 0) return GEMM_OK;
   if (!rows || !kept || (width > 0 && (!dout || !y || !dy)) || (weights && !dweights)) return GEMM_ERR_INVALID;
-  if (tokens * 256 > kMax32) return GEMM_ERR_UNSUPPORTED;
+  if (tokens * 256 > kMax32 || width > kMax32 - 2048) return GEMM_ERR_UNSUPPORTED;
   spt::RouteArgs a{};
   a.src = (const char*)y;
   a.dout = (const char*)dout;
@@ -370,9 +373,6 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   // operands that hold at least one element have to be there
   if ((s.x.rows > 0 && s.x.cols > 0 && !X) || (s.y.rows > 0 && s.y.cols > 0 && !Y)) return GEMM_ERR_INVALID;
   if (s.ws > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < s.ws)) return GEMM_ERR_INVALID;
-  int cu = 0;
-  st = device_cus(&cu);
-  if (st != GEMM_OK) return st;
 
   // 32-row tiles: with at most two of them for every compute unit, two workgroups with six stages in flight
   // (64 rows, 8 experts, 4096^2: 44 us against 57 with three of four stages); with more, a third workgroup
@@ -380,14 +380,17 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   // without 16-byte rows neighbouring loads share lines, and it costs (2044 columns: 56 us against 49).
   const int64_t used = p->experts < p->rows ? p->experts : p->rows;
   const int64_t blocks = used + (p->rows > 16 * used ? (p->rows - 16 * used) / 32 : 0);  // about
-  const bool deep = s.tile == 32 && blocks * ceil_div(out_n, 64) <= 2 * (int64_t)cu && (uintptr_t)Y % 16 == 0 &&
+  const bool deep = s.tile == 32 && blocks * ceil_div(out_n, 64) <= 2 * kCus && (uintptr_t)Y % 16 == 0 &&
                     p->k % 8 == 0 && p->ldy % 8 == 0;
   const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, s.tile, deep, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
   const int64_t tiles_m = ceil_div(p->n, entry.bm), tiles_n = ceil_div(out_n, entry.bn);
   const int64_t units = gb ? p->experts * tiles_m * tiles_n
                            : spt::max_row_blocks(p->rows, p->experts, entry.bm) * tiles_n;
+  if (units > kMaxUnits) return GEMM_ERR_UNSUPPORTED;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
   const int64_t grid = units < (int64_t)cu * entry.per_cu ? units : (int64_t)cu * entry.per_cu;
-  if (units + grid > kMax32) return GEMM_ERR_UNSUPPORTED;
 
   st = pad_operand(s.x, &X, (char*)workspace, stream);
   if (st != GEMM_OK) return st;

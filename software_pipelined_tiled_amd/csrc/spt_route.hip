@@ -17,7 +17,8 @@ namespace spt {
 // ------------------------------------------------------------------------------ counting sort
 constexpr int kSortThreads = 1024, kSortWaves = 16;
 
-__device__ __forceinline__ int slot_key(const SortArgs& a, int i) {
+// Slot numbers are unsigned in loops: a step past the last may pass 2^31.
+__device__ __forceinline__ int slot_key(const SortArgs& a, unsigned i) {
   if (a.id64) {
     const int64_t v = ((const int64_t*)a.ids)[i];
     return v >= 0 && v < a.experts ? (int)v : a.experts;
@@ -61,7 +62,7 @@ __device__ __forceinline__ int block_prefix(int v, int* tmp, int& total) {
 // Places the slots [first, last) of one workgroup. cnt[w][e] holds wave w's count of key e on entry
 // and start[e] the position of the workgroup's first slot with key e. Each wave owns a contiguous
 // run of slots, so the order inside a key is the order of the slots.
-__device__ __forceinline__ void place_slots(const SortArgs& a, int first, int last, int run, int* cnt, const int* start) {
+__device__ __forceinline__ void place_slots(const SortArgs& a, unsigned first, unsigned last, unsigned run, int* cnt, const int* start) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int keys = a.experts + 1;
   for (int e = threadIdx.x; e < keys; e += kSortThreads) {
@@ -74,9 +75,9 @@ __device__ __forceinline__ void place_slots(const SortArgs& a, int first, int la
   }
   __syncthreads();
   const int bits = 32 - __builtin_clz(a.experts);  // keys 0 .. experts
-  const int lo = first + wave * run, hi = lo + run < last ? lo + run : last;
-  for (int i0 = lo; i0 < hi; i0 += 64) {
-    const int i = i0 + lane;
+  const unsigned lo = first + wave * run, hi = lo + run < last ? lo + run : last;
+  for (unsigned i0 = lo; i0 < hi; i0 += 64) {
+    const unsigned i = i0 + lane;
     const bool on = i < hi;
     const unsigned long long active = __ballot(on);
     const int key = on ? slot_key(a, i) : 0;
@@ -86,19 +87,19 @@ __device__ __forceinline__ void place_slots(const SortArgs& a, int first, int la
     if (on && rank == 0) at = atomicAdd(&cnt[wave * keys + key], __popcll(same));  // LDS, one lane per key
     at = __shfl(at, same ? __builtin_ctzll(same) : 0) + rank;
     if (on) {
-      a.slots[at] = i;
+      a.slots[at] = (int)i;
       a.rows_of[i] = at;
     }
   }
 }
 
-__device__ __forceinline__ void count_slots(const SortArgs& a, int first, int last, int run, int* cnt) {
+__device__ __forceinline__ void count_slots(const SortArgs& a, unsigned first, unsigned last, unsigned run, int* cnt) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int keys = a.experts + 1;
   for (int i = threadIdx.x; i < kSortWaves * keys; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
-  const int lo = first + wave * run, hi = lo + run < last ? lo + run : last;
-  for (int i = lo + lane; i < hi; i += 64) atomicAdd(&cnt[wave * keys + slot_key(a, i)], 1);
+  const unsigned lo = first + wave * run, hi = lo + run < last ? lo + run : last;
+  for (unsigned i = lo + lane; i < hi; i += 64) atomicAdd(&cnt[wave * keys + slot_key(a, i)], 1);
   __syncthreads();
 }
 
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_one_kernel(SortArgs a) {
   int* cnt = lds;                       // [16][keys]
   int* start = lds + kSortWaves * keys;  // [keys]
   int* tmp = start + keys;              // [16]
-  const int run = ((a.rows + kSortWaves - 1) / kSortWaves + 63) & ~63;
+  const unsigned run = ((unsigned)(a.rows + kSortWaves - 1) / kSortWaves + 63) & ~63u;
   count_slots(a, 0, a.rows, run, cnt);
   const int e = threadIdx.x;
   int mine = 0, total = 0;
@@ -134,9 +135,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(SortArgs a) {
   const int keys = a.experts + 1;
   for (int i = threadIdx.x; i < keys; i += kSortThreads) lds[i] = 0;
   __syncthreads();
-  const int first = blockIdx.x * a.per_block;
-  const int last = a.rows - first < a.per_block ? a.rows : first + a.per_block;
-  for (int i = first + (int)threadIdx.x; i < last; i += kSortThreads) atomicAdd(&lds[slot_key(a, i)], 1);
+  const unsigned first = blockIdx.x * a.per_block;
+  const unsigned last = a.rows - first < (unsigned)a.per_block ? a.rows : first + a.per_block;
+  for (unsigned i = first + threadIdx.x; i < last; i += kSortThreads) atomicAdd(&lds[slot_key(a, i)], 1);
   __syncthreads();
   for (int i = threadIdx.x; i < keys; i += kSortThreads) a.counts[(int64_t)blockIdx.x * keys + i] = lds[i];
 }
@@ -181,9 +182,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortArgs a) {
       start[e] = before;
     }
   }
-  const int first = blockIdx.x * a.per_block;
-  const int last = a.rows - first < a.per_block ? a.rows : first + a.per_block;
-  const int run = a.per_block / kSortWaves;
+  const unsigned first = blockIdx.x * a.per_block;
+  const unsigned last = a.rows - first < (unsigned)a.per_block ? a.rows : first + a.per_block;
+  const unsigned run = a.per_block / kSortWaves;
   count_slots(a, first, last, run, cnt);  // its barriers also publish tot and start
   const int e = threadIdx.x;
   int total = 0;

@@ -156,13 +156,26 @@ class TokenOrder:
     the number of kept slots. slots [tokens * top_k]: sorted position to slot (token * top_k + j).
     rows [tokens, top_k]: slot to sorted position. All 32-bit.
     """
-    __slots__ = ("offsets", "slots", "rows", "num_experts", "tokens", "top_k", "sorted_rows", "kept_ptr")
+    __slots__ = ("offsets", "slots", "rows", "num_experts", "tokens", "top_k", "sorted_rows")
 
     def __init__(self, offsets: torch.Tensor, slots: torch.Tensor, rows: torch.Tensor, num_experts: int):
+        _need(rows.dim() == 2, "rows must be [tokens, top_k]")
+        for name, t, size in (("offsets", offsets, num_experts + 1), ("slots", slots, rows.numel()),
+                              ("rows", rows, rows.numel())):
+            if t.dtype != torch.int32 or t.numel() != size or not t.is_contiguous() or t.device != rows.device:
+                raise ValueError(f"{name} must be {size} contiguous 32-bit integers on rows' device")
+        self._set(offsets, slots, rows, num_experts)
+
+    def _set(self, offsets, slots, rows, num_experts):
         self.offsets, self.slots, self.rows, self.num_experts = offsets, slots, rows, num_experts
         self.tokens, self.top_k = rows.shape
         self.sorted_rows = self.tokens * self.top_k
-        self.kept_ptr = offsets.data_ptr() + 4 * num_experts  # where offsets[num_experts] lies
+        return self
+
+    @property
+    def kept_ptr(self) -> int:
+        """Where offsets[num_experts] lies."""
+        return self.offsets.data_ptr() + 4 * self.num_experts
 
 
 def sort_tokens(experts: torch.Tensor, num_experts: int) -> TokenOrder:
@@ -188,7 +201,7 @@ def sort_tokens(experts: torch.Tensor, num_experts: int) -> TokenOrder:
     ws = _workspace(ws_bytes, dev)
     _enqueue(dev, _lib.experts_sort, ids.data_ptr(), bits, n, num_experts, offsets.data_ptr(), slots.data_ptr(),
              rows.data_ptr(), _ptr(ws), ws_bytes)
-    return TokenOrder(offsets, slots, rows, num_experts)
+    return TokenOrder.__new__(TokenOrder)._set(offsets, slots, rows, num_experts)  # nothing to check
 
 
 def _gather(x, order, out):
@@ -408,6 +421,12 @@ class W4Weight:
     has_zeros: bool
     dtype: torch.dtype
 
+    def __post_init__(self):
+        nbytes = _lib.gemm_w4_packed_bytes(self.matrices, self.n, self.k, self.group_size, self.has_zeros)
+        p = self.packed
+        _need(p.dtype == torch.uint8 and p.is_contiguous() and p.numel() == nbytes and (self.stacked or self.matrices == 1),
+              f"packed must be {nbytes} contiguous bytes from pack_w4")
+
 
 def pack_w4(q: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
             group_size: int = 128) -> W4Weight:
@@ -470,8 +489,10 @@ def routed_matmul(x: torch.Tensor, weight: torch.Tensor | W4Weight, experts: tor
     rows gathered, multiplied and combined; ids outside the experts are dropped. Differentiable in x, B and
     the weights."""
     four_bits = isinstance(weight, W4Weight)
+    _need(four_bits or weight.dim() == 3, "the weight must be [experts, n, k]")
     num = weight.matrices if four_bits else weight.shape[0]
     _need(not four_bits or weight.stacked, "the weight must be packed from [experts, n, k]")
+    _need(x.dim() == 2 and experts.dim() in (1, 2), "x must be [tokens, k], experts [tokens, top_k] or [tokens]")
     _need(experts.shape[0] == x.shape[0], f"experts must have {x.shape[0]} rows")
     order = sort_tokens(experts, num)
     rows = gather_rows(x, order)

@@ -213,3 +213,35 @@ def test_torch_face_wants_supported_types():
         spt.pack_w4(torch.zeros((8, 32), dtype=torch.uint8), torch.zeros((8, 1)), group_size=32)
     with pytest.raises(ValueError):
         spt.pack_w4(torch.zeros((8, 32), dtype=torch.int8), torch.zeros((8, 1), dtype=torch.float16), group_size=32)
+
+
+def test_too_many_output_tiles():
+    # 2^22 row blocks of 256 by 8 column tiles
+    p = grouped(rows=2**30, experts=1, n=2048, k=8, ldx=8, ldy=8, ldo=2048, stride=2048 * 8, tile=256)
+    assert spt.lib().gemm_grouped_run(ctypes.byref(p), A, A, A, A, None, 0, None) == UNSUPPORTED
+
+
+def test_token_order_checks_its_parts():
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    assert spt.TokenOrder(i32(4), i32(6), i32(3, 2), 3).sorted_rows == 6
+    for bad in ((i32(3), i32(6), i32(3, 2)), (i32(4), i32(5), i32(3, 2)), (i32(4), i32(6), i32(6)),
+                (i32(4), i32(6), i32(2, 3).t()), (i32(4).long(), i32(6), i32(3, 2)), (i32(4), i32(6), i32(3, 2).long())):
+        with pytest.raises(ValueError):
+            spt.TokenOrder(*bad, 3)
+
+
+def test_w4_weight_checks_its_bytes():
+    make = lambda size, stacked=False, m=1: spt.W4Weight(torch.zeros(size, dtype=torch.uint8), m, stacked, 17, 129, 64, False,
+                                                         torch.float16)
+    assert make(2 * 2 * (1024 + 64)).n == 17
+    for bad in (lambda: make(2 * 2 * (1024 + 64) - 1), lambda: make(0), lambda: make(2 * 4 * (1024 + 64), False, 2)):
+        with pytest.raises(ValueError, match="packed"):
+            bad()
+
+
+def test_routed_matmul_shapes():
+    x, b = torch.zeros((4, 8), dtype=torch.bfloat16), torch.zeros((2, 8, 8), dtype=torch.bfloat16)
+    ids = torch.zeros((4, 2), dtype=torch.int64)
+    for bad in ((x[0], b, ids), (x, b[0], ids), (x, b, ids[0, 0]), (x, b, ids[:3])):
+        with pytest.raises(ValueError):
+            spt.routed_matmul(*bad)
