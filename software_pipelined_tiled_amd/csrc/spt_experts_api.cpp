@@ -192,40 +192,50 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
   if (p->n > lim || p->k > lim || p->ldx >= lim / 2 || p->rows > kMax32 || p->matrices > kMax32)
     return GEMM_ERR_UNSUPPORTED;
   const int64_t n16 = ceil_div(p->n, 16), kb = ceil_div(p->k, 128);
-  // The kernel goes by the work: u 16 x 16 blocks of output. Few: one wave's K slices of one column block or
-  // two, straight from memory, which spreads best; from about 1000 blocks on the waves share x in LDS, in
-  // tiles that grow with u (short sums of few rows: fewer K parts, variant 6: 256 rows over 16 experts of 4096 x
-  // 2048 20.6 us against 27.1). us with bf16, G = 128, for variants 0 .. 5:
-  //   8192 x 8192, 1 row (u 512, weights bound)   13.0  10.3  12.9  14.2  15.6  18.8
-  //   4096 x 4096, 1 row (u 256)                   5.0   6.8   8.5   9.5  10.0  12.0
-  //   8192 x 8192, 32 rows (u 1024)               34.1  21.2  17.3  18.2  18.6  21.0
-  //   4096 x 4096, 128 rows (u 2048)              33.4  20.4  16.6  13.6  17.2  19.4
-  //   4096 x 4096, 256 rows (u 4096)              63.4  36.9  30.2  24.8  20.5  24.9
-  //   8192 x 8192, 512 rows (u 16384)            486.5 284.8 226.1 169.8 124.8  99.6
   const int64_t each = p->matrices > 0 ? ceil_div(p->rows, p->matrices) : 0;  // rows that share a matrix, on average
   const int64_t used = p->rows < p->matrices ? p->rows : p->matrices;
-  const int64_t u = n16 * used * ceil_div(each, 16);
-  const int variant = u <= 256               ? 0
-                      : u <= 768 || each <= 4   ? 1
-                      : each <= 16 && kb <= 16  ? 6
-                      : u <= 1100 || each <= 16 ? 2
-                      : u <= 3584               ? 3
-                      : u <= 8000               ? 4
-                                                : 5;
-  s->entry = spt::w4_entry(variant, p->dtype == GEMM_BF16, 128 / p->group, p->has_zeros != 0);
-  const int bm = 16 * s->entry.mt;
-  s->nblocks = ceil_div(n16, s->entry.nt);
-  s->row_blocks = grouped ? spt::max_row_blocks(p->rows, p->matrices, bm) : ceil_div(p->rows, bm);
-  if (s->row_blocks > 65535) return GEMM_ERR_UNSUPPORTED;
-  const int64_t wgs = s->nblocks * s->row_blocks;
+  auto take = [&](int variant) {
+    s->entry = spt::w4_entry(variant, p->dtype == GEMM_BF16, 128 / p->group, p->has_zeros != 0);
+    s->nblocks = ceil_div(n16, s->entry.nt);
+    s->row_blocks = grouped ? spt::max_row_blocks(p->rows, p->matrices, 16 * s->entry.mt) : ceil_div(p->rows, 16 * s->entry.mt);
+  };
   // Cut K when the workgroups alone leave compute units idle, into as many parts as still run at once: one
   // workgroup more than compute units is a second round.
-  s->splits = 1;
-  if (wgs > 0 && wgs < cu) {
-    const int64_t most = kb / s->entry.waves;
-    s->splits = cu / wgs < most ? cu / wgs : most;
-    if (s->splits < 1) s->splits = 1;
+  auto splits = [&](int64_t cus) {
+    const int64_t wgs = s->nblocks * s->row_blocks, most = kb / s->entry.waves;
+    if (wgs <= 0 || wgs >= cus) return (int64_t)1;
+    const int64_t n = cus / wgs < most ? cus / wgs : most;
+    return n < 1 ? (int64_t)1 : n;
+  };
+  // Up to four rows a matrix: the waves take K slices straight from memory, 16 columns to a workgroup where
+  // that fills the compute units at most once (4096 x 4096, 1 row: 5.0 us, 32 columns 6.6; 8192 x 8192: 13.0
+  // against 10.3). Experts of up to 16 rows and short sums: few K parts (64 experts of 1408 x 2048, 256 rows:
+  // 21 us against 26). Else the least time by this model, in us: a start, rounds of workgroups over the
+  // compute units times blocks of K per wave, and the second pass over a split sum. Its constants are a fit to
+  // 960 measured shapes (N 512 .. 14336, K 1024 .. 14336, 1 .. 2000 rows, up to 64 experts): the choice takes
+  // 1.5 % longer than the best kernel of each shape, 30 % at worst; a rule on the number of 16 x 16 output
+  // blocks alone took 8.7 %, 97 % at worst (301 rows, 2048 x 14336: 70 us against 40).
+  if (each <= 4) {
+    take(n16 * used <= kCus ? 0 : 1);
+  } else if (each <= 16 && kb <= 16 && p->matrices > 1) {
+    take(6);
+  } else {
+    struct { double start, block, extra; } const t[] = {
+        {3.8, 1.03, 0.9}, {3.6, .82, 1.6}, {3.5, 1.19, 1.8}, {5.2, .94, 1.4}, {2.9, 1.43, 3.4}};
+    int best = 0;
+    double least = 0;
+    for (int v = 1; v <= 5; ++v) {
+      take(v);
+      const int64_t sp = splits(kCus), wgs = s->nblocks * used * ceil_div(each, 16 * s->entry.mt) * sp;
+      const double blocks = (double)ceil_div(ceil_div(kb, sp), s->entry.wk);
+      const double us = t[v - 1].start + t[v - 1].block * (blocks + t[v - 1].extra) * (double)ceil_div(wgs, kCus) +
+                        (sp > 1 ? 2 + (double)(sp * p->rows * p->n) * 2.4e-6 : 0);
+      if (best == 0 || us < least) best = v, least = us;
+    }
+    take(best);
   }
+  if (s->row_blocks > 65535) return GEMM_ERR_UNSUPPORTED;
+  s->splits = splits(cu);
   s->ws = s->splits > 1 ? s->splits * p->rows * p->n * 4 : 0;
   return GEMM_OK;
 }

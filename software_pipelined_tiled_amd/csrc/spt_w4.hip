@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(256) w4_reduce_kernel(W4ReduceArgs r) {
 // ------------------------------------------------------------------------------ instantiations
 template <int T, int MT, int NT, int W, int D>
 static W4Entry w4_pick_group(int gpk, bool zero) {
-  W4Entry e{nullptr, MT, NT, W};
+  W4Entry e{nullptr, MT, NT, W, W};
   if (gpk == 1) e.fn = zero ? (const void*)&w4_kernel<T, MT, NT, 1, true, W, D> : (const void*)&w4_kernel<T, MT, NT, 1, false, W, D>;
   else if (gpk == 2) e.fn = zero ? (const void*)&w4_kernel<T, MT, NT, 2, true, W, D> : (const void*)&w4_kernel<T, MT, NT, 2, false, W, D>;
   else e.fn = zero ? (const void*)&w4_kernel<T, MT, NT, 4, true, W, D> : (const void*)&w4_kernel<T, MT, NT, 4, false, W, D>;
@@ -544,7 +544,7 @@ static W4Entry w4_pick_group(int gpk, bool zero) {
 }
 template <int T, int MT, int NT, int WN, int WK>
 static W4Entry w4_pick_rows(int gpk, bool zero) {
-  W4Entry e{nullptr, MT, NT * WN, WN * WK};
+  W4Entry e{nullptr, MT, NT * WN, WN * WK, WK};
   if (gpk == 1) e.fn = zero ? (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 1, true> : (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 1, false>;
   else if (gpk == 2) e.fn = zero ? (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 2, true> : (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 2, false>;
   else e.fn = zero ? (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 4, true> : (const void*)&w4_rows_kernel<T, MT, NT, WN, WK, 4, false>;
