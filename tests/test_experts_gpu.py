@@ -296,6 +296,32 @@ def test_grouped_many_tiles_of_short_sums(mode, length, tile):
         assert torch.equal(got, ref.to(got.dtype)), out_dtype
 
 
+# a little more than one round of 256 x 256 tiles over 256 compute units, the last tiles a row or a column wide
+@pytest.mark.parametrize("mode", ["f", "a", "b"])
+@pytest.mark.parametrize("length", [1024, 1101])
+@pytest.mark.parametrize("width", [6016, 6273, 6145])
+@pytest.mark.parametrize("counts,rest", [([1300, 0, 257, 900], 0), ([129, 128, 1281, 640, 1], 100), ([2700], 20)])
+def test_grouped_second_round(mode, length, width, counts, rest):
+    if mode == "b":
+        counts, rest, n, k = [length, length + 65, length + 1, 2 * length][:len(counts) or 1], 7, 2056, width
+        counts = counts if len(counts) > 1 else counts * 2
+    else:
+        n, k = (width, length) if mode == "f" else (length, width)
+    rows, experts = sum(counts) + rest, len(counts)
+    off = offsets_of(counts)
+    x, y = operands(mode, rows, experts, n, k, lambda s, seed: ints(s, BF16, seed))
+    ref, _ = plain_grouped(mode, x, y, off.tolist(), experts, n, k)
+    for out_dtype in (F32, BF16):
+        got = call_grouped(mode, x, y, off, out_dtype)
+        assert torch.equal(got, ref.to(got.dtype)), out_dtype
+        assert torch.equal(got, call_grouped(mode, x, y, off, out_dtype, 256)), out_dtype
+    if mode != "b":
+        out = torch.full((rows, width + 8), 7.0, dtype=BF16, device="cuda")
+        (spt.grouped_matmul if mode == "f" else spt.grouped_matmul_grad_a)(x, y, off, out=out[:, :width])
+        kept = sum(counts)
+        assert torch.equal(out[:kept, :width], ref[:kept].to(BF16)) and (out[kept:] == 7).all() and (out[:, width:] == 7).all()
+
+
 @pytest.mark.parametrize("mode", ["f", "a"])
 @pytest.mark.parametrize("per", [5, 200])
 def test_grouped_out_rows_left_as_they_were(mode, per):
