@@ -186,8 +186,8 @@ struct W4Entry {
   const void* fn;
   int mt, nt, waves, wk;  // 16-row and 16-column blocks of a workgroup, its waves, and how many share out K
 };
-// variant 0, 1: 16 rows by 16 or 32 columns; sharing x, 2: 16 rows by 64; 3, 4: 32 rows by 64, 128; 5: 64 rows
-// by 128; 6: 16 rows by 128, fewer K parts than 2. gpk: groups per 128 k
+// variant 0, 1: 16 rows by 16 or 32 columns; sharing x, 2: 16 rows by 64; 3, 4: 32 rows by 64, 128; 5, 6: 64
+// rows by 128, 256; 7: 16 rows by 128, fewer K parts than 2. gpk: groups per 128 k
 W4Entry w4_entry(int variant, int bf16, int gpk, bool zero);
 const void* w4_pack_fn();
 const void* w4_pack_groups_fn();

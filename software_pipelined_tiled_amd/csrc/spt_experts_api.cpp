@@ -207,24 +207,24 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
     const int64_t n = cus / wgs < most ? cus / wgs : most;
     return n < 1 ? (int64_t)1 : n;
   };
-  // Up to four rows a matrix: the waves take K slices straight from memory, 16 columns to a workgroup where
-  // that fills the compute units at most once (4096 x 4096, 1 row: 5.0 us, 32 columns 6.6; 8192 x 8192: 13.0
-  // against 10.3). Experts of up to 16 rows and short sums: few K parts (64 experts of 1408 x 2048, 256 rows:
-  // 21 us against 26). Else the least time by this model, in us: a start, rounds of workgroups over the
-  // compute units times blocks of K per wave, and the second pass over a split sum. Its constants are a fit to
-  // 960 measured shapes (N 512 .. 14336, K 1024 .. 14336, 1 .. 2000 rows, up to 64 experts): the choice takes
-  // 1.5 % longer than the best kernel of each shape, 30 % at worst; a rule on the number of 16 x 16 output
-  // blocks alone took 8.7 %, 97 % at worst (301 rows, 2048 x 14336: 70 us against 40).
-  if (each <= 4) {
+  // Many blocks of up to 16 rows with short sums: few K parts (64 experts of 1408 x 2048, 64 rows: 21 us
+  // against 25 to 59; 16 of 2048 x 2048, 8 rows: 9.7 against 7.4). Up to four rows a matrix: the waves take K
+  // slices straight from memory, 16 columns to a workgroup where that fills the compute units at most once
+  // (4096 x 4096, 1 row: 5.0 us, 32 columns 6.6; 8192 x 8192: 13.0 against 10.3). Else the least time by this
+  // model, in us: a start, rounds of workgroups over the compute units times blocks of K per wave, and the second
+  // pass over a split sum. Its constants are a fit to 1320 measured shapes (N 512 .. 28672, K 1024 .. 14336, 1 ..
+  // 2000 rows, up to 64 experts). The choice takes 2 % longer than the best kernel of each shape, 39 % at worst; a
+  // rule on the number of 16 x 16 output blocks alone took 9 %, 95 % at worst.
+  if (each <= 16 && kb <= 16 && p->matrices > 1 && n16 * used >= 1536) {
+    take(7);
+  } else if (each <= 4) {
     take(n16 * used <= kCus ? 0 : 1);
-  } else if (each <= 16 && kb <= 16 && p->matrices > 1) {
-    take(6);
   } else {
     struct { double start, block, extra; } const t[] = {
-        {3.8, 1.03, 0.9}, {3.6, .82, 1.6}, {3.5, 1.19, 1.8}, {5.2, .94, 1.4}, {2.9, 1.43, 3.4}};
+        {3.9, 1.03, 0.7}, {3.5, .82, 1.6}, {3.4, 1.19, 1.8}, {4.8, .96, 1.4}, {5.3, .73, 1.9}, {3.4, 1.27, 3.1}};
     int best = 0;
     double least = 0;
-    for (int v = 1; v <= 5; ++v) {
+    for (int v = 1; v <= 6; ++v) {
       take(v);
       const int64_t sp = splits(kCus), wgs = s->nblocks * used * ceil_div(each, 16 * s->entry.mt) * sp;
       const double blocks = (double)ceil_div(ceil_div(kb, sp), s->entry.wk);

@@ -413,28 +413,33 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
 #pragma unroll
     for (int g = 0; g < GPK; ++g) {
       constexpr int SPG = 4 / GPK;  // matrix steps per group
-      u32x4 xf[SPG][MT];
-#pragma unroll
-      for (int s = 0; s < SPG; ++s)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) xf[s][i] = *(const u32x4*)x_at(buf, w, (g * SPG + s) * MT + i);
+      decltype(zero_of<T>(0u)) z[NT];
+      f32x4 sum[NT][MT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const auto z = zero_of<T>(ZERO ? (unsigned)(st.z[j] >> (8 * g)) & 0xFFu : 8u);
-        f32x4 sum[MT];
+        z[j] = zero_of<T>(ZERO ? (unsigned)(st.z[j] >> (8 * g)) & 0xFFu : 8u);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) sum[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < MT; ++i) sum[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
 #pragma unroll
-        for (int s = 0; s < SPG; ++s) {
-          const u32x4 wf = unpack(st.q[j][g * SPG + s], z);
+      for (int s = 0; s < SPG; ++s) {
+        u32x4 xf[MT];
 #pragma unroll
-          for (int i = 0; i < MT; ++i) sum[i] = mfma16<TIn>(xf[s][i], wf, sum[i]);
+        for (int i = 0; i < MT; ++i) xf[i] = *(const u32x4*)x_at(buf, w, (g * SPG + s) * MT + i);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const u32x4 wf = unpack(st.q[j][g * SPG + s], z[j]);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) sum[j][i] = mfma16<TIn>(xf[i], wf, sum[j][i]);
         }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
         const float sc = scale_of<T>((unsigned)(st.s[j] >> (16 * g)) & 0xFFFFu);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(sum[i][r], sc, acc[i][j][r]);
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(sum[j][i][r], sc, acc[i][j][r]);
       }
     }
   };
@@ -558,8 +563,9 @@ static W4Entry w4_pick(int variant, int gpk, bool zero) {
     case 2: return w4_pick_rows<T, 1, 1, 4, 4>(gpk, zero);
     case 3: return w4_pick_rows<T, 2, 1, 4, 4>(gpk, zero);
     case 4: return w4_pick_rows<T, 2, 2, 4, 2>(gpk, zero);
-    case 6: return w4_pick_rows<T, 1, 2, 4, 2>(gpk, zero);
-    default: return w4_pick_rows<T, 4, 2, 4, 2>(gpk, zero);
+    case 5: return w4_pick_rows<T, 4, 1, 8, 1>(gpk, zero);
+    case 6: return w4_pick_rows<T, 4, 2, 8, 1>(gpk, zero);
+    default: return w4_pick_rows<T, 1, 2, 4, 2>(gpk, zero);
   }
 }
 W4Entry w4_entry(int variant, int bf16, int gpk, bool zero) {

@@ -426,7 +426,8 @@ def w4_dense(q, s, z, group):
 W4_SHAPES = [(1, 1, 1), (1, 16, 128), (2, 17, 31), (5, 100, 33), (16, 64, 256), (17, 48, 1000), (1, 1024, 4096), (33, 40, 520),
              (64, 130, 384), (65, 257, 129), (200, 96, 640), (3, 2056, 8190), (16, 16400, 256),
              # one shape for each kernel the choice goes to as the output grows, with blocks of K that K cuts
-             (2, 4160, 200), (15, 17500, 2201), (40, 8000, 303), (130, 9000, 300), (300, 8001, 517), (70, 24000, 120)]
+             (2, 4160, 200), (15, 17500, 2201), (40, 8000, 303), (130, 9000, 300), (300, 8001, 517), (70, 24000, 120),
+             (520, 8200, 261), (301, 1030, 4097)]
 
 
 @pytest.mark.parametrize("rows,n,k", W4_SHAPES)
