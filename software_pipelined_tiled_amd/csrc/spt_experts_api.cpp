@@ -104,29 +104,69 @@ struct GroupedShape {
   int64_t ws;
 };
 
-// Rows of an output tile. Few rows per expert: 32, so that reading B is all there is to do. Else the
-// tile with the shorter time in us: rounds of tiles over the compute units, times K-tiles (and about two
-// more for the stores), times what a K-tile takes. 256-row tiles copy an operand that is off 16 bytes
-// first; 128-row tiles load it as it lies, a tenth slower.
-int grouped_tile(const gemm_grouped_t* p, int cu, const Operand* const (&ops)[2], const bool (&off)[2]) {
-  const bool gb = p->mode == GEMM_GROUPED_GRAD_B;
-  const int64_t e = p->experts > 0 ? p->experts : 1;
-  const int64_t each = ceil_div(p->rows, e);
-  if (!gb && each <= 32) return 32;
+// 32-row tiles: with at most two of them for every compute unit and rows of whole 16-byte chunks, two
+// workgroups with six stages in flight and the hint that keeps Y, which is read once then, out of the caches
+// (64 rows, 8 experts, 4096^2: 44 us against 57 with three workgroups of four stages). With more tiles a third
+// workgroup saves a round (200 rows: 59 against 77), and off 16 bytes neighbouring loads share lines, and the
+// hint costs (2044 columns: 56 us against 49).
+bool grouped_few(const gemm_grouped_t* p) {
   const int64_t out_n = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
-  const double kt = (double)ceil_div(gb ? each : p->mode == GEMM_GROUPED_FORWARD ? p->k : p->n, 64) + 2;
-  auto cost = [&](int bm, int64_t slots, double per_k_tile) {
-    // an expert's last row block is half full on average
-    const int64_t rb = gb ? e * ceil_div(p->n, bm) : (2 * p->rows + e * bm) / (2 * bm) + 1;
-    return (double)ceil_div(rb * ceil_div(out_n, bm), slots) * kt * per_k_tile;
-  };
+  const int64_t used = p->experts < p->rows ? p->experts : p->rows;
+  const int64_t blocks = used + (p->rows > 16 * used ? (p->rows - 16 * used) / 32 : 0);  // about
+  return blocks * ceil_div(out_n, 64) <= 2 * kCus;
+}
+bool grouped_deep(const gemm_grouped_t* p, const void* Y) {
+  return grouped_few(p) && (uintptr_t)Y % 16 == 0 && p->k % 8 == 0 && p->ldy % 8 == 0;
+}
+
+// Rows of an output tile: the least time by this model, in us. A start, and the longer of rounds of tiles over the
+// compute units (K-tiles times what one takes, and the tile's own start and end) and the operands' bytes.
+// 256-row tiles copy an operand that is off 16 bytes first. The constants are a fit to 1608 measured shapes
+// (1 .. 128 experts, 32 .. 16384 rows, N and K 512 .. 8192); the choice takes 2 % longer than the best tile of
+// each shape, 47 % at worst, where 32-row tiles for up to 32 rows per expert and rounds alone took 7 %, 185 % at
+// worst (grad B of 64 experts of 1001 x 1500, 32 rows: 113 us against 39).
+//   Two things the model leaves out. Grad A's 32-row tiles beyond two for every compute unit read B in pieces of 256
+// bytes from many places, and 128-row tiles are faster even for few rows (128 rows, 16 experts, 4096^2: 86 us against
+// 94). And grad B's 128-row tiles reload what the L2 no longer holds from about 64 rows per expert on (16384
+// rows, 128 experts, 2048 x 512: 150 us, the model says 93); with long sums that hides behind the products.
+int grouped_tile(const gemm_grouped_t* p, const Operand* const (&ops)[2], const bool (&off)[2]) {
+  const bool gb = p->mode == GEMM_GROUPED_GRAD_B, fwd = p->mode == GEMM_GROUPED_FORWARD;
+  const int64_t used = p->experts < p->rows ? p->experts : p->rows;
+  if (used == 0) return 128;
+  const int64_t out_n = fwd ? p->n : p->k;
+  const double rows = (double)p->rows, n = (double)p->n, k = (double)p->k;
+  const double mb = ((double)(gb ? p->experts : used) * n * k + rows * (n + k)) * 2e-6;
+  const double each = rows / (double)p->experts;
+  // an expert's last K-tile (grad B) or row block is half full on average
+  const double kt = gb ? each / 64 + 0.5 : (double)ceil_div(fwd ? p->k : p->n, 64);
   double copy = 0;
   for (int i = 0; i < 2; ++i)
     if (off[i]) copy += 3 + (double)ops[i]->rows * (double)ops[i]->cols * 4 / 4.5e6;  // read and written at 4.5 TB/s
-  return cost(256, cu, 1.5) + copy <= cost(128, 2 * (int64_t)cu, copy > 0 ? 1.2 : 1.1) ? 256 : 128;
+  struct Tile {
+    int bm, bn, slots;
+    struct { double start, k_tile, tile, mb; } by_mode[3];
+  };
+  static const Tile tiles[3] = {
+      {32, 64, 3 * kCus, {{1.0, .41, 4.7, .17}, {1.4, .49, 4.1, .19}, {}}},
+      {128, 128, 2 * kCus, {{0, .77, 6.0, .21}, {0, .78, 6.2, .19}, {5.8, .87, 3.2, .19}}},
+      {256, 256, kCus, {{0, 1.07, 7.8, .23}, {0, 1.2, 9.4, .22}, {4.0, 1.5, 6.3, .28}}}};
+  int best = 0;
+  double least = 0;
+  for (const Tile& t : tiles) {
+    if (t.bm == 32 && (gb || (!fwd && !grouped_few(p)))) continue;
+    const auto& c = t.by_mode[p->mode];
+    int64_t rb = gb ? p->experts * ceil_div(p->n, t.bm) : (2 * p->rows + used * t.bm) / (2 * t.bm);
+    if (rb < used) rb = used;
+    const double work = (double)ceil_div(rb * ceil_div(out_n, t.bn), t.slots) * (c.k_tile * kt + c.tile);
+    double us = c.start + (work > c.mb * mb ? work : c.mb * mb);
+    if (t.bm == 256) us += copy;
+    if (t.bm == 128 && gb && each >= 64 && each < 512) us *= 1.2;
+    if (best == 0 || us < least) best = t.bm, least = us;
+  }
+  return best;
 }
 
-gemm_status_t grouped_shape(const gemm_grouped_t* p, int cu, const void* X, const void* Y, GroupedShape* s) {
+gemm_status_t grouped_shape(const gemm_grouped_t* p, const void* X, const void* Y, GroupedShape* s) {
   if (!p || p->mode < GEMM_GROUPED_FORWARD || p->mode > GEMM_GROUPED_GRAD_B) return GEMM_ERR_INVALID;
   if (p->rows < 0 || p->experts < 0 || p->n < 0 || p->k < 0) return GEMM_ERR_INVALID;
   if (!is_dtype(p->in_dtype) || !is_dtype(p->out_dtype)) return GEMM_ERR_INVALID;
@@ -150,7 +190,7 @@ gemm_status_t grouped_shape(const gemm_grouped_t* p, int cu, const void* X, cons
   bool off[2];  // not in rows of whole 16-byte chunks
   for (int i = 0; i < 2; ++i)
     off[i] = (uintptr_t)ptr[i] % 16 != 0 || ops[i]->cols % 8 != 0 || ops[i]->ld % 8 != 0 || ops[i]->stride % 8 != 0;
-  s->tile = p->tile ? p->tile : grouped_tile(p, cu, {ops[0], ops[1]}, off);
+  s->tile = p->tile ? p->tile : grouped_tile(p, {ops[0], ops[1]}, off);
   for (int i = 0; i < 2; ++i) {
     Operand& o = *ops[i];
     o.pad = s->tile == 256 && off[i];
@@ -366,7 +406,7 @@ gemm_status_t experts_combine_grad(const void* dout, int64_t lddo, const void* y
 gemm_status_t gemm_grouped_workspace_bytes(const gemm_grouped_t* p, const void* X, const void* Y, int64_t* out) {
   GroupedShape s;
   if (!out) return GEMM_ERR_INVALID;
-  const gemm_status_t st = grouped_shape(p, kCus, X, Y, &s);
+  const gemm_status_t st = grouped_shape(p, X, Y, &s);
   if (st == GEMM_OK) *out = s.ws;
   return st;
 }
@@ -374,7 +414,7 @@ gemm_status_t gemm_grouped_workspace_bytes(const gemm_grouped_t* p, const void* 
 gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const void* Y, void* out,
                                const int32_t* offsets, void* workspace, int64_t workspace_bytes, void* stream) {
   GroupedShape s;
-  gemm_status_t st = grouped_shape(p, kCus, X, Y, &s);
+  gemm_status_t st = grouped_shape(p, X, Y, &s);
   if (st != GEMM_OK) return st;
   const bool gb = p->mode == GEMM_GROUPED_GRAD_B, fwd = p->mode == GEMM_GROUPED_FORWARD;
   const int64_t out_n = fwd ? p->n : p->k;
@@ -384,14 +424,7 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   if ((s.x.rows > 0 && s.x.cols > 0 && !X) || (s.y.rows > 0 && s.y.cols > 0 && !Y)) return GEMM_ERR_INVALID;
   if (s.ws > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < s.ws)) return GEMM_ERR_INVALID;
 
-  // 32-row tiles: with at most two of them for every compute unit, two workgroups with six stages in flight
-  // (64 rows, 8 experts, 4096^2: 44 us against 57 with three of four stages); with more, a third workgroup
-  // saves a round (200 rows: 59 against 77). The hint keeps B, which is read once then, out of the caches;
-  // without 16-byte rows neighbouring loads share lines, and it costs (2044 columns: 56 us against 49).
-  const int64_t used = p->experts < p->rows ? p->experts : p->rows;
-  const int64_t blocks = used + (p->rows > 16 * used ? (p->rows - 16 * used) / 32 : 0);  // about
-  const bool deep = s.tile == 32 && blocks * ceil_div(out_n, 64) <= 2 * kCus && (uintptr_t)Y % 16 == 0 &&
-                    p->k % 8 == 0 && p->ldy % 8 == 0;
+  const bool deep = s.tile == 32 && grouped_deep(p, Y);
   const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, s.tile, deep, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
   const int64_t tiles_m = ceil_div(p->n, entry.bm), tiles_n = ceil_div(out_n, entry.bn);
   const int64_t units = gb ? p->experts * tiles_m * tiles_n

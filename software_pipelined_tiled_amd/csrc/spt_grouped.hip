@@ -311,7 +311,7 @@ GroupedEntry grouped_entry(int mode, int tile, bool deep, int bf16, int out) {
   if (mode == kGroupedGradA)
     return tile == 128 ? grouped_pick<kGroupedGradA, 128, 128, 2, 2, 2, 2>(bf16, out)
            : deep      ? grouped_pick<kGroupedGradA, 32, 64, 2, 2, 6, 2, true>(bf16, out)
-                       : grouped_pick<kGroupedGradA, 32, 64, 2, 2, 4, 3>(bf16, out);
+                       : grouped_pick<kGroupedGradA, 32, 128, 2, 2, 4, 2>(bf16, out);  // B's rows are c: longer pieces
   return grouped_pick<kGroupedGradB, 128, 128, 2, 2, 2, 2>(bf16, out);
 }
 
