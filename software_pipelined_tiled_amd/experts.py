@@ -7,8 +7,9 @@ Workspaces come from torch's allocator, so calls on several streams, or captured
 never share one. Rows of a tensor may be any distance apart (unit column stride).
 
 ``gather_rows``, ``combine_rows``, ``grouped_matmul`` and ``routed_matmul`` are differentiable once. The
-``*_grad`` functions are the same gradients as plain calls, for programs that keep no autograd graph (a
-training step captured into a HIP graph among them).
+``*_grad`` functions are the same gradients as plain calls, for programs that keep no autograd graph. A
+training step captured into a HIP graph is safest with those: while an eager graph of the same leaves is alive, torch's
+backward ties a capture to that graph's stream and ends the process.
 """
 from __future__ import annotations
 

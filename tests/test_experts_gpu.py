@@ -668,6 +668,33 @@ def test_captured_steps_replay_to_the_eager_bits(odd):
                 assert torch.equal(o, e), rep
 
 
+def test_captured_autograd_step():
+    # autograd's own way: warmed up on the capture's kind of stream, and no eager graph of the leaves alive
+    x, b = normal((70, 96), BF16, 161).requires_grad_(), normal((5, 130, 96), BF16, 162).requires_grad_()
+    w = torch.rand((70, 2), device="cuda").requires_grad_()
+    ids, dout = ids_of(70, 2, 5, 163), normal((70, 130), BF16, 164)
+
+    def train():
+        return torch.autograd.grad(spt.routed_matmul(x, b, ids, w), (x, b, w), dout)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            train()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = train()
+    for rep in range(3):
+        with torch.no_grad():
+            x.copy_(normal(x.shape, BF16, 170 + rep))
+            dout.copy_(normal(dout.shape, BF16, 180 + rep))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, e in zip(got, train()):
+            assert torch.equal(a, e), rep
+
+
 def test_side_streams_at_once():
     cases = [step_inputs(900, 110 + i, i & 1) for i in range(4)]
     want = [step(*c) for c in cases]
