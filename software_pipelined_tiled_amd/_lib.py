@@ -277,43 +277,11 @@ def experts_sort_workspace_bytes(slots: int, experts: int) -> int:
     return n.value
 
 
-def experts_sort(ids_ptr: int, id_bits: int, slots: int, experts: int, offsets_ptr: int, order_ptr: int, rows_ptr: int,
-                 workspace_ptr: int = 0, workspace_bytes: int = 0, stream: int = 0) -> None:
-    _check(lib().experts_sort(ids_ptr, id_bits, slots, experts, offsets_ptr, order_ptr,
-                              rows_ptr, workspace_ptr, workspace_bytes, stream), "experts_sort")
-
-
-def experts_gather(x_ptr: int, dtype: int, tokens: int, top_k: int, width: int, ldx: int, rows_ptr: int, kept_ptr: int,
-                   out_ptr: int, ldo: int, zero_rest: bool, stream: int = 0) -> None:
-    _check(lib().experts_gather(x_ptr, dtype, tokens, top_k, width, ldx, rows_ptr, kept_ptr,
-                                out_ptr, ldo, int(zero_rest), stream), "experts_gather")
-
-
-def experts_combine(y_ptr: int, dtype: int, tokens: int, top_k: int, width: int, ldy: int, rows_ptr: int, kept_ptr: int,
-                    weights_ptr: int, weight_dtype: int, out_ptr: int, ldo: int, stream: int = 0) -> None:
-    _check(lib().experts_combine(y_ptr, dtype, tokens, top_k, width, ldy, rows_ptr, kept_ptr,
-                                 weights_ptr, weight_dtype, out_ptr, ldo, stream), "experts_combine")
-
-
-def experts_combine_grad(dout_ptr: int, lddo: int, y_ptr: int, dtype: int, tokens: int, top_k: int, width: int, ldy: int,
-                         rows_ptr: int, kept_ptr: int, weights_ptr: int, weight_dtype: int, dy_ptr: int, lddy: int,
-                         dweights_ptr: int, zero_rest: bool, stream: int = 0) -> None:
-    _check(lib().experts_combine_grad(dout_ptr, lddo, y_ptr, dtype, tokens, top_k, width, ldy,
-                                      rows_ptr, kept_ptr, weights_ptr, weight_dtype, dy_ptr,
-                                      lddy, dweights_ptr, int(zero_rest), stream), "experts_combine_grad")
-
-
 def gemm_grouped_workspace_bytes(p: GemmGrouped, x_ptr: int, y_ptr: int) -> int:
     n = ctypes.c_int64()
     _check(lib().gemm_grouped_workspace_bytes(ctypes.byref(p), x_ptr, y_ptr, ctypes.byref(n)),
            "gemm_grouped_workspace_bytes")
     return n.value
-
-
-def gemm_grouped_run(p: GemmGrouped, x_ptr: int, y_ptr: int, out_ptr: int, offsets_ptr: int, workspace_ptr: int = 0,
-                     workspace_bytes: int = 0, stream: int = 0) -> None:
-    _check(lib().gemm_grouped_run(ctypes.byref(p), x_ptr, y_ptr, out_ptr, offsets_ptr,
-                                  workspace_ptr, workspace_bytes, stream), "gemm_grouped_run")
 
 
 def gemm_w4_packed_bytes(matrices: int, n: int, k: int, group: int, has_zeros: bool) -> int:
@@ -322,19 +290,7 @@ def gemm_w4_packed_bytes(matrices: int, n: int, k: int, group: int, has_zeros: b
     return b.value
 
 
-def gemm_w4_pack(q_ptr: int, scales_ptr: int, zeros_ptr: int, matrices: int, n: int, k: int, group: int, packed_ptr: int,
-                 stream: int = 0) -> None:
-    _check(lib().gemm_w4_pack(q_ptr, scales_ptr, zeros_ptr, matrices, n, k, group,
-                              packed_ptr, stream), "gemm_w4_pack")
-
-
 def gemm_w4_workspace_bytes(p: GemmW4, has_offsets: bool) -> int:
     n = ctypes.c_int64()
     _check(lib().gemm_w4_workspace_bytes(ctypes.byref(p), int(has_offsets), ctypes.byref(n)), "gemm_w4_workspace_bytes")
     return n.value
-
-
-def gemm_w4_run(p: GemmW4, x_ptr: int, packed_ptr: int, offsets_ptr: int, out_ptr: int, workspace_ptr: int = 0,
-                workspace_bytes: int = 0, stream: int = 0) -> None:
-    _check(lib().gemm_w4_run(ctypes.byref(p), x_ptr, packed_ptr, offsets_ptr, out_ptr,
-                             workspace_ptr, workspace_bytes, stream), "gemm_w4_run")

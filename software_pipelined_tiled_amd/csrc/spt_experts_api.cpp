@@ -223,7 +223,7 @@ struct W4Shape {
   int64_t nblocks, row_blocks, splits, ws;
 };
 
-gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
+gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
   if (!p || p->rows < 0 || p->matrices < 0 || p->n < 0 || p->k < 0) return GEMM_ERR_INVALID;
   if (!is_dtype(p->dtype) || !is_dtype(p->out_dtype)) return GEMM_ERR_INVALID;
   if (!is16(p->dtype) || (p->group != 32 && p->group != 64 && p->group != 128)) return GEMM_ERR_UNSUPPORTED;
@@ -241,10 +241,10 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
   };
   // Cut K when the workgroups alone leave compute units idle, into as many parts as still run at once: one
   // workgroup more than compute units is a second round.
-  auto splits = [&](int64_t cus) {
+  auto splits = [&]() {
     const int64_t wgs = s->nblocks * s->row_blocks, most = kb / s->entry.waves;
-    if (wgs <= 0 || wgs >= cus) return (int64_t)1;
-    const int64_t n = cus / wgs < most ? cus / wgs : most;
+    if (wgs <= 0 || wgs >= kCus) return (int64_t)1;
+    const int64_t n = kCus / wgs < most ? kCus / wgs : most;
     return n < 1 ? (int64_t)1 : n;
   };
   // Many blocks of up to 16 rows with short sums: few K parts (64 experts of 1408 x 2048, 64 rows: 21 us
@@ -266,7 +266,7 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
     double least = 0;
     for (int v = 1; v <= 6; ++v) {
       take(v);
-      const int64_t sp = splits(kCus), wgs = s->nblocks * used * ceil_div(each, 16 * s->entry.mt) * sp;
+      const int64_t sp = splits(), wgs = s->nblocks * used * ceil_div(each, 16 * s->entry.mt) * sp;
       const double blocks = (double)ceil_div(ceil_div(kb, sp), s->entry.wk);
       const double us = t[v - 1].start + t[v - 1].block * (blocks + t[v - 1].extra) * (double)ceil_div(wgs, kCus) +
                         (sp > 1 ? 2 + (double)(sp * p->rows * p->n) * 2.4e-6 : 0);
@@ -275,7 +275,7 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, int cu, W4Shape* s) {
     take(best);
   }
   if (s->row_blocks > 65535) return GEMM_ERR_UNSUPPORTED;
-  s->splits = splits(cu);
+  s->splits = splits();
   s->ws = s->splits > 1 ? s->splits * p->rows * p->n * 4 : 0;
   return GEMM_OK;
 }
@@ -503,12 +503,7 @@ gemm_status_t gemm_w4_pack(const uint8_t* q, const void* scales, const uint8_t* 
 gemm_status_t gemm_w4_workspace_bytes(const gemm_w4_t* p, int has_offsets, int64_t* out) {
   if (!out) return GEMM_ERR_INVALID;
   W4Shape s;
-  int cu = 0;
-  gemm_status_t st = w4_shape(p, has_offsets != 0, 1, &s);  // the arguments first, on any host
-  if (st != GEMM_OK) return st;
-  st = device_cus(&cu);
-  if (st != GEMM_OK) return st;
-  st = w4_shape(p, has_offsets != 0, cu, &s);
+  const gemm_status_t st = w4_shape(p, has_offsets != 0, &s);
   if (st == GEMM_OK) *out = s.ws;
   return st;
 }
@@ -517,15 +512,13 @@ gemm_status_t gemm_w4_run(const gemm_w4_t* p, const void* x, const void* packed,
                           void* workspace, int64_t workspace_bytes, void* stream) {
   W4Shape s;
   int cu = 0;
-  gemm_status_t st = w4_shape(p, offsets != nullptr, 1, &s);
+  gemm_status_t st = w4_shape(p, offsets != nullptr, &s);
   if (st != GEMM_OK) return st;
   if (p->rows == 0 || p->n == 0) return GEMM_OK;
   if (!out || (p->k > 0 && (!x || (p->matrices > 0 && (!packed || (uintptr_t)packed % 16 != 0))))) return GEMM_ERR_INVALID;
+  if (s.ws > 0 && (!workspace || (uintptr_t)workspace % 4 != 0 || workspace_bytes < s.ws)) return GEMM_ERR_INVALID;
   st = device_cus(&cu);
   if (st != GEMM_OK) return st;
-  st = w4_shape(p, offsets != nullptr, cu, &s);
-  if (st != GEMM_OK) return st;
-  if (s.ws > 0 && (!workspace || (uintptr_t)workspace % 4 != 0 || workspace_bytes < s.ws)) return GEMM_ERR_INVALID;
   const int gpk = 128 / p->group;
   const int64_t blocks = w4_blocks(p->matrices, p->n, p->k);
   spt::W4Args a;

@@ -24,6 +24,8 @@ from .torch_api import dtype_code
 _16BIT = (torch.float16, torch.bfloat16)
 _FLOATS = (*_16BIT, torch.float32)
 _SORT_ONE = 4096  # slots that one workgroup sorts without a workspace
+_CODES = {t: dtype_code(t) for t in _FLOATS}
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -62,6 +64,8 @@ def _matrix(name: str, t: torch.Tensor, rows: int | None = None, cols: int | Non
         raise ValueError(f"{name} must have {rows} rows, has {r}")
     if cols is not None and c != cols:
         raise ValueError(f"{name} must have {cols} columns, has {c}")
+    if t.is_contiguous():
+        return c
     if c > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     if r <= 1:
@@ -102,9 +106,10 @@ def _offsets(offsets: torch.Tensor, experts: int) -> None:
 
 
 def _type(name: str, t: torch.Tensor, kinds) -> int:
-    if t.dtype not in kinds:
-        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
-    return dtype_code(t.dtype)
+    dtype = t.dtype
+    if dtype not in kinds:
+        raise TypeError(f"unsupported dtype {dtype} of {name}")
+    return _CODES[dtype]
 
 
 def _wants_grad(*tensors) -> bool:
@@ -130,14 +135,16 @@ def _no_autograd(out, *inputs) -> None:
     _need(not _wants_grad(out, *inputs), "out= takes no part in autograd; call under torch.no_grad()")
 
 
-def _enqueue(device: torch.device, fn, *args) -> None:
-    """fn(*args, stream) with `device` current, on its current stream."""
-    index = device.index
-    if index == torch.cuda.current_device():
-        fn(*args, _raw_stream(index))
+def _enqueue(device: torch.device, entry: str, *args) -> None:
+    """The C entry point `entry`(*args, stream) with `device` current, on its current stream."""
+    index, fn = device.index, getattr(_lib.lib(), entry)
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            fn(*args, _raw_stream(index))
+            status = fn(*args, _raw_stream(index))
+    if status:
+        raise _lib.GemmError(status, entry)
 
 
 def _workspace(nbytes: int, device: torch.device):
@@ -200,18 +207,22 @@ def sort_tokens(experts: torch.Tensor, num_experts: int) -> TokenOrder:
     slots = torch.empty(n, dtype=torch.int32, device=dev)
     rows = torch.empty(ids.shape, dtype=torch.int32, device=dev)
     ws = _workspace(ws_bytes, dev)
-    _enqueue(dev, _lib.experts_sort, ids.data_ptr(), bits, n, num_experts, offsets.data_ptr(), slots.data_ptr(),
+    _enqueue(dev, "experts_sort", ids.data_ptr(), bits, n, num_experts, offsets.data_ptr(), slots.data_ptr(),
              rows.data_ptr(), _ptr(ws), ws_bytes)
     return TokenOrder.__new__(TokenOrder)._set(offsets, slots, rows, num_experts)  # nothing to check
 
 
 def _gather(x, order, out):
-    code = _type("x", x, _FLOATS)
-    _on_device("x order", x, order.rows)
+    code, rows, dev = _type("x", x, _FLOATS), order.rows, x.device
+    if not x.is_cuda or rows.device != dev:
+        _on_device("x order", x, rows)
     ldx = _matrix("x", x, order.tokens)
-    width, dev = x.shape[1], x.device
-    out, ldo, fresh = _out(out, order.sorted_rows, width, x.dtype, dev)
-    _enqueue(dev, _lib.experts_gather, x.data_ptr(), code, order.tokens, order.top_k, width, ldx, order.rows.data_ptr(),
+    width = x.shape[1]
+    if out is None:
+        out, ldo, fresh = x.new_empty((order.sorted_rows, width)), width, True
+    else:
+        out, ldo, fresh = _out(out, order.sorted_rows, width, x.dtype, dev)
+    _enqueue(dev, "experts_gather", x.data_ptr(), code, order.tokens, order.top_k, width, ldx, rows.data_ptr(),
              order.kept_ptr, out.data_ptr(), ldo, fresh)
     return out
 
@@ -227,13 +238,17 @@ def _router_weights(weights, order):
 
 
 def _combine(y, order, weights, out):
-    code = _type("y", y, _FLOATS)
-    _on_device("y order weights", y, order.rows, weights)
+    code, rows, dev = _type("y", y, _FLOATS), order.rows, y.device
+    if not y.is_cuda or rows.device != dev or (weights is not None and weights.device != dev):
+        _on_device("y order weights", y, rows, weights)
     ldy = _matrix("y", y, order.sorted_rows)
     weights, wcode = _router_weights(weights, order)
-    width, dev = y.shape[1], y.device
-    out, ldo, _ = _out(out, order.tokens, width, y.dtype, dev)
-    _enqueue(dev, _lib.experts_combine, y.data_ptr(), code, order.tokens, order.top_k, width, ldy, order.rows.data_ptr(),
+    width = y.shape[1]
+    if out is None:
+        out, ldo = y.new_empty((order.tokens, width)), width
+    else:
+        out, ldo, _ = _out(out, order.tokens, width, y.dtype, dev)
+    _enqueue(dev, "experts_combine", y.data_ptr(), code, order.tokens, order.top_k, width, ldy, rows.data_ptr(),
              order.kept_ptr, _ptr(weights), wcode, out.data_ptr(), ldo)
     return out
 
@@ -256,7 +271,7 @@ def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, order: TokenOrder,
     weights, wcode = _router_weights(weights, order)
     dw = torch.empty(order.rows.shape, dtype=weights.dtype, device=dev) if weights is not None else None
     dy = torch.empty((order.sorted_rows, width), dtype=y.dtype, device=dev)
-    _enqueue(dev, _lib.experts_combine_grad, dout.data_ptr(), lddo, y.data_ptr(), code, order.tokens, order.top_k, width,
+    _enqueue(dev, "experts_combine_grad", dout.data_ptr(), lddo, y.data_ptr(), code, order.tokens, order.top_k, width,
              ldy, order.rows.data_ptr(), order.kept_ptr, _ptr(weights), wcode, dy.data_ptr(), width, _ptr(dw), True)
     return dy, dw
 
@@ -317,7 +332,7 @@ def _grouped_run(mode, x, y, out, offsets, rows, experts, n, k, ldx, ldy, ldo, s
     xp, yp = x.data_ptr(), y.data_ptr()
     ws_bytes = _lib.gemm_grouped_workspace_bytes(p, xp, yp)
     ws = _workspace(ws_bytes, x.device)
-    _enqueue(x.device, _lib.gemm_grouped_run, p, xp, yp, out.data_ptr(), offsets.data_ptr(), _ptr(ws), ws_bytes)
+    _enqueue(x.device, "gemm_grouped_run", p, xp, yp, out.data_ptr(), offsets.data_ptr(), _ptr(ws), ws_bytes)
     return out
 
 
@@ -448,7 +463,7 @@ def pack_w4(q: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = 
     q, scales = q.contiguous(), scales.detach().contiguous()
     zeros = zeros.contiguous() if zeros is not None else None
     packed = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _enqueue(q.device, _lib.gemm_w4_pack, q.data_ptr(), scales.data_ptr(), _ptr(zeros), matrices, n, k, group_size,
+    _enqueue(q.device, "gemm_w4_pack", q.data_ptr(), scales.data_ptr(), _ptr(zeros), matrices, n, k, group_size,
              packed.data_ptr())
     return W4Weight(packed, matrices, q.dim() == 3, n, k, group_size, zeros is not None, scales.dtype)
 
@@ -471,14 +486,10 @@ def w4_matmul(x: torch.Tensor, w: W4Weight, offsets: torch.Tensor | None = None,
     dtype = _result_type(out_dtype, out, x.dtype)
     out, ldo, fresh = _out(out, rows, w.n, dtype, dev)
     p = _lib.GemmW4(rows, w.matrices, w.n, w.k, w.group_size, w.has_zeros, code, dtype_code(dtype), ldx, ldo, fresh)
-    _enqueue(dev, _w4_run, p, x, w.packed, offsets, out)
-    return out
-
-
-def _w4_run(p, x, packed, offsets, out, stream):
     ws_bytes = _lib.gemm_w4_workspace_bytes(p, offsets is not None)
-    ws = _workspace(ws_bytes, x.device)
-    _lib.gemm_w4_run(p, x.data_ptr(), packed.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(ws), ws_bytes, stream)
+    ws = _workspace(ws_bytes, dev)
+    _enqueue(dev, "gemm_w4_run", p, x.data_ptr(), w.packed.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(ws), ws_bytes)
+    return out
 
 
 # --------------------------------------------------------------------------------- all together

@@ -245,3 +245,18 @@ def test_routed_matmul_shapes():
     for bad in ((x[0], b, ids), (x, b[0], ids), (x, b, ids[0, 0]), (x, b, ids[:3])):
         with pytest.raises(ValueError):
             spt.routed_matmul(*bad)
+
+
+def test_w4_workspace_and_refusals_of_it():
+    def ws(has_offsets=False, **change):
+        p = dict(rows=4, matrices=1, n=16, k=128, group=64, has_zeros=0, dtype=F16, out_dtype=F16, ldx=128, ldo=16, zero_rest=0)
+        p.update(change)
+        return _lib.gemm_w4_workspace_bytes(_lib.GemmW4(**p), has_offsets)
+    assert ws() == 0  # one block of K
+    assert ws(k=4096, ldx=4096) == 4 * 4 * 16 * 4  # 32 blocks over eight waves: four parts
+    assert ws(n=8192, ldo=8192, k=8192, ldx=8192) == 0  # columns enough
+    with pytest.raises(_lib.GemmError):
+        ws(matrices=2)
+    p = _lib.GemmW4(rows=4, matrices=1, n=16, k=4096, group=64, has_zeros=0, dtype=F16, out_dtype=F16, ldx=4096, ldo=16)
+    for workspace, size in ((None, 0), (A, 1023), (A + 2, 2048)):
+        assert spt.lib().gemm_w4_run(ctypes.byref(p), A, A, None, A, workspace, size, None) == INVALID
