@@ -296,6 +296,21 @@ def test_grouped_many_tiles_of_short_sums(mode, length, tile):
         assert torch.equal(got, ref.to(got.dtype)), out_dtype
 
 
+# the same with 32-row tiles, beyond the longest ring's sizes, aligned and not
+@pytest.mark.parametrize("mode", ["f", "a"])
+@pytest.mark.parametrize("length", [8, 72, 193, 200])
+@pytest.mark.parametrize("width", [2600, 2605])
+def test_grouped_many_small_tiles_of_short_sums(mode, length, width):
+    counts, rest = [300, 0, 1, 129, 900, 0, 255], 300
+    n, k = (width, length) if mode == "f" else (length, width)
+    off = offsets_of(counts)
+    x, y = operands(mode, sum(counts) + rest, len(counts), n, k, lambda s, seed: ints(s, F16, seed))
+    ref, _ = plain_grouped(mode, x, y, off.tolist(), len(counts), n, k)
+    for out_dtype in (F32, F16):
+        got = call_grouped(mode, x, y, off, out_dtype, 32)
+        assert torch.equal(got, ref.to(got.dtype)), out_dtype
+
+
 # a little more than one round of 256 x 256 tiles over 256 compute units, the last tiles a row or a column wide
 @pytest.mark.parametrize("mode", ["f", "a", "b"])
 @pytest.mark.parametrize("length", [1024, 1101])
