@@ -98,7 +98,8 @@ typedef struct {
  * sums run in a fixed order: results do not change from run to run.
  *   Any element alignment and row length will do. The 256-row tiles want whole 16-byte chunks: where they
  * are chosen, an operand whose base, row length, leading dimension or expert stride is not a multiple of
- * 16 bytes is first copied to padded rows in the workspace.
+ * 16 bytes is first copied to padded rows in the workspace. 32-row tiles cut a long sum of few tiles into parts,
+ * fp32 planes in the workspace that a second kernel adds in their order.
  * Errors: GEMM_ERR_INVALID (null pointer, bad enum, negative size, ld or stride too small, workspace
  *         too small), GEMM_ERR_UNSUPPORTED (types; rows beyond 2^31 - 1; more than 2^24 output
  *         tiles; a leading dimension of 2^20 elements or more), GEMM_ERR_HIP.

@@ -130,6 +130,8 @@ struct GroupedArgs {
   int grid;
   int rest;              // zero the output rows behind the last expert
   int nt;                // gradients, 256-row tiles: non-temporal stores
+  int splits;            // 32-row tiles: parts of the sum, each into its fp32 plane at C (1: none)
+  int64_t plane;         // elements between planes
 };
 
 struct PadArgs {
@@ -174,7 +176,7 @@ struct W4Args {
   int out_dtype;
 };
 
-struct W4ReduceArgs {
+struct PlaneArgs {
   const float* parts;
   char* out;
   const int* kept;  // rows that were computed: *kept, or `rows` when null
@@ -191,6 +193,6 @@ struct W4Entry {
 W4Entry w4_entry(int variant, int bf16, int gpk, bool zero);
 const void* w4_pack_fn();
 const void* w4_pack_groups_fn();
-const void* w4_reduce_fn();
+const void* add_planes_fn();
 
 }  // namespace spt

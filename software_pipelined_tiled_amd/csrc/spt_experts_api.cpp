@@ -59,6 +59,23 @@ int stream_grid(int64_t threads) {
   return (int)(b < 1 ? 1 : (b > 8192 ? 8192 : b));
 }
 
+// out = the planes of a cut sum, added in their order
+gemm_status_t add_planes(const float* parts, void* out, const int32_t* kept, int64_t ldo, int64_t rows, int64_t n,
+                         int64_t splits, int out_dtype, int rest, void* stream) {
+  spt::PlaneArgs r;
+  r.parts = parts;
+  r.out = (char*)out;
+  r.kept = kept;
+  r.ldo = ldo;
+  r.plane = rows * n;
+  r.rows = (int)rows;
+  r.n = (int)n;
+  r.splits = (int)splits;
+  r.out_dtype = out_dtype;
+  r.rest = rest;
+  return launch(spt::add_planes_fn(), dim3(stream_grid(r.plane)), 256, 0, &r, stream);
+}
+
 // ---------------------------------------------------------------------------------- sort
 // One workgroup sorts up to kSortOne slots by itself (4096 slots of 64 experts: 6.7 us in one launch, 6.9 in
 // two; 8192: 10.5 against 6.9); beyond, each workgroup takes kSortBlock of them
@@ -101,7 +118,7 @@ struct Operand {
 struct GroupedShape {
   int tile;
   Operand x, y;
-  int64_t ws;
+  int64_t splits, planes, ws;  // parts of a sum; where their planes begin in the workspace
 };
 
 // 32-row tiles: with at most two of them for every compute unit and rows of whole 16-byte chunks, two
@@ -109,12 +126,13 @@ struct GroupedShape {
 // (64 rows, 8 experts, 4096^2: 44 us against 57 with three workgroups of four stages). With more tiles a third
 // workgroup saves a round (200 rows: 59 against 77), and off 16 bytes neighbouring loads share lines, and the
 // hint costs (2044 columns: 56 us against 49).
-bool grouped_few(const gemm_grouped_t* p) {
+int64_t grouped_small_tiles(const gemm_grouped_t* p) {
   const int64_t out_n = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
   const int64_t used = p->experts < p->rows ? p->experts : p->rows;
   const int64_t blocks = used + (p->rows > 16 * used ? (p->rows - 16 * used) / 32 : 0);  // about
-  return blocks * ceil_div(out_n, 64) <= 2 * kCus;
+  return blocks * ceil_div(out_n, 64);
 }
+bool grouped_few(const gemm_grouped_t* p) { return grouped_small_tiles(p) <= 2 * kCus; }
 bool grouped_deep(const gemm_grouped_t* p, const void* Y) {
   return grouped_few(p) && (uintptr_t)Y % 16 == 0 && p->k % 8 == 0 && p->ldy % 8 == 0;
 }
@@ -199,6 +217,21 @@ gemm_status_t grouped_shape(const gemm_grouped_t* p, const void* X, const void* 
     o.at = s->ws;
     o.bytes = round_up(o.rows * o.pad_ld * 2, 256);
     s->ws += o.bytes;
+  }
+  // 32-row tiles that fill less than half of two to a compute unit: parts of the sum of eight K-tiles or more, as
+  // many as run at once, where that spares a workgroup 18 K-tiles (5 us; the second pass costs 4): 2 rows, 8 experts
+  // of 4096^2 21 -> 18.5 us, of 4096 x 14336 67 -> 43, 1 row of 4096^2 20 -> 14; but 2 rows of 4096 x 1536, three
+  // parts, 11.1 -> 11.6, and 8 rows, 64 experts of 1408 x 2048, two parts, 14 -> 16.
+  s->splits = 1;
+  s->planes = s->ws;
+  if (s->tile == 32 && p->rows > 0) {
+    const int64_t tiles = grouped_small_tiles(p), kt = ceil_div(p->mode == GEMM_GROUPED_FORWARD ? p->k : p->n, 64);
+    if (tiles > 0) {
+      const int64_t fit = 2 * kCus / tiles, most = kt / 8;
+      s->splits = fit < most ? fit : most;
+      if (s->splits < 2 || kt - kt / s->splits < 18) s->splits = 1;
+      else s->ws += s->splits * p->rows * oc * 4;
+    }
   }
   return GEMM_OK;
 }
@@ -425,10 +458,11 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   if (s.ws > 0 && (!workspace || (uintptr_t)workspace % 16 != 0 || workspace_bytes < s.ws)) return GEMM_ERR_INVALID;
 
   const bool deep = s.tile == 32 && grouped_deep(p, Y);
-  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, s.tile, deep, p->in_dtype == GEMM_BF16, (int)p->out_dtype);
+  const spt::GroupedEntry entry = spt::grouped_entry((int)p->mode, s.tile, deep, p->in_dtype == GEMM_BF16,
+                                                       s.splits > 1 ? (int)GEMM_F32 : (int)p->out_dtype);
   const int64_t tiles_m = ceil_div(p->n, entry.bm), tiles_n = ceil_div(out_n, entry.bn);
   const int64_t units = gb ? p->experts * tiles_m * tiles_n
-                           : spt::max_row_blocks(p->rows, p->experts, entry.bm) * tiles_n;
+                           : spt::max_row_blocks(p->rows, p->experts, entry.bm) * tiles_n * s.splits;
   if (units > kMaxUnits) return GEMM_ERR_UNSUPPORTED;
   int cu = 0;
   st = device_cus(&cu);
@@ -464,7 +498,15 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   // experts, 4096 x 2048: fp32 258 -> 224 us, bf16 188 -> 159); among long ones they only leave the caches
   // (16384 rows, 8 experts, 8192 x 4096: 886 -> 917).
   a.nt = (gb ? ceil_div(p->rows, p->experts) : a.kc) < 1024;
-  return launch(entry.fn, dim3((unsigned)grid), entry.threads, 0, &a, stream);
+  a.splits = (int)s.splits;
+  a.plane = p->rows * out_n;
+  if (s.splits == 1) return launch(entry.fn, dim3((unsigned)grid), entry.threads, 0, &a, stream);
+  a.C = (char*)workspace + s.planes;
+  a.ldc = out_n;
+  st = launch(entry.fn, dim3((unsigned)grid), entry.threads, 0, &a, stream);
+  if (st != GEMM_OK) return st;
+  return add_planes((const float*)a.C, out, offsets + p->experts, p->ldo, p->rows, out_n, s.splits, (int)p->out_dtype, a.rest,
+                    stream);
 }
 
 gemm_status_t gemm_w4_packed_bytes(int64_t matrices, int64_t n, int64_t k, int group, int has_zeros, int64_t* out) {
@@ -543,18 +585,8 @@ gemm_status_t gemm_w4_run(const gemm_w4_t* p, const void* x, const void* packed,
   st = launch(s.entry.fn, dim3((unsigned)(s.nblocks * s.splits), (unsigned)s.row_blocks), 64 * s.entry.waves, 0, &a,
               stream);
   if (st != GEMM_OK || s.splits == 1) return st;
-  spt::W4ReduceArgs r;
-  r.parts = (const float*)workspace;
-  r.out = (char*)out;
-  r.kept = offsets ? offsets + p->matrices : nullptr;
-  r.ldo = p->ldo;
-  r.plane = a.plane;
-  r.rows = a.rows;
-  r.n = a.n;
-  r.splits = a.splits;
-  r.out_dtype = a.out_dtype;
-  r.rest = a.rest;
-  return launch(spt::w4_reduce_fn(), dim3(stream_grid(a.plane)), 256, 0, &r, stream);
+  return add_planes((const float*)workspace, out, offsets ? offsets + p->matrices : nullptr, p->ldo, p->rows, p->n, s.splits,
+                    a.out_dtype, a.rest, stream);
 }
 
 }  // extern "C"

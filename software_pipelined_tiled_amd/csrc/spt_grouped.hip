@@ -24,6 +24,9 @@
 // offsets (find_group), since the host does not know the counts. K-tiles of 64 stream through a ring
 // of S LDS stages by direct global->LDS loads; one barrier per K-tile.
 //
+// Long sums of few tiles are cut into parts, each into its own fp32 plane, and a second kernel adds the planes in
+// their order (32-row tiles only).
+//
 // What bounds it. Few rows per expert: reading B. 32 x 64 tiles keep 150 KiB of loads on the way per compute
 // unit: 64 rows, 8 experts of 4096 x 4096 in 44 us, 6.2 TB/s where every expert is met (a read-only
 // stream reaches 5456 GB/s; the rest are cache hits). More rows: 128 x 128 tiles, two workgroups a compute unit, whose
@@ -92,9 +95,15 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
     else return tr_frag<2 * BN>(t + tr_offset<BN>(32 * s + 8 * h + (p >> 2), (wn * TN + 16 * f) / 16) + 8 * (p & 3));
   };
 
-  for (int t = xcd_remap(blockIdx.x, a.grid);; t += a.grid) {
-    // this unit: output tile (row0, col0), its row and column counts, and the sum's length
-    int e, row0, rows_left, tm, tn, kc, c0 = 0;
+  constexpr bool kSplit = BM == 32;
+  for (int tp = xcd_remap(blockIdx.x, a.grid);; tp += a.grid) {
+    // this unit: output tile (row0, col0), its row and column counts, the sum's length and its part of it
+    int e, row0, rows_left, tm, tn, kc, c0 = 0, part = 0;
+    int t = tp;
+    if constexpr (kSplit) {
+      t = tp / a.splits;
+      part = tp - t * a.splits;
+    }
     if constexpr (MODE == kGroupedGradB) {
       const int per = a.tiles_m * a.tiles_n;
       e = t / per;
@@ -128,12 +137,17 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
     const int x_more = (TX ? rows_left : kc) & (at_most_1(x_behind) | at_most_1(rows_left - BM));
     const int y_more = (TY ? cols_left : kc) & (at_most_1(y_behind) | at_most_1(cols_left - BN));
     const bool x_patch = ((TX ? rows_left : kc) & 1) != x_more, y_patch = ((TY ? cols_left : kc) & 1) != y_more;
-    auto issue = [&](int kt) SPT_INLINE {
-      const int k0 = kt * BK;
-      const unsigned dst = lds0 + (unsigned)(kt % S) * STAGE;
+    // K-tiles first .. first + kt - 1; `end`: where the part's K-tiles end (or the sum)
+    const int all = (kc + BK - 1) / BK, per = kSplit ? (all + a.splits - 1) / a.splits : all, first = part * per;
+    const int kt = all - first < per ? (all - first < 0 ? 0 : all - first) : per;
+    const int end = (first + kt) * BK < kc ? (first + kt) * BK : kc;
+    const bool last_part = first + kt == all;
+    auto issue = [&](int i) SPT_INLINE {
+      const int k0 = (first + i) * BK;
+      const unsigned dst = lds0 + (unsigned)(i % S) * STAGE;
       // K-tiles past the end read nothing and fill zeros, so every K-tile issues LW loads
       auto rsrc = [&](bool tr, const char* base, int64_t ld, int rows, int width, int odd) SPT_INLINE {
-        const int some = kc > k0;
+        const int some = end > k0;
         const int64_t left = some ? (tr ? kc - k0 : rows) : 1;  // memory rows that may be read
         const int64_t bytes = ((left - 1) * ld + width + odd) * 2 * some;
         return make_rsrc(base + (tr ? (int64_t)k0 * ld * 2 : 0), (uint64_t)bytes);
@@ -160,7 +174,6 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
 #pragma unroll
       for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    const int kt = (kc + BK - 1) / BK;
     // K-tile k's products, from its stage. kCut: the K-tile reaches past kc, whose elements from there on are
     // masked in operands contiguous in c.
     auto products = [&](int k, auto cut_c) SPT_INLINE {
@@ -175,7 +188,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
 #pragma unroll
         for (int f = 0; f < FM; ++f) xf[f] = read_x(xt, s, f);
         if constexpr (kCut) {
-          const int left = kc - k * BK - 32 * s - 8 * h;  // elements of the lane's eight that exist
+          const int left = kc - (first + k) * BK - 32 * s - 8 * h;  // elements of the lane's eight that exist
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             const unsigned keep = left >= 2 * w + 2 ? ~0u : (left == 2 * w + 1 ? 0xFFFFu : 0u);
@@ -197,7 +210,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
     };
     // an operand's very last element, which no load reaches (see the top), into its place in stage `st`
     auto patch = [&](int st) SPT_INLINE {
-      const int c = kc - 1 - (kt - 1) * BK;
+      const int c = kc - 1 - (all - 1) * BK;
       char* xt = smem + st * STAGE;
       if (x_patch && threadIdx.x == 0) {
         const int r = rows_left - 1;
@@ -229,13 +242,13 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
       }
       wait_vmcnt<(S - 2) * LW>();
       barrier_sync();
-      if (x_patch || y_patch) patch((kt - 1) % S);
-      if ((!TX || !TY) && (kc & 7)) products(kt - 1, std::true_type{});
+      if (last_part && (x_patch || y_patch)) patch((kt - 1) % S);
+      if ((!TX || !TY) && last_part && (kc & 7)) products(kt - 1, std::true_type{});
       else products(kt - 1, std::false_type{});
     }
 
     const __amdgpu_buffer_rsrc_t rc = make_rsrc(
-        a.C + ((MODE == kGroupedGradB ? (int64_t)e * a.sc : 0) + (int64_t)row0 * a.ldc) * es,
+        a.C + ((MODE == kGroupedGradB ? (int64_t)e * a.sc : 0) + (kSplit ? part * a.plane : 0) + (int64_t)row0 * a.ldc) * es,
         ((uint64_t)(rows_left - 1) * a.ldc + a.n) * es);
     const bool full = rows_left >= BM && cols_left >= BN;
     if constexpr (OUT == 2) {

@@ -533,9 +533,9 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
   }
 }
 
-// out = the planes added in order, rounded once. With `kept`, rows from *kept on hold zeros or are
+// out = the planes of a cut sum (of these products or the grouped ones) added in order, rounded once. With `kept`, rows from *kept on hold zeros or are
 // left alone.
-__global__ void __launch_bounds__(256) w4_reduce_kernel(W4ReduceArgs r) {
+__global__ void __launch_bounds__(256) add_planes_kernel(PlaneArgs r) {
   const int kept = r.kept && !r.rest ? clampi(*r.kept, 0, r.rows) : r.rows;
   const int64_t total = (int64_t)kept * r.n;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
@@ -581,6 +581,6 @@ W4Entry w4_entry(int variant, int bf16, int gpk, bool zero) {
 }
 const void* w4_pack_fn() { return (const void*)&w4_pack_kernel; }
 const void* w4_pack_groups_fn() { return (const void*)&w4_pack_groups_kernel; }
-const void* w4_reduce_fn() { return (const void*)&w4_reduce_kernel; }
+const void* add_planes_fn() { return (const void*)&add_planes_kernel; }
 
 }  // namespace spt

@@ -414,7 +414,8 @@ def grouped_matmul(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out_
     """C[i] = A[i]·B[e]ᵀ for expert e's rows offsets[e] <= i < offsets[e + 1]: A [rows, k] and B [experts, n, k]
     fp16 or bf16, fp32 sums, C in A's type or ``out_dtype``. ``offsets``: 32-bit, on the device (a
     ``TokenOrder``'s). Rows behind the last expert are zeros in a new tensor, left as they were in ``out``.
-    ``tile``: rows of an output tile, 0 for the library's choice, else 32, 128 or 256 (the same values)."""
+    ``tile``: rows of an output tile, 0 for the library's choice, else 32, 128 or 256 (the same sums, in
+    fp32, which 32-row tiles may add in parts)."""
     if out is not None:
         _no_autograd(out, A, B)
     elif _wants_grad(A, B):

@@ -311,6 +311,33 @@ def test_grouped_many_small_tiles_of_short_sums(mode, length, width):
         assert torch.equal(got, ref.to(got.dtype)), out_dtype
 
 
+# few rows and long sums: parts of the sum in planes, the last part cut by K or empty
+@pytest.mark.parametrize("mode", ["f", "a"])
+@pytest.mark.parametrize("counts,rest", [([1, 0, 1], 0), ([3], 2), ([0, 2, 40, 0, 1], 5), ([0, 0], 4), ([1] * 9, 0)])
+@pytest.mark.parametrize("width,length", [(64, 1536), (146, 5556), (697, 2047), (1000, 4097), (33, 9001), (520, 1600)])
+def test_grouped_long_sums_of_few_tiles(mode, counts, rest, width, length):
+    n, k = (width, length) if mode == "f" else (length, width)
+    rows, experts = sum(counts) + rest, len(counts)
+    off = offsets_of(counts)
+    x, y = operands(mode, rows, experts, n, k, lambda s, seed: ints(s, BF16, seed))
+    ref, _ = plain_grouped(mode, x, y, off.tolist(), experts, n, k)
+    if rest:
+        x[sum(counts):] = float("nan")
+    for tile in (0, 32):
+        for out_dtype in (F32, BF16):
+            got = call_grouped(mode, x, y, off, out_dtype, tile)
+            assert torch.equal(got, ref.to(got.dtype)), (tile, out_dtype)
+    got2 = call_grouped(mode, padded(x, 3, 1), padded(y, 3, 1), off, F32)
+    assert torch.equal(got2, call_grouped(mode, x, y, off, F32))
+    out = torch.full((rows, width + 7), 7.0, dtype=BF16, device="cuda")
+    (spt.grouped_matmul if mode == "f" else spt.grouped_matmul_grad_a)(x, y, off, out=out[:, :width])
+    kept = sum(counts)
+    assert torch.equal(out[:kept, :width], ref[:kept].to(BF16)) and (out[kept:] == 7).all() and (out[:, width:] == 7).all()
+    xr, yr = operands(mode, rows, experts, n, k, lambda s, seed: normal(s, F16, seed))
+    ref, tot = plain_grouped(mode, xr, yr, off.tolist(), experts, n, k)
+    close(call_grouped(mode, xr, yr, off, F16), ref, tot, length, F16)
+
+
 # a little more than one round of 256 x 256 tiles over 256 compute units, the last tiles a row or a column wide
 @pytest.mark.parametrize("mode", ["f", "a", "b"])
 @pytest.mark.parametrize("length", [1024, 1101])

@@ -260,3 +260,16 @@ def test_w4_workspace_and_refusals_of_it():
     p = _lib.GemmW4(rows=4, matrices=1, n=16, k=4096, group=64, has_zeros=0, dtype=F16, out_dtype=F16, ldx=4096, ldo=16)
     for workspace, size in ((None, 0), (A, 1023), (A + 2, 2048)):
         assert spt.lib().gemm_w4_run(ctypes.byref(p), A, A, None, A, workspace, size, None) == INVALID
+
+
+def test_grouped_workspace_of_cut_sums():
+    def ws(**change):
+        return _lib.gemm_grouped_workspace_bytes(grouped(**{"rows": 2, "k": 4096, "ldx": 4096, "ldy": 4096, "stride": 32 * 4096,
+                                                            **change}), A, A)
+    assert ws() == 8 * 2 * 32 * 4                       # two tiles, 64 K-tiles: parts of eight
+    assert ws(tile=128) == 0 and ws(k=1024) == 0
+    assert ws(n=8192, ldo=8192, stride=8192 * 4096) == 2 * 2 * 8192 * 4  # 256 tiles: two parts
+    assert ws(rows=4, n=8192, ldo=8192, stride=8192 * 4096) == 0         # 512: tiles enough
+    p = grouped(rows=2, k=4096, ldx=4096, ldy=4096, stride=32 * 4096)
+    for workspace, size in ((None, 0), (A, 8 * 2 * 32 * 4 - 1), (A + 4, 1 << 20)):
+        assert spt.lib().gemm_grouped_run(ctypes.byref(p), A, A, A, A, workspace, size, None) == INVALID
