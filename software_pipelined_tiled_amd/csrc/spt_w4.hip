@@ -16,7 +16,7 @@
 // vector instructions per 8 weights and lane; at the rate HBM delivers weights that is about a third
 // (two thirds) of the vector issue slots.
 //
-// Work split. Up to four rows a matrix: a workgroup owns 16 or 32 columns, its eight waves take the 128-deep
+// Work split. Few rows, or few columns of a long K: a workgroup owns 16 or 32 columns, its eight waves take the 128-deep
 // blocks of K in turn, straight from memory, and add their sums through LDS in wave order (w4_kernel). More
 // rows: the waves share x in LDS and divide the columns, and with few columns K too (w4_rows_kernel). When
 // that leaves compute units without work, K is cut over workgroups as well, into fp32 planes that a second
