@@ -17,6 +17,7 @@ from dataclasses import dataclass
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import _lib
 from .torch_api import dtype_code
@@ -121,7 +122,8 @@ def _wants_grad(*tensors) -> bool:
 
 
 def _out(out, rows: int, cols: int, dtype, device) -> tuple[torch.Tensor, int, bool]:
-    """The output, its row stride, and whether it is new (then the rows nobody computes are zeroed)."""
+    """The output, its row stride, and whether it is new (then the rows nobody computes are zeroed). One that is not
+    new was written behind torch's back, which ``increment_version`` tells autograd: it may have been saved."""
     if out is None:
         return torch.empty((rows, cols), dtype=dtype, device=device), cols, True
     if out.device != device:
@@ -224,6 +226,8 @@ def _gather(x, order, out):
         out, ldo, fresh = _out(out, order.sorted_rows, width, x.dtype, dev)
     _enqueue(dev, "experts_gather", x.data_ptr(), code, order.tokens, order.top_k, width, ldx, rows.data_ptr(),
              order.kept_ptr, out.data_ptr(), ldo, fresh)
+    if not fresh:
+        increment_version(out)
     return out
 
 
@@ -245,11 +249,13 @@ def _combine(y, order, weights, out):
     weights, wcode = _router_weights(weights, order)
     width = y.shape[1]
     if out is None:
-        out, ldo = y.new_empty((order.tokens, width)), width
+        out, ldo, fresh = y.new_empty((order.tokens, width)), width, True
     else:
-        out, ldo, _ = _out(out, order.tokens, width, y.dtype, dev)
+        out, ldo, fresh = _out(out, order.tokens, width, y.dtype, dev)
     _enqueue(dev, "experts_combine", y.data_ptr(), code, order.tokens, order.top_k, width, ldy, rows.data_ptr(),
              order.kept_ptr, _ptr(weights), wcode, out.data_ptr(), ldo)
+    if not fresh:
+        increment_version(out)
     return out
 
 
@@ -333,6 +339,8 @@ def _grouped_run(mode, x, y, out, offsets, rows, experts, n, k, ldx, ldy, ldo, s
     ws_bytes = _lib.gemm_grouped_workspace_bytes(p, xp, yp)
     ws = _workspace(ws_bytes, x.device)
     _enqueue(x.device, "gemm_grouped_run", p, xp, yp, out.data_ptr(), offsets.data_ptr(), _ptr(ws), ws_bytes)
+    if not fresh:
+        increment_version(out)
     return out
 
 
@@ -490,6 +498,8 @@ def w4_matmul(x: torch.Tensor, w: W4Weight, offsets: torch.Tensor | None = None,
     ws_bytes = _lib.gemm_w4_workspace_bytes(p, offsets is not None)
     ws = _workspace(ws_bytes, dev)
     _enqueue(dev, "gemm_w4_run", p, x.data_ptr(), w.packed.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(ws), ws_bytes)
+    if not fresh:
+        increment_version(out)
     return out
 
 
