@@ -7,6 +7,7 @@ from __future__ import annotations
 from collections import OrderedDict
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib
 
@@ -49,6 +50,11 @@ class Plan:
         _lib.gemm_run(self.handle, a_ptr, b_ptr, c_ptr, stream)
 
     def run(self, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, stream: int | None = None) -> torch.Tensor:
+        self._run(A, B, C, stream)
+        increment_version(C)  # written behind torch's back: autograd may have saved it
+        return C
+
+    def _run(self, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor, stream: int | None) -> None:
         # the kernels touch rows x cols elements at row stride ld from each base pointer
         for name, t, rows, cols, ld, dt in (("A", A, self.M, self.K, self.lda, self.in_dtype),
                                             ("B", B, self.N, self.K, self.ldb, self.in_dtype),
@@ -61,7 +67,6 @@ class Plan:
                                           or t.stride(0) != ld):
                 raise ValueError(f"{name} must be [>= {rows}, >= {cols}] row-major with row stride {ld}")
         self.run_ptrs(A.data_ptr(), B.data_ptr(), C.data_ptr(), stream)
-        return C
 
     def close(self) -> None:
         if self.handle is not None:
@@ -113,4 +118,7 @@ def matmul(A: torch.Tensor, B: torch.Tensor, out_dtype: torch.dtype | None = Non
             _plan_cache[key] = plan
         else:
             _plan_cache.move_to_end(key)
-        return plan.run(A, B, C, stream)
+        if out is not None:
+            return plan.run(A, B, C, stream)
+        plan._run(A, B, C, stream)
+        return C

@@ -66,6 +66,21 @@ def test_a_gather_buffer_used_for_two_batches():
         first.sum().backward()
 
 
+@pytest.mark.parametrize("through", ["matmul", "plan"])
+def test_the_dense_product_writing_a_saved_out_is_seen(through):
+    a, b, buf = ones(4, 32), ones(16, 32), ones(4, 16)
+    experts = ones(1, 8, 16).requires_grad_()
+    off = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    first = spt.grouped_matmul(buf, experts, off)
+    if through == "matmul":
+        spt.matmul(a, b, out=buf)
+    else:
+        spt.Plan(4, 16, 32, BF16, BF16).run(a, b, buf)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        first.sum().backward()
+    assert torch.equal(spt.matmul(a, b), buf)
+
+
 def test_out_made_in_inference_mode():
     with torch.inference_mode():
         order = spt.sort_tokens(torch.tensor([[0], [1]], device="cuda"), 2)
