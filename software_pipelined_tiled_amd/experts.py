@@ -282,30 +282,35 @@ def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, order: TokenOrder,
     return dy, dw
 
 
+# A graph keeps an order's tensors where torch watches what it saves: one that is changed before backward raises.
+
+def _saved_order(rows, offsets) -> TokenOrder:
+    return TokenOrder.__new__(TokenOrder)._set(offsets, None, rows, offsets.numel() - 1)  # backward needs no slots
+
+
 class _Gather(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, order):
-        ctx.order = order
+        ctx.save_for_backward(order.rows, order.offsets)
         return _gather(x, order, None)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dsorted):
-        return gather_rows_grad(_rows_apart(dsorted), ctx.order), None
+        return gather_rows_grad(_rows_apart(dsorted), _saved_order(*ctx.saved_tensors)), None
 
 
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, order, weights):
-        ctx.order = order
-        ctx.save_for_backward(y, weights)
+        ctx.save_for_backward(y, weights, order.rows, order.offsets)
         return _combine(y, order, weights, None)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        y, weights = ctx.saved_tensors
-        dy, dw = combine_rows_grad(_rows_apart(dout), y, ctx.order, weights)
+        y, weights, rows, offsets = ctx.saved_tensors
+        dy, dw = combine_rows_grad(_rows_apart(dout), y, _saved_order(rows, offsets), weights)
         return dy, None, dw
 
 

@@ -1,0 +1,61 @@
+"""Derivatives of the experts' operators: an order changed before backward is seen."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # collected on CPU-only hosts, never run there
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import software_pipelined_tiled_amd as spt  # noqa: E402
+
+BF16 = torch.bfloat16
+
+
+def ones(*shape, dtype=BF16):
+    return torch.ones(shape, dtype=dtype, device="cuda")
+
+
+def operands():
+    ids = torch.tensor([[0, 1], [1, 2], [2, 0], [1, 1]], device="cuda")
+    return ids, spt.sort_tokens(ids, 3), ones(4, 32), ones(8, 32), ones(3, 32, 32), ones(4, 2)
+
+
+# ------------------------------------------------------------------------------- the saved order
+
+@pytest.mark.parametrize("name", ["gather_rows", "combine_rows"])
+@pytest.mark.parametrize("part", ["rows", "offsets"])
+def test_an_order_changed_before_backward_is_seen(name, part):
+    _, order, x, rows, _, w = operands()
+    if name == "gather_rows":
+        out = spt.gather_rows(x.requires_grad_(), order)
+    else:
+        out = spt.combine_rows(rows.requires_grad_(), order, w)
+    getattr(order, part).add_(0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+
+
+def test_saved_orders_through_hooks():
+    # tensors saved for backward may come back as copies
+    ids, _, x, _, b, w = operands()
+    leaves = [t.clone().requires_grad_() for t in (x, b, w)]
+
+    def train():
+        return torch.autograd.grad(spt.routed_matmul(leaves[0], leaves[1], ids, leaves[2]).float().square().sum(), leaves)
+    want = train()
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.cpu(), lambda t: t.cuda()):
+        got = train()
+    for g, e in zip(got, want):
+        assert torch.equal(g, e)
+
+
+@pytest.mark.parametrize("wanted", [(True, False, False), (False, True, False), (False, False, True), (True, False, True)])
+def test_gradients_of_some_inputs_only(wanted):
+    ids, _, x, _, b, w = operands()
+    def grads(which):
+        leaves = [t.clone().requires_grad_(on) for t, on in zip((x, b, w), which)]
+        spt.routed_matmul(leaves[0], leaves[1], ids, leaves[2]).float().square().sum().backward()
+        return [t.grad for t in leaves]
+    for got, want, on in zip(grads(wanted), grads((True, True, True)), wanted):
+        assert torch.equal(got, want) if on else got is None
