@@ -7,9 +7,10 @@ Workspaces come from torch's allocator, so calls on several streams, or captured
 never share one. Rows of a tensor may be any distance apart (unit column stride).
 
 ``gather_rows``, ``combine_rows``, ``grouped_matmul`` and ``routed_matmul`` are differentiable once. The
-``*_grad`` functions are the same gradients as plain calls, for programs that keep no autograd graph. A
-training step captured into a HIP graph is safest with those: while an eager graph of the same leaves is alive, torch's
-backward ties a capture to that graph's stream and ends the process.
+``*_grad`` functions are the same gradients as plain calls, for programs that keep no autograd graph; of tensors that
+require grad they stay in the graph, where differentiating them raises. A training step captured into a HIP graph is
+safest with those: while an eager graph of the same leaves is alive, torch's backward ties a capture to that graph's
+stream and ends the process.
 """
 from __future__ import annotations
 
@@ -157,6 +158,19 @@ def _ptr(t) -> int:
     return t.data_ptr() if t is not None else 0
 
 
+class _Once(torch.autograd.Function):
+    """A gradient of tensors that a graph holds: it stays in the graph, and differentiating it raises there instead of
+    leaving a term out."""
+    @staticmethod
+    def forward(ctx, gradient, *args):
+        return gradient(*args)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the experts' operators are differentiable once; call their gradients under torch.no_grad() "
+                           "where they are constants")
+
+
 # ---------------------------------------------------------------------------- tokens by expert
 
 class TokenOrder:
@@ -261,13 +275,19 @@ def _combine(y, order, weights, out):
 
 def gather_rows_grad(dsorted: torch.Tensor, order: TokenOrder, out: torch.Tensor | None = None) -> torch.Tensor:
     """Gradient of ``gather_rows``: each token's sum over its kept rows of ``dsorted``, in fp32, rounded once."""
-    return _combine(dsorted.detach(), order, None, out)
+    if out is not None:
+        _no_autograd(out, dsorted)
+    elif _wants_grad(dsorted):
+        return _Once.apply(gather_rows_grad, dsorted, order)
+    return _combine(dsorted, order, None, out)
 
 
 def combine_rows_grad(dout: torch.Tensor, y: torch.Tensor, order: TokenOrder,
                       weights: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
     """Gradients of ``combine_rows`` for y and the weights (None without weights), in their types. Rows
     and weights of dropped slots get zeros."""
+    if _wants_grad(dout, y, weights):
+        return _Once.apply(combine_rows_grad, dout, y, order, weights)
     code = _type("y", y, _FLOATS)
     _on_device("y dout order weights", y, dout, order.rows, weights)
     _need(dout.dtype == y.dtype, "dout must have y's dtype")
@@ -372,6 +392,10 @@ def grouped_matmul_grad_a(dC: torch.Tensor, B: torch.Tensor, offsets: torch.Tens
                           tile: int = 0) -> torch.Tensor:
     """Gradient of ``grouped_matmul`` for A: dA[i] = dC[i]·B[e] for expert e's rows i, in dC's type. Rows behind
     the last expert: zeros in a new tensor, left as they were in ``out``."""
+    if out is not None:
+        _no_autograd(out, dC, B)
+    elif _wants_grad(dC, B):
+        return _Once.apply(grouped_matmul_grad_a, dC, B, offsets, None, tile)
     _type("dC", dC, _16BIT)
     _need(B.dtype == dC.dtype, "B must have dC's dtype")
     _on_device("dC B offsets", dC, B, offsets)
@@ -379,8 +403,6 @@ def grouped_matmul_grad_a(dC: torch.Tensor, B: torch.Tensor, offsets: torch.Tens
     lddc = _matrix("dC", dC, None, N)
     _offsets(offsets, E)
     rows = dC.shape[0]
-    if out is not None:
-        _no_autograd(out)
     dA, lda, fresh = _out(out, rows, K, dC.dtype, dC.device)
     return _grouped_run(_lib.GEMM_GROUPED_GRAD_A, dC, B, dA, offsets, rows, E, N, K, lddc, ldb, lda, stride, fresh,
                         tile)
@@ -391,6 +413,8 @@ def grouped_matmul_grad_b(dC: torch.Tensor, A: torch.Tensor, offsets: torch.Tens
     """Gradient of ``grouped_matmul`` for B, [experts, n, k]: dB[e] = sum over expert e's rows i of
     dC[i]ᵀ·A[i], in A's type or ``out_dtype`` (fp32 for a main copy of the weights); zeros for an expert
     without rows."""
+    if _wants_grad(dC, A):
+        return _Once.apply(grouped_matmul_grad_b, dC, A, offsets, out_dtype, tile)
     _type("A", A, _16BIT)
     _need(dC.dtype == A.dtype, "dC must have A's dtype")
     _on_device("A dC offsets", A, dC, offsets)

@@ -1,4 +1,5 @@
-"""Derivatives of the experts' operators: an order changed before backward is seen."""
+"""Derivatives of the experts' operators: an order changed before backward is seen, and the derivative of a gradient,
+which there is none of, is refused and not left out."""
 import pytest
 import torch
 
@@ -59,3 +60,52 @@ def test_gradients_of_some_inputs_only(wanted):
         return [t.grad for t in leaves]
     for got, want, on in zip(grads(wanted), grads((True, True, True)), wanted):
         assert torch.equal(got, want) if on else got is None
+
+
+# ---------------------------------------------------------------------- derivatives of the gradients
+
+def gradient_calls():
+    """name -> (the call on its tensors, the tensors)"""
+    _, order, x, rows, b, w = operands()
+    off = order.offsets
+    return {
+        "gather_rows_grad": (lambda d: spt.gather_rows_grad(d, order), [rows]),
+        "combine_rows_grad": (lambda d, y, w: spt.combine_rows_grad(d, y, order, w), [x, rows, w]),
+        "combine_rows_grad without weights": (lambda d, y: spt.combine_rows_grad(d, y, order)[0], [x, rows]),
+        "grouped_matmul_grad_a": (lambda d, b: spt.grouped_matmul_grad_a(d, b, off), [rows, b]),
+        "grouped_matmul_grad_b": (lambda d, a: spt.grouped_matmul_grad_b(d, a, off, torch.float32), [rows, rows.clone()]),
+    }
+
+
+@pytest.mark.parametrize("name,which", [("gather_rows_grad", 0), ("combine_rows_grad", 0), ("combine_rows_grad", 1),
+                                        ("combine_rows_grad", 2), ("combine_rows_grad without weights", 0),
+                                        ("grouped_matmul_grad_a", 0), ("grouped_matmul_grad_a", 1),
+                                        ("grouped_matmul_grad_b", 0), ("grouped_matmul_grad_b", 1)])
+def test_a_gradient_of_a_gradient_raises(name, which):
+    call, args = gradient_calls()[name]
+    def each(r):
+        return r if isinstance(r, tuple) else (r,)
+    want = each(call(*args))
+    leaf = args[which].clone().requires_grad_()
+    args[which] = leaf
+    got = each(call(*args))
+    for g, e in zip(got, want):
+        assert torch.equal(g, e)
+        # beside a term that has its derivative, so that a lost one would not be noticed
+        with pytest.raises(RuntimeError, match="differentiable once"):
+            (leaf.float().sum() + g.float().square().sum()).backward()
+    with torch.no_grad():
+        assert not any(g.requires_grad for g in each(call(*args)))
+
+
+def test_out_takes_no_part_in_a_graph():
+    _, order, _, rows, b, _ = operands()
+    leaf = rows.clone().requires_grad_()
+    for call in (lambda: spt.gather_rows_grad(leaf, order, out=ones(4, 32)),
+                 lambda: spt.gather_rows_grad(rows, order, out=ones(4, 32).requires_grad_()),
+                 lambda: spt.grouped_matmul_grad_a(leaf, b, order.offsets, out=ones(8, 32)),
+                 lambda: spt.grouped_matmul_grad_a(rows, b.clone().requires_grad_(), order.offsets, out=ones(8, 32))):
+        with pytest.raises(ValueError, match="no part in autograd"):
+            call()
+        with torch.no_grad():
+            call()
