@@ -486,7 +486,8 @@ def pack_w4(q: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = 
             group_size: int = 128) -> W4Weight:
     """Lay out weights (q - z) * s: q [n, k] or [experts, n, k] bytes holding 0 .. 15 (the low four bits are
     taken), scales [..., n, ceil(k / group_size)] fp16 or bf16 (the products' type), zeros bytes of the same
-    shape, or None for z = 8. group_size 32, 64 or 128."""
+    shape, or None for z = 8. group_size 32, 64 or 128. No gradient for the scales."""
+    _need(not _wants_grad(scales), "pack_w4 has no gradient for the scales; call under torch.no_grad()")
     _need(q.dtype == torch.uint8 and q.dim() in (2, 3), "q must be [n, k] or [experts, n, k] bytes")
     _type("scales", scales, _16BIT)
     _on_device("q scales zeros", q, scales, zeros)
@@ -498,7 +499,7 @@ def pack_w4(q: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = 
     _need(zeros is None or (zeros.dtype == torch.uint8 and tuple(zeros.shape) == shape), f"zeros must be bytes {shape}")
     matrices = q.shape[0] if q.dim() == 3 else 1
     nbytes = _lib.gemm_w4_packed_bytes(matrices, n, k, group_size, zeros is not None)
-    q, scales = q.contiguous(), scales.detach().contiguous()
+    q, scales = q.contiguous(), scales.contiguous()
     zeros = zeros.contiguous() if zeros is not None else None
     packed = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     _enqueue(q.device, "gemm_w4_pack", q.data_ptr(), scales.data_ptr(), _ptr(zeros), matrices, n, k, group_size,

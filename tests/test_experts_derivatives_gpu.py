@@ -1,5 +1,5 @@
-"""Derivatives of the experts' operators: an order changed before backward is seen, and the derivative of a gradient,
-which there is none of, is refused and not left out."""
+"""Derivatives of the experts' operators: an order changed before backward is seen, and derivatives that the operators
+do not have (of a gradient, of the scales) are refused, not left out."""
 import pytest
 import torch
 
@@ -109,3 +109,15 @@ def test_out_takes_no_part_in_a_graph():
             call()
         with torch.no_grad():
             call()
+
+
+# ---------------------------------------------------------------------------------- the scales
+
+def test_scales_that_require_grad_are_refused():
+    q = torch.full((32, 32), 9, dtype=torch.uint8, device="cuda")
+    s = ones(32, 1).requires_grad_()
+    with pytest.raises(ValueError, match="no gradient"):
+        spt.pack_w4(q, s, group_size=32)
+    with torch.no_grad():
+        w = spt.pack_w4(q, s, group_size=32)
+    assert torch.equal(spt.w4_matmul(ones(4, 32), w), 32 * ones(4, 32))
