@@ -6,17 +6,18 @@ Every call enqueues on its tensors' device, on that device's current stream, and
 Workspaces come from torch's allocator, so calls on several streams, or captured into several graphs,
 never share one. Rows of a tensor may be any distance apart (unit column stride).
 
-``gather_rows``, ``combine_rows``, ``grouped_matmul`` and ``routed_matmul`` are differentiable once. The
-``*_grad`` functions are the same gradients as plain calls, for programs that keep no autograd graph; of tensors that
-require grad they stay in the graph, where differentiating them raises. A training step captured into a HIP graph is
-safest with those: while an eager graph of the same leaves is alive, torch's backward ties a capture to that graph's
-stream and ends the process.
+``gather_rows``, ``combine_rows``, ``grouped_matmul`` and ``routed_matmul`` are differentiable once, in reverse mode;
+operands with a forward-mode tangent are refused. The ``*_grad`` functions are the same gradients as plain calls, for
+programs that keep no autograd graph; of tensors that require grad they stay in the graph, where differentiating them
+raises. A training step captured into a HIP graph is safest with those: while an eager graph of the same leaves is alive,
+torch's backward ties a capture to that graph's stream and ends the process.
 """
 from __future__ import annotations
 
 from dataclasses import dataclass
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 from torch.autograd.graph import increment_version
 
@@ -114,7 +115,18 @@ def _type(name: str, t: torch.Tensor, kinds) -> int:
     return _CODES[dtype]
 
 
+def _refuse_tangents(tensors) -> None:
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError("the experts' operators have no forward-mode derivative; pass the primal "
+                             "(torch.autograd.forward_ad.unpack_dual)")
+
+
 def _wants_grad(*tensors) -> bool:
+    """Whether these operands make the call part of a graph. Every call asks, so that operands with a tangent, which
+    the kernels' results would not carry, are refused here; they exist only inside a dual level."""
+    if getattr(forward_ad, "_current_level", 0) >= 0:
+        _refuse_tangents(tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:

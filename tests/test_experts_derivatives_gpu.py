@@ -1,7 +1,8 @@
 """Derivatives of the experts' operators: an order changed before backward is seen, and derivatives that the operators
-do not have (of a gradient, of the scales) are refused, not left out."""
+do not have (of a gradient, of the scales, in forward mode) are refused, not left out."""
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +122,45 @@ def test_scales_that_require_grad_are_refused():
     with torch.no_grad():
         w = spt.pack_w4(q, s, group_size=32)
     assert torch.equal(spt.w4_matmul(ones(4, 32), w), 32 * ones(4, 32))
+
+
+# ---------------------------------------------------------------------------------- forward mode
+
+def test_tensors_with_a_tangent_are_refused():
+    ids, order, x, rows, b, w = operands()
+    off = order.offsets
+    q = torch.full((32, 32), 9, dtype=torch.uint8, device="cuda")
+    w4 = spt.pack_w4(q, ones(32, 1), group_size=32)
+    with forward_ad.dual_level():
+        def dual(t):
+            return forward_ad.make_dual(t, torch.ones_like(t))
+        bad = [
+            lambda: spt.gather_rows(dual(x), order), lambda: spt.gather_rows(dual(x), order, out=rows.clone()),
+            lambda: spt.gather_rows(x, order, out=dual(rows.clone())),
+            lambda: spt.combine_rows(dual(rows), order), lambda: spt.combine_rows(rows, order, dual(w)),
+            lambda: spt.grouped_matmul(dual(rows), b, off), lambda: spt.grouped_matmul(rows, dual(b), off),
+            lambda: spt.w4_matmul(dual(x), w4), lambda: spt.w4_matmul(x, w4, out=dual(x.clone())),
+            lambda: spt.pack_w4(q, dual(ones(32, 1)), group_size=32),
+            lambda: spt.gather_rows_grad(dual(rows), order), lambda: spt.gather_rows_grad(rows, order, out=dual(x.clone())),
+            lambda: spt.combine_rows_grad(dual(x), rows, order), lambda: spt.combine_rows_grad(x, dual(rows), order),
+            lambda: spt.combine_rows_grad(x, rows, order, dual(w)),
+            lambda: spt.grouped_matmul_grad_a(dual(rows), b, off), lambda: spt.grouped_matmul_grad_a(rows, dual(b), off),
+            lambda: spt.grouped_matmul_grad_b(dual(rows), rows, off), lambda: spt.grouped_matmul_grad_b(rows, dual(rows), off),
+            lambda: spt.routed_matmul(dual(x), b, ids, w), lambda: spt.routed_matmul(x, dual(b), ids, w),
+            lambda: spt.routed_matmul(x, b, ids, dual(w)),
+            lambda: spt.gather_rows(dual(x.clone().requires_grad_()), order),
+        ]
+        for i, call in enumerate(bad):
+            for mode in (torch.no_grad, torch.enable_grad):
+                with mode(), pytest.raises(ValueError, match="forward-mode"):
+                    call()
+                    print("not refused:", i)
+        # tensors without a tangent pass inside a level, and so does a backward of them
+        leaf = x.clone().requires_grad_()
+        spt.routed_matmul(leaf, b, ids, w).sum().backward()
+        assert leaf.grad is not None
+        # a gradient that arrives with a tangent
+        out = spt.gather_rows(leaf, order)
+        with pytest.raises(ValueError, match="forward-mode"):
+            torch.autograd.grad(out, leaf, dual(torch.ones_like(out)))
+    assert torch.equal(spt.gather_rows(x, order), rows)
