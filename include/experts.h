@@ -132,7 +132,8 @@ gemm_status_t gemm_w4_pack(const uint8_t* q, const void* scales, const uint8_t* 
  * stay inside fp32's range), and the result is rounded once. Rows behind the last expert: zero_rest
  * as above. With few columns the sum over k is split over workgroups, into planes in the workspace.
  * Errors: GEMM_ERR_INVALID, GEMM_ERR_UNSUPPORTED (types; group; n or k beyond 2^24; ldx of 2^23 or
- *         more; more than 65535 blocks of rows), GEMM_ERR_HIP.
+ *         more; more than 65535 blocks of 64 rows: 4194240 rows of one matrix, and with offsets
+ *         (rows - g) / 64 + g blocks, g = min(matrices + 1, rows)), GEMM_ERR_HIP.
  */
 typedef struct {
   int64_t rows, matrices, n, k;

@@ -14,6 +14,7 @@ constexpr int kMaxExperts = 1024;
 // smallest tiles these are 2^35 elements.
 constexpr int64_t kMaxUnits = (int64_t)1 << 24;
 constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxGridY = 65535;
 constexpr int kCus = 256;  // the MI355X's, for choices that must not depend on the device in use
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -103,7 +104,7 @@ gemm_status_t route_grid(int64_t tokens, int64_t width, int* lanes_log2, dim3* g
   int l = 0;
   while (l < 8 && ((int64_t)1 << l) < chunks) ++l;
   const int64_t gx = ceil_div(tokens, 256 >> l), gy = ceil_div(chunks, (int64_t)1 << l);
-  if (gx * 256 > kMax32 || gy > 65535) return GEMM_ERR_UNSUPPORTED;
+  if (gx * 256 > kMax32 || gy > kMaxGridY) return GEMM_ERR_UNSUPPORTED;
   *lanes_log2 = l;
   *grid = dim3((unsigned)gx, (unsigned)gy);
   return GEMM_OK;
@@ -288,26 +289,29 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
   // pass over a split sum. Its constants are a fit to 1320 measured shapes (N 512 .. 28672, K 1024 .. 14336, 1 ..
   // 2000 rows, up to 64 experts). The choice takes 2 % longer than the best kernel of each shape, 39 % at worst; a
   // rule on the number of 16 x 16 output blocks alone took 9 %, 95 % at worst.
-  if (each <= 16 && kb <= 16 && p->matrices > 1 && n16 * used >= 1536) {
-    take(7);
-  } else if (each <= 4) {
-    take(n16 * used <= kCus ? 0 : 1);
-  } else {
+  // Blocks of rows are the grid's second dimension: where a kernel's are too many, only those with more rows a block
+  // are candidates.
+  int chosen = -1;
+  if (each <= 16 && kb <= 16 && p->matrices > 1 && n16 * used >= 1536) chosen = 7;
+  else if (each <= 4) chosen = n16 * used <= kCus ? 0 : 1;
+  if (chosen >= 0) take(chosen);
+  if (chosen < 0 || s->row_blocks > kMaxGridY) {
     struct { double start, block, extra; } const t[] = {
         {3.9, 1.03, 0.7}, {3.5, .82, 1.6}, {3.4, 1.19, 1.8}, {4.8, .96, 1.4}, {5.3, .73, 1.9}, {3.4, 1.27, 3.1}};
     int best = 0;
     double least = 0;
     for (int v = 1; v <= 6; ++v) {
       take(v);
+      if (s->row_blocks > kMaxGridY) continue;
       const int64_t sp = splits(), wgs = s->nblocks * used * ceil_div(each, 16 * s->entry.mt) * sp;
       const double blocks = (double)ceil_div(ceil_div(kb, sp), s->entry.wk);
       const double us = t[v - 1].start + t[v - 1].block * (blocks + t[v - 1].extra) * (double)ceil_div(wgs, kCus) +
                         (sp > 1 ? 2 + (double)(sp * p->rows * p->n) * 2.4e-6 : 0);
       if (best == 0 || us < least) best = v, least = us;
     }
+    if (best == 0) return GEMM_ERR_UNSUPPORTED;
     take(best);
   }
-  if (s->row_blocks > 65535) return GEMM_ERR_UNSUPPORTED;
   s->splits = splits();
   s->ws = s->splits > 1 ? s->splits * p->rows * p->n * 4 : 0;
   return GEMM_OK;
