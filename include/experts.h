@@ -102,7 +102,8 @@ typedef struct {
  * fp32 planes in the workspace that a second kernel adds in their order.
  * Errors: GEMM_ERR_INVALID (null pointer, bad enum, negative size, ld or stride too small, workspace
  *         too small), GEMM_ERR_UNSUPPORTED (types; rows beyond 2^31 - 1; more than 2^24 output
- *         tiles; a leading dimension of 2^20 elements or more), GEMM_ERR_HIP.
+ *         tiles; a leading dimension of 2^20 elements or more; experts times stride beyond 2^54 elements),
+ *         GEMM_ERR_HIP.
  */
 gemm_status_t gemm_grouped_workspace_bytes(const gemm_grouped_t* p, const void* X, const void* Y, int64_t* out);
 gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const void* Y, void* out,
@@ -118,7 +119,8 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
  * gemm_w4_pack lays them out for gemm_w4_run, once: q is [matrices, n, k] with one value per byte
  * (the low four bits), scales [matrices, n, ceil(k / group)] 16-bit, zeros the same shape in bytes
  * (low four bits) or NULL, all contiguous; `packed` is gemm_w4_packed_bytes long and 16-byte aligned.
- * Errors: GEMM_ERR_INVALID, GEMM_ERR_UNSUPPORTED (group; n or k beyond 2^24), GEMM_ERR_HIP.
+ * Errors: GEMM_ERR_INVALID, GEMM_ERR_UNSUPPORTED (group; matrices, n or k beyond 2^24; more than 2^45
+ *         blocks of 16 n by 128 k), GEMM_ERR_HIP.
  */
 gemm_status_t gemm_w4_packed_bytes(int64_t matrices, int64_t n, int64_t k, int group, int has_zeros, int64_t* out);
 gemm_status_t gemm_w4_pack(const uint8_t* q, const void* scales, const uint8_t* zeros, int64_t matrices, int64_t n,
@@ -131,8 +133,8 @@ gemm_status_t gemm_w4_pack(const uint8_t* q, const void* scales, const uint8_t* 
  * group's sum is fp32 and multiplied by its scale in fp32 (the sum of x * (q - z) over a group has to
  * stay inside fp32's range), and the result is rounded once. Rows behind the last expert: zero_rest
  * as above. With few columns the sum over k is split over workgroups, into planes in the workspace.
- * Errors: GEMM_ERR_INVALID, GEMM_ERR_UNSUPPORTED (types; group; n or k beyond 2^24; ldx of 2^23 or
- *         more; more than 65535 blocks of 64 rows: 4194240 rows of one matrix, and with offsets
+ * Errors: GEMM_ERR_INVALID, GEMM_ERR_UNSUPPORTED (types; group; a weight that gemm_w4_pack refuses; ldx of
+ *         2^23 or more; more than 65535 blocks of 64 rows: 4194240 rows of one matrix, and with offsets
  *         (rows - g) / 64 + g blocks, g = min(matrices + 1, rows)), GEMM_ERR_HIP.
  */
 typedef struct {

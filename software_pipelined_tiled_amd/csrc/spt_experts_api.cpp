@@ -14,6 +14,8 @@ constexpr int kMaxExperts = 1024;
 // smallest tiles these are 2^35 elements.
 constexpr int64_t kMaxUnits = (int64_t)1 << 24;
 constexpr int kMaxDevices = 64;
+// Bytes of one operand: byte counts and offsets stay inside 64 bits, and no memory is as large.
+constexpr int64_t kMaxBytes = (int64_t)1 << 56;
 constexpr int64_t kMaxGridY = 65535;
 constexpr int kCus = 256;  // the MI355X's, for choices that must not depend on the device in use
 
@@ -197,9 +199,11 @@ gemm_status_t grouped_shape(const gemm_grouped_t* p, const void* X, const void* 
   const int64_t xc = p->mode == GEMM_GROUPED_FORWARD ? p->k : p->n;
   const int64_t oc = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
   if (p->ldx < xc || p->ldy < p->k || p->ldo < oc) return GEMM_ERR_INVALID;
-  const int64_t mat_ld = gb ? p->ldo : p->ldy;  // of the [experts, n, k] tensor
-  if (p->experts > 1 && p->n > 0 && p->stride < (p->n - 1) * mat_ld + p->k) return GEMM_ERR_INVALID;
   if (p->ldx >= lim || p->ldy >= lim || p->ldo >= lim) return GEMM_ERR_UNSUPPORTED;
+  const int64_t mat_ld = gb ? p->ldo : p->ldy;  // of the [experts, n, k] tensor
+  const int64_t span = p->n > 0 ? (p->n - 1) * mat_ld + p->k : 0;
+  if (p->experts > 1 && p->stride < span) return GEMM_ERR_INVALID;
+  if (p->experts > 0 && (p->stride > span ? p->stride : span) > kMaxBytes / 4 / p->experts) return GEMM_ERR_UNSUPPORTED;
   s->x = Operand{p->rows, xc, p->ldx, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
   if (gb) s->y = Operand{p->rows, p->k, p->ldy, p->rows > 0 ? p->rows : 1, 0, false, 0, 0, 0};
   else s->y = Operand{p->experts * p->n, p->k, p->ldy, p->n > 0 ? p->n : 1, p->stride, false, 0, 0, 0};
@@ -252,6 +256,14 @@ gemm_status_t pad_operand(Operand& o, const void** ptr, char* ws, void* stream) 
 }
 
 // ---------------------------------------------------------------------------------- 4-bit weights
+int64_t w4_blocks(int64_t matrices, int64_t n, int64_t k) { return matrices * ceil_div(n, 16) * ceil_div(k, 128); }
+
+// n and k up to 2^24 leave a matrix up to 2^37 blocks, of at most 1024 + 16 * 4 * 3 bytes
+bool w4_too_large(int64_t matrices, int64_t n, int64_t k) {
+  const int64_t each = w4_blocks(1, n, k);
+  return each > 0 && matrices > kMaxBytes / 2048 / each;
+}
+
 struct W4Shape {
   spt::W4Entry entry;
   int64_t nblocks, row_blocks, splits, ws;
@@ -263,7 +275,8 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
   if (!is16(p->dtype) || (p->group != 32 && p->group != 64 && p->group != 128)) return GEMM_ERR_UNSUPPORTED;
   if (p->ldx < p->k || p->ldo < p->n || (!grouped && p->matrices != 1)) return GEMM_ERR_INVALID;
   const int64_t lim = (int64_t)1 << 24;
-  if (p->n > lim || p->k > lim || p->ldx >= lim / 2 || p->rows > kMax32 || p->matrices > kMax32)
+  if (p->n > lim || p->k > lim || p->ldx >= lim / 2 || p->rows > kMax32 || p->matrices > kMax32 ||
+      w4_too_large(p->matrices, p->n, p->k))
     return GEMM_ERR_UNSUPPORTED;
   const int64_t n16 = ceil_div(p->n, 16), kb = ceil_div(p->k, 128);
   const int64_t each = p->matrices > 0 ? ceil_div(p->rows, p->matrices) : 0;  // rows that share a matrix, on average
@@ -316,8 +329,6 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
   s->ws = s->splits > 1 ? s->splits * p->rows * p->n * 4 : 0;
   return GEMM_OK;
 }
-
-int64_t w4_blocks(int64_t matrices, int64_t n, int64_t k) { return matrices * ceil_div(n, 16) * ceil_div(k, 128); }
 
 }  // namespace
 
@@ -516,7 +527,9 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
 gemm_status_t gemm_w4_packed_bytes(int64_t matrices, int64_t n, int64_t k, int group, int has_zeros, int64_t* out) {
   if (!out || matrices < 0 || n < 0 || k < 0) return GEMM_ERR_INVALID;
   const int64_t lim = (int64_t)1 << 24;
-  if ((group != 32 && group != 64 && group != 128) || n > lim || k > lim || matrices > lim) return GEMM_ERR_UNSUPPORTED;
+  if ((group != 32 && group != 64 && group != 128) || n > lim || k > lim || matrices > lim ||
+      w4_too_large(matrices, n, k))
+    return GEMM_ERR_UNSUPPORTED;
   *out = w4_blocks(matrices, n, k) * (1024 + 16 * (128 / group) * (has_zeros ? 3 : 2));
   return GEMM_OK;
 }

@@ -31,3 +31,36 @@ def test_rows_of_one_4_bit_weight(n, k, rows, status):
     (70_000, 70_000, 16, 128, UNSUPPORTED)])                       # a block for each row
 def test_rows_of_4_bit_experts(rows, matrices, n, k, status):
     assert w4_status(rows, n, k, matrices, offsets=True) == status
+
+
+# Sizes whose byte counts would pass 64 bits: no such operand exists, and the counts came out small or negative
+@pytest.mark.parametrize("matrices,n,k,status", [
+    (1 << 24, 1 << 24, 1 << 24, UNSUPPORTED), (1 << 24, 1 << 24, 1 << 20, UNSUPPORTED), (1 << 24, 16, 128, OK),
+    (1, 1 << 24, 1 << 24, OK), (256, 1 << 24, 1 << 24, OK), (257, 1 << 24, 1 << 24, UNSUPPORTED)])
+@pytest.mark.parametrize("group,zeros", [(32, 1), (128, 0)])
+def test_bytes_of_4_bit_weights(matrices, n, k, status, group, zeros):
+    b = ctypes.c_int64(-5)
+    assert spt.lib().gemm_w4_packed_bytes(matrices, n, k, group, zeros, ctypes.byref(b)) == status
+    if status == OK:
+        assert b.value == matrices * -(-n // 16) * -(-k // 128) * (1024 + 16 * 128 // group * (2 + zeros))
+    else:
+        assert spt.lib().gemm_w4_pack(0x1000, 0x1000, None, matrices, n, k, group, 0x1000, None) == UNSUPPORTED
+        assert w4_status(4, n, k, matrices, offsets=True) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("mode", [_lib.GEMM_GROUPED_FORWARD, _lib.GEMM_GROUPED_GRAD_A, _lib.GEMM_GROUPED_GRAD_B])
+@pytest.mark.parametrize("change,status", [
+    (dict(experts=2**31 - 1, n=2**19 + 1, stride=2**39, ld=2**19 + 1), UNSUPPORTED),
+    (dict(experts=2**31 - 1, n=2**19 + 1, stride=2**62, ld=2**19 + 1), UNSUPPORTED), (dict(stride=2**63 - 1), UNSUPPORTED),
+    (dict(experts=1, stride=2**63 - 1), UNSUPPORTED), (dict(stride=2**40), OK),
+    (dict(n=2**19 + 1, ld=2**62, stride=2**40), UNSUPPORTED)])  # rows of the matrices too far apart for the products
+def test_bytes_of_experts(mode, change, status):
+    c = dict(experts=4, n=32, stride=32 * 48, ld=48)
+    c.update(change)
+    gb = mode == _lib.GEMM_GROUPED_GRAD_B
+    wide = 2**19 + 1  # at least n and k
+    p = _lib.GemmGrouped(mode=mode, rows=3, experts=c["experts"], n=c["n"], k=min(c["ld"], 48), in_dtype=BF16, out_dtype=BF16,
+                         ldx=wide, ldy=wide if gb else c["ld"], ldo=c["ld"] if gb else wide, stride=c["stride"], tile=256)
+    b = ctypes.c_int64(0)
+    got = spt.lib().gemm_grouped_workspace_bytes(ctypes.byref(p), 0x1000, 0x1000, ctypes.byref(b))
+    assert got == status and b.value >= 0
