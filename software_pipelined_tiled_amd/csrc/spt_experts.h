@@ -31,7 +31,8 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // Unit u's expert, where every block of `bm` rows holds `per` units: a wave reads 64 experts'
 // offsets at once (one per lane), scans their unit counts, and finds the first lane whose running
 // total passes u. All 64 lanes must be active. Offsets are clamped to [0, rows] and to ascending
-// order inside an expert, so that no content of `offsets` leads outside the operands. With
+// order inside an expert, so that no content of `offsets` leads outside the operands; a caller stops at the
+// most units that ascending offsets can have, since experts whose rows overlap add up to more. With
 // `rest`, the rows behind the last expert are one more group, e = E. The result is wave-uniform.
 __device__ __forceinline__ GroupBlock find_group(const int* __restrict__ offsets, int E, int rows, int bm, int per,
                                                  bool rest, int u) {
@@ -128,6 +129,7 @@ struct GroupedArgs {
   int tiles_m, tiles_n;  // grad B: tiles of one expert; else tiles_n only
   int group_m;
   int grid;
+  int units;             // output tiles (times parts of the sum) that ascending offsets make at most
   int rest;              // zero the output rows behind the last expert
   int nt;                // gradients, 256-row tiles: non-temporal stores
   int splits;            // 32-row tiles: parts of the sum, each into its fp32 plane at C (1: none)

@@ -508,6 +508,7 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   a.tiles_n = (int)tiles_n;
   a.group_m = 8;
   a.grid = (int)grid;
+  a.units = (int)units;
   a.rest = p->zero_rest != 0;
   // Short sums write as fast as HBM takes it, and non-temporal stores are taken faster (8190 rows, 16
   // experts, 4096 x 2048: fp32 258 -> 224 us, bf16 188 -> 159); among long ones they only leave the caches

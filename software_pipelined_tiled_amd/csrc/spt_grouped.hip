@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
   };
 
   constexpr bool kSplit = BM == 32;
-  for (int tp = xcd_remap(blockIdx.x, a.grid);; tp += a.grid) {
+  for (int tp = xcd_remap(blockIdx.x, a.grid); tp < a.units; tp += a.grid) {
     // this unit: output tile (row0, col0), its row and column counts, the sum's length and its part of it
     int e, row0, rows_left, tm, tn, kc, c0 = 0, part = 0;
     int t = tp;
@@ -107,7 +107,6 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
     if constexpr (MODE == kGroupedGradB) {
       const int per = a.tiles_m * a.tiles_n;
       e = t / per;
-      if (e >= a.experts) break;
       grouped_raster(t - e * per, a.tiles_m, a.tiles_n, a.group_m, tm, tn);
       row0 = tm * BM;
       rows_left = a.m - row0;

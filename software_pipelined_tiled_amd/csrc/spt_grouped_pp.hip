@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
     u.e = u.row0 = u.col0 = u.rows_left = u.cols_left = u.c0 = u.kc = 0;
     if constexpr (MODE == kGroupedGradB) {
       const int per = args.tiles_m * args.tiles_n;
-      if (t < args.experts * per) {
+      if (t < args.units) {
         u.t = t;
         u.e = t / per;
         grouped_raster(t - u.e * per, args.tiles_m, args.tiles_n, args.group_m, tm, tn);
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(512, 1) grouped_pp_kernel(GroupedArgs args) {
         u.c0 = __builtin_amdgcn_readfirstlane(u.c0);
         u.kc = __builtin_amdgcn_readfirstlane(u.kc);
       }
-    } else {
+    } else if (t < args.units) {
       const GroupBlock g = find_group(args.offsets, args.experts, args.rows, BM, args.tiles_n, args.rest != 0, t);
       if (g.e >= 0) {
         u.t = t;

@@ -39,3 +39,20 @@ def test_4_bit_products_of_more_rows_than_16_row_blocks(matrices):
         for i in range(lo, hi, 1 << 17):
             j = min(hi, i + (1 << 17))
             assert torch.equal(got[i:j].to(torch.float64).sum(1, keepdim=True), x[i:j].to(torch.float64) @ col.t())
+
+
+@pytest.mark.parametrize("tile", [32, 128, 256])
+@pytest.mark.parametrize("grad", [False, True])
+def test_experts_that_claim_the_same_rows_add_no_work(tile, grad):
+    # wrong contents of offsets: four experts have all rows each. The walk over the output tiles ends with the most
+    # tiles that ascending offsets can have, so the last experts' are not computed, and nothing outside is touched.
+    rows, k, n = 8 * tile, 32, 48
+    x = torch.ones((rows, n if grad else k), dtype=BF16, device="cuda")
+    # experts 0, 2, 4 and 6 have the rows, with weights 1, 2, 3 and 4; those between have none
+    b = torch.tensor([1, 0, 2, 0, 3, 0, 4], dtype=BF16, device="cuda")[:, None, None].repeat(1, n, k)
+    off = torch.tensor([0, rows, 0, rows, 0, rows, 0, rows], dtype=torch.int32, device="cuda")
+    out = torch.full((rows + 128, k if grad else n), 7.0, dtype=BF16, device="cuda")
+    (spt.grouped_matmul_grad_a if grad else spt.grouped_matmul)(x, b, off, out=out[64:-64], tile=tile)
+    length = n if grad else k
+    assert ((out[64:-64] == length) | (out[64:-64] == 2 * length)).all()
+    assert (out[:64] == 7).all() and (out[-64:] == 7).all()
