@@ -4,8 +4,9 @@
  * their gradients, and products with 4-bit weights.
  *
  * Rows sorted by expert. With E experts, `offsets` is E + 1 ascending 32-bit integers in device
- * memory, offsets[0] = 0: expert e owns rows [offsets[e], offsets[e + 1]). Rows from offsets[E] on
- * belong to nobody. Kernels clamp what they read from `offsets` (and from `rows`, the position of
+ * memory: expert e owns rows [offsets[e], offsets[e + 1]). Rows from offsets[E] on belong to nobody, and
+ * so do those before offsets[0], which is 0 where experts_sort made it: offsets + lo with the weights of
+ * experts lo .. hi - 1 and E = hi - lo are the products of those experts alone. Kernels clamp what they read from `offsets` (and from `rows`, the position of
  * each slot) to the operands, so wrong contents give wrong results but no access out of range.
  *
  * Conventions of gemm.h hold: entry points only enqueue kernels on `stream` for the current device,
@@ -89,7 +90,7 @@ typedef struct {
   gemm_dtype_t in_dtype;  /* F16 or BF16, X and Y alike */
   gemm_dtype_t out_dtype; /* F16, BF16 or F32 */
   int64_t ldx, ldy, ldo, stride;
-  int zero_rest; /* FORWARD, GRAD_A: zero the output rows behind the last expert, else leave them */
+  int zero_rest; /* FORWARD, GRAD_A: zero the output rows that belong to no expert, else leave them */
   int tile;      /* rows of an output tile: 0 for the library's choice, else 32 (not GRAD_B), 128 or 256 */
 } gemm_grouped_t;
 
@@ -131,11 +132,11 @@ gemm_status_t gemm_w4_pack(const uint8_t* q, const void* scales, const uint8_t* 
  * else expert e's (matrices = E). x [rows, k] and the scales are `dtype` (F16 or BF16); out_dtype F16,
  * BF16 or F32. q - z is exact in either type, so no weight is rounded: products are exact, each
  * group's sum is fp32 and multiplied by its scale in fp32 (the sum of x * (q - z) over a group has to
- * stay inside fp32's range), and the result is rounded once. Rows behind the last expert: zero_rest
+ * stay inside fp32's range), and the result is rounded once. Rows that belong to no expert: zero_rest
  * as above. With few columns the sum over k is split over workgroups, into planes in the workspace.
  * Errors: GEMM_ERR_INVALID, GEMM_ERR_UNSUPPORTED (types; group; a weight that gemm_w4_pack refuses; ldx of
  *         2^23 or more; more than 65535 blocks of 64 rows: 4194240 rows of one matrix, and with offsets
- *         (rows - g) / 64 + g blocks, g = min(matrices + 1, rows)), GEMM_ERR_HIP.
+ *         (rows - g) / 64 + g blocks, g = min(matrices + 2, rows)), GEMM_ERR_HIP.
  */
 typedef struct {
   int64_t rows, matrices, n, k;

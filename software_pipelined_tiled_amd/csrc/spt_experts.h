@@ -2,23 +2,24 @@
 // of work to the expert whose rows it covers.
 //
 // Rows sorted by expert are described by offsets[0 .. E] in device memory: expert e owns rows
-// [offsets[e], offsets[e+1]). Rows from offsets[E] on belong to nobody. The counts are not known
-// to the host, so a launch covers an upper bound of row blocks and every unit looks its expert up.
+// [offsets[e], offsets[e+1]). Rows before offsets[0] (some experts of an order) and from offsets[E] on
+// belong to nobody. The counts are not known to the host, so a launch covers an upper bound of row blocks and every unit looks its expert up.
 #pragma once
 
 #include "spt_common.h"
 
 namespace spt {
 
-// Blocks of `bm` rows that E groups (and the rows behind the last) can cut R rows into, at most:
-// with g non-empty groups, (R - g) / bm + g.
+// Blocks of `bm` rows that E groups (and the rows behind the last, which the choice of a kernel counts on)
+// can cut R rows into, at most: with g non-empty groups, (R - g) / bm + g. A launch covers one group more,
+// the rows in front of the first.
 SPT_HD int64_t max_row_blocks(int64_t rows, int64_t groups, int bm) {
   const int64_t g = groups + 1 < rows ? groups + 1 : rows;
   return rows <= 0 ? 0 : (rows - g) / bm + g;
 }
 
 struct GroupBlock {
-  int e;       // the expert; E: rows behind the last one; -1: no such unit
+  int e;       // the expert; E: rows of nobody; -1: no such unit
   int begin, end;  // the expert's rows
   int block;   // row block inside the expert
   int blocks;  // row blocks of the expert
@@ -33,7 +34,8 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // total passes u. All 64 lanes must be active. Offsets are clamped to [0, rows] and to ascending
 // order inside an expert, so that no content of `offsets` leads outside the operands; a caller stops at the
 // most units that ascending offsets can have, since experts whose rows overlap add up to more. With
-// `rest`, the rows behind the last expert are one more group, e = E. The result is wave-uniform.
+// `rest`, the rows behind the last expert and those in front of the first are two more groups, e = E. The
+// result is wave-uniform.
 __device__ __forceinline__ GroupBlock find_group(const int* __restrict__ offsets, int E, int rows, int bm, int per,
                                                  bool rest, int u) {
   GroupBlock g;
@@ -41,14 +43,15 @@ __device__ __forceinline__ GroupBlock find_group(const int* __restrict__ offsets
   g.begin = g.end = g.block = g.blocks = g.local = 0;
   int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
   asm volatile("" : "+v"(lane));  // lane addresses are made here, not kept in registers across a caller's loop
-  const int groups = rest ? E + 1 : E;
+  const int groups = rest ? E + 2 : E;
   int left = u;  // units still to skip
   for (int base = 0; base < groups; base += 64) {
     const int l = base + lane;
     int b = 0, en = 0;
     if (l < groups) {
-      b = clampi(offsets[l], 0, rows);
-      en = l < E ? clampi(offsets[l + 1], b, rows) : rows;
+      const int at = clampi(offsets[l <= E ? l : 0], 0, rows);
+      b = l <= E ? at : 0;
+      en = l < E ? clampi(offsets[l + 1], b, rows) : l == E ? rows : at;
     }
     const int nb = (int)((unsigned)(en - b + bm - 1) / (unsigned)bm);
     int s = nb * per;
@@ -60,7 +63,7 @@ __device__ __forceinline__ GroupBlock find_group(const int* __restrict__ offsets
     const unsigned long long m = __ballot(s > left);
     if (m) {
       const int f = __builtin_ctzll(m);
-      g.e = __builtin_amdgcn_readfirstlane(base + f);
+      g.e = __builtin_amdgcn_readfirstlane(base + f < E ? base + f : E);
       g.begin = __builtin_amdgcn_readlane(b, f);
       g.end = __builtin_amdgcn_readlane(en, f);
       g.blocks = __builtin_amdgcn_readlane(nb, f);
@@ -130,7 +133,7 @@ struct GroupedArgs {
   int group_m;
   int grid;
   int units;             // output tiles (times parts of the sum) that ascending offsets make at most
-  int rest;              // zero the output rows behind the last expert
+  int rest;              // zero the output rows of nobody
   int nt;                // gradients, 256-row tiles: non-temporal stores
   int splits;            // 32-row tiles: parts of the sum, each into its fp32 plane at C (1: none)
   int64_t plane;         // elements between planes
@@ -181,9 +184,9 @@ struct W4Args {
 struct PlaneArgs {
   const float* parts;
   char* out;
-  const int* kept;  // rows that were computed: *kept, or `rows` when null
+  const int* offsets;  // rows that were computed: offsets[0] .. offsets[experts], or all when null
   int64_t ldo, plane;
-  int rows, n, splits, out_dtype, rest;
+  int rows, experts, n, splits, out_dtype;
 };
 
 struct W4Entry {

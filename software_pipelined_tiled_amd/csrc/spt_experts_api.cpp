@@ -62,20 +62,20 @@ int stream_grid(int64_t threads) {
   return (int)(b < 1 ? 1 : (b > 8192 ? 8192 : b));
 }
 
-// out = the planes of a cut sum, added in their order
-gemm_status_t add_planes(const float* parts, void* out, const int32_t* kept, int64_t ldo, int64_t rows, int64_t n,
-                         int64_t splits, int out_dtype, int rest, void* stream) {
+// out = the planes of a cut sum, added in their order; with offsets, the experts' rows only
+gemm_status_t add_planes(const float* parts, void* out, const int32_t* offsets, int64_t experts, int64_t ldo, int64_t rows,
+                         int64_t n, int64_t splits, int out_dtype, void* stream) {
   spt::PlaneArgs r;
   r.parts = parts;
   r.out = (char*)out;
-  r.kept = kept;
+  r.offsets = offsets;
   r.ldo = ldo;
   r.plane = rows * n;
   r.rows = (int)rows;
+  r.experts = (int)experts;
   r.n = (int)n;
   r.splits = (int)splits;
   r.out_dtype = out_dtype;
-  r.rest = rest;
   return launch(spt::add_planes_fn(), dim3(stream_grid(r.plane)), 256, 0, &r, stream);
 }
 
@@ -266,7 +266,7 @@ bool w4_too_large(int64_t matrices, int64_t n, int64_t k) {
 
 struct W4Shape {
   spt::W4Entry entry;
-  int64_t nblocks, row_blocks, splits, ws;
+  int64_t nblocks, row_blocks, grid_y, splits, ws;  // row_blocks: what the choice counts on
 };
 
 gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
@@ -284,7 +284,9 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
   auto take = [&](int variant) {
     s->entry = spt::w4_entry(variant, p->dtype == GEMM_BF16, 128 / p->group, p->has_zeros != 0);
     s->nblocks = ceil_div(n16, s->entry.nt);
-    s->row_blocks = grouped ? spt::max_row_blocks(p->rows, p->matrices, 16 * s->entry.mt) : ceil_div(p->rows, 16 * s->entry.mt);
+    const int bm = 16 * s->entry.mt;
+    s->row_blocks = grouped ? spt::max_row_blocks(p->rows, p->matrices, bm) : ceil_div(p->rows, bm);
+    s->grid_y = grouped ? spt::max_row_blocks(p->rows, p->matrices + 1, bm) : s->row_blocks;
   };
   // Cut K when the workgroups alone leave compute units idle, into as many parts as still run at once: one
   // workgroup more than compute units is a second round.
@@ -308,14 +310,14 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
   if (each <= 16 && kb <= 16 && p->matrices > 1 && n16 * used >= 1536) chosen = 7;
   else if (each <= 4) chosen = n16 * used <= kCus ? 0 : 1;
   if (chosen >= 0) take(chosen);
-  if (chosen < 0 || s->row_blocks > kMaxGridY) {
+  if (chosen < 0 || s->grid_y > kMaxGridY) {
     struct { double start, block, extra; } const t[] = {
         {3.9, 1.03, 0.7}, {3.5, .82, 1.6}, {3.4, 1.19, 1.8}, {4.8, .96, 1.4}, {5.3, .73, 1.9}, {3.4, 1.27, 3.1}};
     int best = 0;
     double least = 0;
     for (int v = 1; v <= 6; ++v) {
       take(v);
-      if (s->row_blocks > kMaxGridY) continue;
+      if (s->grid_y > kMaxGridY) continue;
       const int64_t sp = splits(), wgs = s->nblocks * used * ceil_div(each, 16 * s->entry.mt) * sp;
       const double blocks = (double)ceil_div(ceil_div(kb, sp), s->entry.wk);
       const double us = t[v - 1].start + t[v - 1].block * (blocks + t[v - 1].extra) * (double)ceil_div(wgs, kCus) +
@@ -477,7 +479,7 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
                                                        s.splits > 1 ? (int)GEMM_F32 : (int)p->out_dtype);
   const int64_t tiles_m = ceil_div(p->n, entry.bm), tiles_n = ceil_div(out_n, entry.bn);
   const int64_t units = gb ? p->experts * tiles_m * tiles_n
-                           : spt::max_row_blocks(p->rows, p->experts, entry.bm) * tiles_n * s.splits;
+                           : spt::max_row_blocks(p->rows, p->experts + 1, entry.bm) * tiles_n * s.splits;
   if (units > kMaxUnits) return GEMM_ERR_UNSUPPORTED;
   int cu = 0;
   st = device_cus(&cu);
@@ -521,8 +523,8 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
   a.ldc = out_n;
   st = launch(entry.fn, dim3((unsigned)grid), entry.threads, 0, &a, stream);
   if (st != GEMM_OK) return st;
-  return add_planes((const float*)a.C, out, offsets + p->experts, p->ldo, p->rows, out_n, s.splits, (int)p->out_dtype, a.rest,
-                    stream);
+  return add_planes((const float*)a.C, out, a.rest ? nullptr : offsets, p->experts, p->ldo, p->rows, out_n, s.splits,
+                    (int)p->out_dtype, stream);
 }
 
 gemm_status_t gemm_w4_packed_bytes(int64_t matrices, int64_t n, int64_t k, int group, int has_zeros, int64_t* out) {
@@ -600,11 +602,11 @@ gemm_status_t gemm_w4_run(const gemm_w4_t* p, const void* x, const void* packed,
   a.splits = (int)s.splits;
   a.rest = p->zero_rest != 0;
   a.out_dtype = (int)p->out_dtype;
-  st = launch(s.entry.fn, dim3((unsigned)(s.nblocks * s.splits), (unsigned)s.row_blocks), 64 * s.entry.waves, 0, &a,
+  st = launch(s.entry.fn, dim3((unsigned)(s.nblocks * s.splits), (unsigned)s.grid_y), 64 * s.entry.waves, 0, &a,
               stream);
   if (st != GEMM_OK || s.splits == 1) return st;
-  return add_planes((const float*)workspace, out, offsets ? offsets + p->matrices : nullptr, p->ldo, p->rows, p->n, s.splits,
-                    a.out_dtype, a.rest, stream);
+  return add_planes((const float*)workspace, out, a.rest ? nullptr : offsets, p->matrices, p->ldo, p->rows, p->n, s.splits,
+                    a.out_dtype, stream);
 }
 
 }  // extern "C"

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(64 * WM * WN, WM * WN * PER_CU / 4) grouped_ke
       grouped_raster(g.local, g.blocks, a.tiles_n, a.group_m, tm, tn);
       row0 = g.begin + tm * BM;
       rows_left = g.end - row0;
-      kc = e == a.experts ? 0 : a.kc;  // behind the last expert: zeros
+      kc = e == a.experts ? 0 : a.kc;  // rows of nobody: zeros
     }
     const int col0 = tn * BN, cols_left = a.n - col0;
     const char* xb = a.X + (MODE == kGroupedGradB ? ((int64_t)c0 * a.ldx + row0) * 2 : (int64_t)row0 * a.ldx * 2);

@@ -8,7 +8,7 @@
 // computed in phases 2g+1 and 2g+2. Five 32 KiB operand slots: K-tile g's X tile sits in slot 2g mod 5 and
 // its Y tile in slot 2g+1 mod 5; group 0 loads Y(g+1) in phase 2g, group 1 X(g+2) in phase 2g+1. The
 // stream runs on across units: a unit's stores go out in its group's next memory phase. A unit without a
-// sum (an expert without rows in grad B; the rows behind the last expert) is one K-tile of zeros.
+// sum (an expert without rows in grad B; rows that belong to no expert) is one K-tile of zeros.
 //
 // What differs by mode is the side on which an operand is contiguous (spt_grouped.hip):
 //   * contiguous in c: 256 rows of 64 c, as in the dense kernel;

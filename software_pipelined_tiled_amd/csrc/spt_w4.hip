@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
     rows = g.end - row0;
   }
   rows = rows < BM ? rows : BM;
-  const bool none = a.offsets && e == a.experts;  // rows behind the last expert: zeros
+  const bool none = a.offsets && e == a.experts;  // rows of nobody: zeros
   const int per = (a.kb + a.splits - 1) / a.splits;
   const int kb0 = split * per, kb1 = none ? kb0 : (kb0 + per < a.kb ? kb0 + per : a.kb);
   const int kb_full = kb1 < (a.k >> 7) ? kb1 : a.k >> 7;
@@ -533,12 +533,13 @@ __global__ void __launch_bounds__(64 * WN * WK) w4_rows_kernel(W4Args a) {
   }
 }
 
-// out = the planes of a cut sum (of these products or the grouped ones) added in order, rounded once. With `kept`, rows from *kept on hold zeros or are
-// left alone.
+// out = the planes of a cut sum (of these products or the grouped ones) added in order, rounded once. With
+// offsets, rows that belong to no expert are left alone.
 __global__ void __launch_bounds__(256) add_planes_kernel(PlaneArgs r) {
-  const int kept = r.kept && !r.rest ? clampi(*r.kept, 0, r.rows) : r.rows;
-  const int64_t total = (int64_t)kept * r.n;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+  const int first = r.offsets ? clampi(r.offsets[0], 0, r.rows) : 0;
+  const int last = r.offsets ? clampi(r.offsets[r.experts], 0, r.rows) : r.rows;
+  const int64_t end = (int64_t)last * r.n;
+  for (int64_t i = (int64_t)first * r.n + (int64_t)blockIdx.x * 256 + threadIdx.x; i < end; i += (int64_t)gridDim.x * 256) {
     float v = r.parts[i];
     for (int s = 1; s < r.splits; ++s) v += r.parts[s * r.plane + i];
     const int64_t row = i / r.n;

@@ -402,8 +402,8 @@ def _grouped_forward(A, B, offsets, out_dtype, out, tile):
 
 def grouped_matmul_grad_a(dC: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
                           tile: int = 0) -> torch.Tensor:
-    """Gradient of ``grouped_matmul`` for A: dA[i] = dC[i]·B[e] for expert e's rows i, in dC's type. Rows behind
-    the last expert: zeros in a new tensor, left as they were in ``out``."""
+    """Gradient of ``grouped_matmul`` for A: dA[i] = dC[i]·B[e] for expert e's rows i, in dC's type. Rows of no
+    expert: zeros in a new tensor, left as they were in ``out``."""
     if out is not None:
         _no_autograd(out, dC, B)
     elif _wants_grad(dC, B):
@@ -461,10 +461,11 @@ class _Grouped(torch.autograd.Function):
 def grouped_matmul(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out_dtype: torch.dtype | None = None,
                    out: torch.Tensor | None = None, tile: int = 0) -> torch.Tensor:
     """C[i] = A[i]·B[e]ᵀ for expert e's rows offsets[e] <= i < offsets[e + 1]: A [rows, k] and B [experts, n, k]
-    fp16 or bf16, fp32 sums, C in A's type or ``out_dtype``. ``offsets``: 32-bit, on the device (a
-    ``TokenOrder``'s). Rows behind the last expert are zeros in a new tensor, left as they were in ``out``.
-    ``tile``: rows of an output tile, 0 for the library's choice, else 32, 128 or 256 (the same sums, in
-    fp32, which 32-row tiles may add in parts)."""
+    fp16 or bf16, fp32 sums, C in A's type or ``out_dtype``. ``offsets``: 32-bit, ascending, on the device: a
+    ``TokenOrder``'s, or its [lo : hi + 1] with B of experts lo .. hi - 1. Rows of no expert, behind the last or in
+    front of the first, are zeros in a new tensor, left as they were in ``out``. ``tile``: rows of an output
+    tile, 0 for the library's choice, else 32, 128 or 256 (the same sums, in fp32, which 32-row tiles may add in
+    parts)."""
     if out is not None:
         _no_autograd(out, A, B)
     elif _wants_grad(A, B):
@@ -523,8 +524,8 @@ def w4_matmul(x: torch.Tensor, w: W4Weight, offsets: torch.Tensor | None = None,
               out: torch.Tensor | None = None) -> torch.Tensor:
     """x [rows, k] times the 4-bit weight, [rows, n]: one weight for all rows, or expert e's for rows
     offsets[e] <= i < offsets[e + 1] of a weight packed from [experts, n, k]. x in the scales' type; no weight
-    is rounded, sums are fp32. No gradient. Rows behind the last expert are zeros in a new tensor, left as they
-    were in ``out``."""
+    is rounded, sums are fp32. No gradient. Rows of no expert, behind the last or in front of the first, are zeros
+    in a new tensor, left as they were in ``out``."""
     code = _type("x", x, _16BIT)
     _need(x.dtype == w.dtype, "x must have the dtype of the scales")
     _on_device("x weight offsets", x, w.packed, offsets)
