@@ -125,7 +125,7 @@ def _refuse_tangents(tensors) -> None:
 def _wants_grad(*tensors) -> bool:
     """Whether these operands make the call part of a graph. Every call asks, so that operands with a tangent, which
     the kernels' results would not carry, are refused here; they exist only inside a dual level."""
-    if getattr(forward_ad, "_current_level", 0) >= 0:
+    if forward_ad._current_level >= 0:
         _refuse_tangents(tensors)
     if torch.is_grad_enabled():
         for t in tensors:
