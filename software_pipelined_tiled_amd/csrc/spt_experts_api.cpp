@@ -9,7 +9,8 @@
 namespace {
 
 constexpr int64_t kMax32 = 0x7FFFFFFF;
-constexpr int kMaxExperts = 1024;
+constexpr int kMaxExperts = 1024;  // of the sort, whose workgroups count in LDS
+constexpr int64_t kMaxGroups = (int64_t)1 << 24;  // of the products: the search adds 64 to their number in 32 bits
 // Output tiles of a grouped product: 64 experts' counts add up in 32 bits whatever the offsets hold. Of the
 // smallest tiles these are 2^35 elements.
 constexpr int64_t kMaxUnits = (int64_t)1 << 24;
@@ -194,7 +195,7 @@ gemm_status_t grouped_shape(const gemm_grouped_t* p, const void* X, const void* 
   if (p->tile != 0 && p->tile != 32 && p->tile != 128 && p->tile != 256) return GEMM_ERR_INVALID;
   if (!is16(p->in_dtype) || (p->tile == 32 && p->mode == GEMM_GROUPED_GRAD_B)) return GEMM_ERR_UNSUPPORTED;
   const int64_t lim = (int64_t)1 << 20;
-  if (p->rows > kMax32 || p->experts > kMax32 || p->n > kMax32 || p->k > kMax32) return GEMM_ERR_UNSUPPORTED;
+  if (p->rows > kMax32 || p->experts > kMaxGroups || p->n > kMax32 || p->k > kMax32) return GEMM_ERR_UNSUPPORTED;
   const bool gb = p->mode == GEMM_GROUPED_GRAD_B;
   const int64_t xc = p->mode == GEMM_GROUPED_FORWARD ? p->k : p->n;
   const int64_t oc = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
@@ -275,7 +276,7 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
   if (!is16(p->dtype) || (p->group != 32 && p->group != 64 && p->group != 128)) return GEMM_ERR_UNSUPPORTED;
   if (p->ldx < p->k || p->ldo < p->n || (!grouped && p->matrices != 1)) return GEMM_ERR_INVALID;
   const int64_t lim = (int64_t)1 << 24;
-  if (p->n > lim || p->k > lim || p->ldx >= lim / 2 || p->rows > kMax32 || p->matrices > kMax32 ||
+  if (p->n > lim || p->k > lim || p->ldx >= lim / 2 || p->rows > kMax32 || p->matrices > kMaxGroups ||
       w4_too_large(p->matrices, p->n, p->k))
     return GEMM_ERR_UNSUPPORTED;
   const int64_t n16 = ceil_div(p->n, 16), kb = ceil_div(p->k, 128);
@@ -530,7 +531,7 @@ gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const voi
 gemm_status_t gemm_w4_packed_bytes(int64_t matrices, int64_t n, int64_t k, int group, int has_zeros, int64_t* out) {
   if (!out || matrices < 0 || n < 0 || k < 0) return GEMM_ERR_INVALID;
   const int64_t lim = (int64_t)1 << 24;
-  if ((group != 32 && group != 64 && group != 128) || n > lim || k > lim || matrices > lim ||
+  if ((group != 32 && group != 64 && group != 128) || n > lim || k > lim || matrices > kMaxGroups ||
       w4_too_large(matrices, n, k))
     return GEMM_ERR_UNSUPPORTED;
   *out = w4_blocks(matrices, n, k) * (1024 + 16 * (128 / group) * (has_zeros ? 3 : 2));

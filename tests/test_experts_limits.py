@@ -64,3 +64,12 @@ def test_bytes_of_experts(mode, change, status):
     b = ctypes.c_int64(0)
     got = spt.lib().gemm_grouped_workspace_bytes(ctypes.byref(p), 0x1000, 0x1000, ctypes.byref(b))
     assert got == status and b.value >= 0
+
+
+@pytest.mark.parametrize("experts,status", [(1 << 24, OK), ((1 << 24) + 1, UNSUPPORTED), (2**31 - 1, UNSUPPORTED)])
+def test_number_of_experts(experts, status):
+    # the search for a tile's expert counts experts, and the rows of nobody, in 32 bits
+    p = _lib.GemmGrouped(mode=0, rows=3, experts=experts, n=1, k=1, in_dtype=BF16, out_dtype=BF16, ldx=1, ldy=1, ldo=1, stride=1)
+    b = ctypes.c_int64(0)
+    assert spt.lib().gemm_grouped_workspace_bytes(ctypes.byref(p), 0x1000, 0x1000, ctypes.byref(b)) == status
+    assert w4_status(3, 16, 128, experts, offsets=True) == status
