@@ -126,8 +126,8 @@ struct GroupedShape {
 };
 
 // 32-row tiles: with at most two of them for every compute unit and rows of whole 16-byte chunks, two
-// workgroups with six stages in flight and the hint that keeps Y, which is read once then, out of the caches
-// (64 rows, 8 experts, 4096^2: 44 us against 57 with three workgroups of four stages). With more tiles a third
+// workgroups of six stages, five in flight, and the hint that keeps Y, which is read once then, out of the caches
+// (64 rows, 8 experts, 4096^2: 44 us against 57 with three workgroups of four stages, three in flight). With more tiles a third
 // workgroup saves a round (200 rows: 59 against 77), and off 16 bytes neighbouring loads share lines, and the
 // hint costs (2044 columns: 56 us against 49).
 int64_t grouped_small_tiles(const gemm_grouped_t* p) {
@@ -144,9 +144,10 @@ bool grouped_deep(const gemm_grouped_t* p, const void* Y) {
 // Rows of an output tile: the least time by this model, in us. A start, and the longer of rounds of tiles over the
 // compute units (K-tiles times what one takes, and the tile's own start and end) and the operands' bytes.
 // 256-row tiles copy an operand that is off 16 bytes first. The constants are a fit to 1608 measured shapes
-// (1 .. 128 experts, 32 .. 16384 rows, N and K 512 .. 8192); the choice takes 2 % longer than the best tile of
+// (1 .. 128 experts, 32 .. 16384 rows, N and K 512 .. 8192); on them the choice takes 2 % longer than the best tile of
 // each shape, 47 % at worst, where 32-row tiles for up to 32 rows per expert and rounds alone took 7 %, 185 % at
-// worst (grad B of 64 experts of 1001 x 1500, 32 rows: 113 us against 39).
+// worst (grad B of 64 experts of 1001 x 1500, 32 rows: 113 us against 39). On 414 other shapes, drawn at random
+// with uneven experts, it takes 2.9 %, 73 % at worst (3230 rows, one expert of 5249 x 7795: 585 us against 338).
 //   Two things the model leaves out. Grad A's 32-row tiles beyond two for every compute unit read B in pieces of 256
 // bytes from many places, and 128-row tiles are faster even for few rows (128 rows, 16 experts, 4096^2: 86 us against
 // 94). And grad B's 128-row tiles reload what the L2 no longer holds from about 64 rows per expert on (16384
@@ -303,8 +304,10 @@ gemm_status_t w4_shape(const gemm_w4_t* p, bool grouped, W4Shape* s) {
   // (4096 x 4096, 1 row: 5.0 us, 32 columns 6.6; 8192 x 8192: 13.0 against 10.3). Else the least time by this
   // model, in us: a start, rounds of workgroups over the compute units times blocks of K per wave, and the second
   // pass over a split sum. Its constants are a fit to 1320 measured shapes (N 512 .. 28672, K 1024 .. 14336, 1 ..
-  // 2000 rows, up to 64 experts). The choice takes 2 % longer than the best kernel of each shape, 39 % at worst; a
-  // rule on the number of 16 x 16 output blocks alone took 9 %, 95 % at worst.
+  // 2000 rows, up to 64 experts). On them the choice takes 2 % longer than the best kernel of each shape, 39 % at
+  // worst; a rule on the number of 16 x 16 output blocks alone took 9 %, 95 % at worst. On 132 other shapes, drawn at
+  // random with uneven experts, it takes 9 %, 62 % at worst (290 rows over 26 experts of 539 x 13773: 92 us against
+  // 57), most of it where the model's candidates leave out the kernels of the two rules before it.
   // Blocks of rows are the grid's second dimension: where a kernel's are too many, only those with more rows a block
   // are candidates.
   int chosen = -1;

@@ -27,9 +27,10 @@
 // Long sums of few tiles are cut into parts, each into its own fp32 plane, and a second kernel adds the planes in
 // their order (32-row tiles only).
 //
-// What bounds it. Few rows per expert: reading B. 32 x 64 tiles keep 150 KiB of loads on the way per compute
-// unit: 64 rows, 8 experts of 4096 x 4096 in 44 us, 6.2 TB/s where every expert is met (a read-only
-// stream reaches 5456 GB/s; the rest are cache hits). More rows: 128 x 128 tiles, two workgroups a compute unit, whose
+// What bounds it. Few rows per expert: reading B. 32 x 64 tiles keep 120 KiB of loads on the way per compute
+// unit (two workgroups, five of six stages of 12 KiB; 108 KiB with three workgroups, three of four stages): 64
+// rows, 8 experts of 4096 x 4096 in 44 us, 6.2 TB/s where every expert is met (a read-only stream reaches 5456
+// GB/s; the rest are cache hits). More rows: 128 x 128 tiles, two workgroups a compute unit, whose
 // barriers and waits overlap the other's products: 5003 rows, 64 experts of 1409 x 2044 (rows off 16 bytes, fp32
 // out) 125 us, 3.3 TB/s and 230 TFLOP/s, where the loads' latency per K-tile (0.8 us for two tiles a compute unit)
 // is what is left. Longer rings with one workgroup, 128 x 64 tiles and eight waves were no faster. From about 250

@@ -21,11 +21,14 @@
 // exchange between quarter-waves makes them eight per fragment pair.
 //
 // What bounds it: the matrix cores at the clock the power limit allows. 16384 rows, 8 experts of 8192 x 4096, bf16:
-// forward 790 us, 1393 TFLOP/s, the matrix cores 0.84 busy (grad A 0.79, grad B 0.65, since its sums of 2048 rows end
-// in stores twice as often); the dense kernel of this library reaches 1488 TFLOP/s at 8192^3. No read of LDS has
+// forward 779 to 811 us in a loop, 1356 to 1411 TFLOP/s (838 the median of a trace), the matrix cores 0.84 busy (grad
+// A 0.79, grad B 0.65, since its sums of 2048 rows end in stores twice as often); the dense kernel of this library
+// reaches 1488 TFLOP/s at 8192^3. No read of LDS has
 // a bank conflict. What is left: the last round of tiles, which is as long as a full one (328 tiles over 256
-// compute units: 189 us where 256 take 100), and grad B's fp32 stores (8190 rows, 16 experts of 4096 x 2048: 218 us,
-// 132 without the stores), which go out while one of the two groups computes and take longer than that.
+// compute units: 189 us where 256 take 100), and grad B's fp32 stores (8190 rows, 16 experts of 4096 x 2048: 218 us with its
+// operands in the caches, 132 without the stores), which go out while one of the two groups computes and take longer
+// than that. In a training step, where operands come from HBM, it takes 234 us with even experts and 261 to 291 with
+// uneven ones: a workgroup's tiles are every 256th, whatever their sums' lengths.
 #include "spt_device.h"
 #include "spt_experts.h"
 #include "spt_transpose.h"

@@ -11,11 +11,12 @@
 // so every result is the same bits on every run.
 //
 // What bounds it. The sort moves a few bytes per slot: 32 slots of 8 experts take 3.2 us and 49146 slots of 64
-// experts 4.8 + 5.2 us, launches and dependent loads, not bandwidth. The row kernels are bound by HBM, with 16
+// experts 4.7 + 5.8 us, launches and dependent loads, not bandwidth. The row kernels are bound by HBM, with 16
 // bytes per lane and access (a large copy reaches 5156 GB/s): 8191 tokens of 2048 16-bit columns to 6 experts
 // each gathered in 40 us (234 MB, 5.8 TB/s, part of it left in the caches); 8192 tokens of 4096 columns with 4
-// experts each combined in 67 us (336 MB, 5.0 TB/s), both gradients in 105 us (604 MB, 5.7 TB/s). At 37 tokens
-// the launch is all there is (5 us).
+// experts each combined in 67 us (336 MB, 5.0 TB/s), both gradients in 105 us (604 MB, 5.7 TB/s). 37
+// tokens with 8 experts each take 5.1 us: 3 for the launch, the rest two rounds of four slots, whose positions, then
+// rows and weights, each wait for a trip to memory.
 #include "spt_device.h"
 #include "spt_experts.h"
 

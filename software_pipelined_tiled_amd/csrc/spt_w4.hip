@@ -22,11 +22,13 @@
 // that leaves compute units without work, K is cut over workgroups as well, into fp32 planes that a second
 // kernel adds in order.
 //
-// Measured (weights cold). 1 row of 8192 x 8192, G = 128: 9.4 us, 3.7 TB/s of 35 MB, with 5 us of them the launch
-// and the first loads; 16 rows of 28672 x 8192, G = 64 with zero points: 30 us, 4.3 TB/s (a read-only stream 5.5); 32
-// rows over 8 experts of 4096 x 4096: 16.2 us, 4.3 TB/s. With many rows the unpacking bounds it, since every 64
-// rows unpack all weights again: 512 rows of 8192 x 8192, G = 128: 76 us fp16, 908 TFLOP/s, bf16 85
-// us. 128 rows to a workgroup halve that but leave registers for two waves a SIMD only: 90 and 95 us.
+// Measured (weights cold, medians). 1 row of 8192 x 8192, G = 128: 10.4 us, 3.3 TB/s of 35 MB, with 5 us of them the
+// launch and the first loads; 16 rows of 28672 x 8192, G = 64 with zero points: 31 us, 4.0 TB/s (a read-only stream
+// 5.5); 32 rows over 8 experts of 4096 x 4096: 17.4 us, 4.0 TB/s. With many rows the unpacking bounds it, since every
+// 64 rows unpack all weights again: 512 rows of 8192 x 8192, G = 128: 79 us fp16, 874 TFLOP/s, bf16 93 us. 128 rows to
+// a workgroup halve that but leave registers for two waves a SIMD only (timed together, 90 and 95 us against 76 and
+// 85). From about a thousand rows on, one unpacking and a dense product would be faster
+// (8192 x 8192 bf16, G = 64 with zero points, 1024 rows: 178 us; the dense product takes 103).
 #include "spt_device.h"
 #include "spt_experts.h"
 
@@ -81,7 +83,8 @@ __global__ void __launch_bounds__(256) w4_pack_groups_kernel(W4PackArgs a) {
 // ------------------------------------------------------------------------------ four bits to operands
 // Eight weights minus their zero point as a matrix operand. A nibble placed in the low bits of the
 // fp16 pattern of 1024 (or, shifted by four, of 64) reads 1024 + q (64 + q): two pairs come out of a
-// word by a mask alone, two more after one shift.
+// word by a mask alone, two more after one shift. (The pattern of 1024 for this: Kim, Henry, Fahim and Hassan
+// Awadalla, "Who Says Elephants Can't Run", 2022.)
 struct ZeroF16 {
   unsigned c0, c1;  // -(1024 + z), -(64 + z) in both halves
 };
