@@ -6,14 +6,16 @@
  * Rows sorted by expert. With E experts, `offsets` is E + 1 ascending 32-bit integers in device
  * memory: expert e owns rows [offsets[e], offsets[e + 1]). Rows from offsets[E] on belong to nobody, and
  * so do those before offsets[0], which is 0 where experts_sort made it: offsets + lo with the weights of
- * experts lo .. hi - 1 and E = hi - lo are the products of those experts alone. Kernels clamp what they read from `offsets` (and from `rows`, the position of
- * each slot) to the operands, so wrong contents give wrong results but no access out of range.
+ * experts lo .. hi - 1 and E = hi - lo are the products of those experts alone. Kernels clamp what they
+ * read from `offsets` (and from `rows`, the position of each slot) to the operands and their work to what
+ * ascending offsets can make, so wrong contents give wrong results but no access out of range.
  *
  * Conventions of gemm.h hold: entry points only enqueue kernels on `stream` for the current device,
  * allocate nothing, never synchronise, return a gemm_status_t and throw nothing. Workspaces are the
  * caller's: a *_workspace_bytes function gives the size (0: none needed, NULL allowed), its contents
- * need no preparation, and calls that may overlap need one each. All entry points may be recorded
- * into a HIP graph (no memset nodes, only kernels), after one call on that device outside the capture.
+ * need no preparation, and calls that may overlap need one each. Outputs and workspaces must not
+ * overlap an operand. All entry points may be recorded into a HIP graph (no memset nodes, only kernels),
+ * after one call on that device outside the capture.
  * Dimensions are counted in elements, leading dimensions too.
  */
 #ifndef SPT_EXPERTS_H
@@ -66,6 +68,7 @@ gemm_status_t experts_combine(const void* y, gemm_dtype_t dtype, int64_t tokens,
  * Gradients of experts_combine: dy[rows[s]] = weights[s] * dout[t] and, where weights are given,
  * dweights[s] = <dout[t], y[rows[s]]> (fp32 sums; the weights' type) for every kept slot s of token
  * t. A dropped slot has dweights 0 and its row of dy is zeros (zero_rest != 0) or left as it was.
+ * Errors: as experts_gather; GEMM_ERR_UNSUPPORTED from 2^23 tokens on.
  */
 gemm_status_t experts_combine_grad(const void* dout, int64_t lddo, const void* y, gemm_dtype_t dtype, int64_t tokens,
                                    int64_t top_k, int64_t width, int64_t ldy, const int32_t* rows,

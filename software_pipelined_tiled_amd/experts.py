@@ -4,7 +4,8 @@ autograd graph; all arithmetic runs in the HIP kernels.
 
 Every call enqueues on its tensors' device, on that device's current stream, and synchronises nothing.
 Workspaces come from torch's allocator, so calls on several streams, or captured into several graphs,
-never share one. Rows of a tensor may be any distance apart (unit column stride).
+never share one. Rows of a tensor may be any distance apart (unit column stride). ``out`` must not overlap an
+operand: kernels read and write at once.
 
 ``gather_rows``, ``combine_rows``, ``grouped_matmul`` and ``routed_matmul`` are differentiable once, in reverse mode;
 operands with a forward-mode tangent are refused. The ``*_grad`` functions are the same gradients as plain calls, for
@@ -402,8 +403,8 @@ def _grouped_forward(A, B, offsets, out_dtype, out, tile):
 
 def grouped_matmul_grad_a(dC: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out: torch.Tensor | None = None,
                           tile: int = 0) -> torch.Tensor:
-    """Gradient of ``grouped_matmul`` for A: dA[i] = dC[i]·B[e] for expert e's rows i, in dC's type. Rows of no
-    expert: zeros in a new tensor, left as they were in ``out``."""
+    """Gradient of ``grouped_matmul`` for A: dA[i] = dC[i]·B[e] for expert e's rows i, dC 16-bit, dA in its type
+    whatever the forward's ``out_dtype`` was. Rows of no expert: zeros in a new tensor, left as they were in ``out``."""
     if out is not None:
         _no_autograd(out, dC, B)
     elif _wants_grad(dC, B):
@@ -452,7 +453,7 @@ class _Grouped(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dC):
         A, B, offsets = ctx.saved_tensors
-        dC = _rows_apart(dC.to(A.dtype))  # the products take 16-bit operands of one type
+        dC = _rows_apart(dC.to(A.dtype))  # the products take 16-bit operands of one type: fp32 loses range and bits
         dA = grouped_matmul_grad_a(dC, B, offsets) if ctx.needs_input_grad[0] else None
         dB = grouped_matmul_grad_b(dC, A, offsets) if ctx.needs_input_grad[1] else None
         return dA, dB, None, None, None
@@ -465,7 +466,11 @@ def grouped_matmul(A: torch.Tensor, B: torch.Tensor, offsets: torch.Tensor, out_
     ``TokenOrder``'s, or its [lo : hi + 1] with B of experts lo .. hi - 1. Rows of no expert, behind the last or in
     front of the first, are zeros in a new tensor, left as they were in ``out``. ``tile``: rows of an output
     tile, 0 for the library's choice, else 32, 128 or 256 (the same sums, in fp32, which 32-row tiles may add in
-    parts)."""
+    parts).
+
+    Gradients: the products take 16-bit operands, so a dC that arrives in fp32 (``out_dtype``) is rounded to A's type
+    first, and dA and dB come in it. With fp16 operands a gradient above 65504 becomes infinite and one below 2^-25
+    zero: scale the loss, or take bf16."""
     if out is not None:
         _no_autograd(out, A, B)
     elif _wants_grad(A, B):
@@ -552,8 +557,10 @@ def routed_matmul(x: torch.Tensor, weight: torch.Tensor | W4Weight, experts: tor
                   weights: torch.Tensor | None = None) -> torch.Tensor:
     """A routed linear layer: out[t] = sum over j of weights[t, j] * x[t]·B[experts[t, j]]ᵀ, with B
     [experts, n, k] 16-bit, or packed in 4 bits (no gradient then). The tokens are sorted by expert, their
-    rows gathered, multiplied and combined; ids outside the experts are dropped. Differentiable in x, B and
-    the weights."""
+    rows gathered, multiplied and combined; ids outside the experts are dropped. The experts' outputs are rounded to
+    x's 16-bit type before the weighted sum, which is fp32 and rounded again (half the bytes between the two kernels;
+    ``grouped_matmul`` with ``out_dtype=torch.float32`` and ``combine_rows`` keep them in fp32). Differentiable in x, B
+    and the weights."""
     four_bits = isinstance(weight, W4Weight)
     _need(four_bits or weight.dim() == 3, "the weight must be [experts, n, k]")
     num = weight.matrices if four_bits else weight.shape[0]
