@@ -106,8 +106,8 @@ typedef struct {
  * fp32 planes in the workspace that a second kernel adds in their order.
  * Errors: GEMM_ERR_INVALID (null pointer, bad enum, negative size, ld or stride too small, workspace
  *         too small), GEMM_ERR_UNSUPPORTED (types; rows beyond 2^31 - 1; experts beyond 2^24; more than
- *         2^24 output tiles; a leading dimension of 2^20 elements or more; experts times stride beyond 2^54 elements),
- *         GEMM_ERR_HIP.
+ *         2^24 output tiles; a leading dimension of 2^20 elements or more; experts times stride beyond
+ *         2^54 elements), GEMM_ERR_HIP.
  */
 gemm_status_t gemm_grouped_workspace_bytes(const gemm_grouped_t* p, const void* X, const void* Y, int64_t* out);
 gemm_status_t gemm_grouped_run(const gemm_grouped_t* p, const void* X, const void* Y, void* out,

@@ -3,7 +3,8 @@
 //
 // Rows sorted by expert are described by offsets[0 .. E] in device memory: expert e owns rows
 // [offsets[e], offsets[e+1]). Rows before offsets[0] (some experts of an order) and from offsets[E] on
-// belong to nobody. The counts are not known to the host, so a launch covers an upper bound of row blocks and every unit looks its expert up.
+// belong to nobody. The counts are not known to the host, so a launch covers an upper bound of row blocks and
+// every unit looks its expert up.
 #pragma once
 
 #include "spt_common.h"

@@ -127,9 +127,9 @@ struct GroupedShape {
 
 // 32-row tiles: with at most two of them for every compute unit and rows of whole 16-byte chunks, two
 // workgroups of six stages, five in flight, and the hint that keeps Y, which is read once then, out of the caches
-// (64 rows, 8 experts, 4096^2: 44 us against 57 with three workgroups of four stages, three in flight). With more tiles a third
-// workgroup saves a round (200 rows: 59 against 77), and off 16 bytes neighbouring loads share lines, and the
-// hint costs (2044 columns: 56 us against 49).
+// (64 rows, 8 experts, 4096^2: 44 us against 57 with three workgroups of four stages, three in flight). With more
+// tiles a third workgroup saves a round (200 rows: 59 against 77), and off 16 bytes neighbouring loads share lines,
+// and the hint costs (2044 columns: 56 us against 49).
 int64_t grouped_small_tiles(const gemm_grouped_t* p) {
   const int64_t out_n = p->mode == GEMM_GROUPED_FORWARD ? p->n : p->k;
   const int64_t used = p->experts < p->rows ? p->experts : p->rows;

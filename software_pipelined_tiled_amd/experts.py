@@ -10,8 +10,9 @@ operand: kernels read and write at once.
 ``gather_rows``, ``combine_rows``, ``grouped_matmul`` and ``routed_matmul`` are differentiable once, in reverse mode;
 operands with a forward-mode tangent are refused. The ``*_grad`` functions are the same gradients as plain calls, for
 programs that keep no autograd graph; of tensors that require grad they stay in the graph, where differentiating them
-raises. A training step captured into a HIP graph is safest with those: while an eager graph of the same leaves is alive,
-torch's backward ties a capture to that graph's stream and ends the process.
+raises. A training step captured into a HIP graph is safest with those, under ``torch.no_grad()``: while an eager graph of
+the same leaves is alive (a result that stayed in it will do), torch's backward ties a capture to that graph's stream and
+ends the process.
 """
 from __future__ import annotations
 

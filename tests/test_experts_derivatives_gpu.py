@@ -164,3 +164,33 @@ def test_tensors_with_a_tangent_are_refused():
         with pytest.raises(ValueError, match="forward-mode"):
             torch.autograd.grad(out, leaf, dual(torch.ones_like(out)))
     assert torch.equal(spt.gather_rows(x, order), rows)
+
+
+# -------------------------------------------------------------------------------------- captured
+
+@pytest.mark.parametrize("grad_mode", [False, True])
+def test_gradients_of_leaves_captured_while_eager_ones_live(grad_mode):
+    # a training step by the gradients' own calls, with parameters as operands: its results stay in the graph where
+    # grad mode is on, and neither they nor eager results of the same leaves stand in the way of a capture
+    _, order, _, rows, b, _ = operands()
+    b.requires_grad_()
+    dc = torch.arange(8, device="cuda", dtype=BF16)[:, None].repeat(1, 32)
+
+    def step():
+        da = spt.grouped_matmul_grad_a(dc, b, order.offsets)
+        return [da, spt.grouped_matmul_grad_b(dc, rows, order.offsets), spt.gather_rows_grad(da, order)]
+    with torch.set_grad_enabled(grad_mode):
+        eager = step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = step()
+    for rep in range(3):
+        dc.add_(1)
+        g.replay()
+        with torch.no_grad():
+            want = step()
+        torch.cuda.synchronize()
+        for a, e in zip(got, want):
+            assert torch.equal(a, e), rep
+    assert eager[0].requires_grad == grad_mode and got[0].requires_grad == grad_mode
