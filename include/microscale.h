@@ -1,0 +1,126 @@
+/*
+ * microscale.h — C ABI of products in microscaled formats and of the norm that writes their operands, for
+ * AMD Instinct MI355X (gfx950).
+ *
+ * A microscaled (MX) tensor [rows, k] holds each value in 8 bits (e4m3: 4 exponent and 3 mantissa bits, up to 448)
+ * or 4 (e2m1: up to 6), with one scale, a power of two, for each block of 32 neighbours of a row. Scales are bytes s
+ * that stand for 2^(s - 127); 255 stands for NaN, and so does every value of its block. Layout, for kb = 4 * ceil(k / 128)
+ * blocks a row (those behind k hold zeros):
+ *   codes   [rows][kb * 32 * bits / 8] bytes; of two 4-bit values in a byte the first is in its low half
+ *   scales  [ceil(rows / 64)][kb][64] bytes: row i's block b at ((i / 64) * kb + b) * 64 + i % 64
+ * Both begin on 16 bytes. The products read neighbouring rows' scales of one block together, hence blocks of 64 rows.
+ *
+ * Conventions of gemm.h hold: entry points only enqueue kernels on `stream` for the current device, allocate
+ * nothing, never synchronise, return a gemm_status_t and throw nothing. Workspaces are the caller's (a
+ * *_workspace_bytes function gives the size; 0: none needed, NULL allowed), their contents need no preparation, and
+ * calls that may overlap need one each. Outputs and workspaces must not overlap an operand unless stated. All entry
+ * points may be recorded into a HIP graph (kernels only), after one call on that device outside the capture.
+ * Dimensions are counted in elements, leading dimensions too. Tensors that are not MX may have any element alignment.
+ */
+#ifndef SPT_MICROSCALE_H
+#define SPT_MICROSCALE_H
+
+#include "gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* ------------------------------------------------------------------ microscaled tensors */
+
+/*
+ * Bytes of an MX tensor's codes and scales.
+ * Errors (here and below): GEMM_ERR_INVALID (a null pointer, a negative size, a leading dimension below the row,
+ *         bits not 4 or 8, a bad enum, codes or scales off 16 bytes, workspace too small), GEMM_ERR_UNSUPPORTED (rows
+ *         beyond 2^31 - 64, k beyond 2^22; types), GEMM_ERR_HIP.
+ */
+gemm_status_t mx_bytes(int64_t rows, int64_t k, int bits, int64_t* codes, int64_t* scales);
+
+/*
+ * x [rows, k], row stride ldx, F16, BF16 or F32, to MX: a block's scale is 2^(floor(log2 of its largest magnitude) - e),
+ * e = 8 (e4m3) or 2 (e2m1), not below 2^-127; each value is divided by it and rounded to the nearest of the format, ties
+ * to the even code, magnitudes beyond the largest to the largest. Every step but that rounding is exact. A block with
+ * an infinity or a NaN gets the scale NaN and zeros as codes.
+ */
+gemm_status_t mx_quantize(const void* x, gemm_dtype_t dtype, int64_t rows, int64_t k, int64_t ldx, int bits, void* codes,
+                          void* scales, void* stream);
+
+/* The values of an MX tensor, out [rows, k] in F16, BF16 or F32, rounded once. */
+gemm_status_t mx_dequantize(const void* codes, const void* scales, int bits, int64_t rows, int64_t k, void* out,
+                            gemm_dtype_t dtype, int64_t ldo, void* stream);
+
+/*
+ * Lay out what a checkpoint holds row by row: codes [rows, ceil(k * bits / 8)] bytes, row stride ldc bytes, and scales
+ * [rows, ceil(k / 32)] bytes, row stride lds.
+ */
+gemm_status_t mx_pack(const void* codes, int64_t ldc, const void* scales, int64_t lds, int bits, int64_t rows, int64_t k,
+                      void* out_codes, void* out_scales, void* stream);
+
+/* ------------------------------------------------------------------ products */
+
+/*
+ * C[m, n] = A . B^T of MX tensors A [m, k] (a_bits) and B [n, k] (b_bits): 8 x 8, 4 x 4 or 8 x 4. C in F16, BF16 or
+ * F32, row stride ldc, rounded once from an fp32 sum.
+ *   16-bit results, and all of 4 x 4, come from the scaled matrix instructions. For operands of 8 bits these keep, of
+ * the products that they add at a time, 13 bits below the largest (on Gaussian data 1.5e-5 of a result's size for 8 x 8
+ * and 5e-6 for 8 x 4, a hundredth and less of a 16-bit rounding). With F32 results operands of 8 bits go through
+ * bf16 matrix instructions instead, whose sums are fp32 throughout, at less than half the rate; values then have to be
+ * bf16 numbers, which all but those with scales under 2^-117 or over 2^119 are.
+ *   Few output tiles with a long sum are cut over workgroups into fp32 planes in the workspace, which a second kernel
+ * adds in their order: results do not change from run to run.
+ * Errors: as above; GEMM_ERR_UNSUPPORTED (4 x 8; ldc of 2^20 or more; more than 2^24 tiles of 64 x 64).
+ */
+typedef struct {
+  int64_t m, n, k;
+  int a_bits, b_bits;
+  gemm_dtype_t out_dtype;
+  int64_t ldc;
+} gemm_mx_t;
+gemm_status_t gemm_mx_workspace_bytes(const gemm_mx_t* p, int64_t* out);
+gemm_status_t gemm_mx_run(const gemm_mx_t* p, const void* a_codes, const void* a_scales, const void* b_codes,
+                          const void* b_scales, void* C, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------ root-mean-square norm */
+
+/*
+ * h = x + residual, rounded to `dtype` (x itself without a residual), and y = h / sqrt(mean(h^2) + eps) * weight over
+ * rows of n: the statistics in fp32, y rounded once. dtype F16, BF16 or F32 for x, residual, h and y; weight [n] F16,
+ * BF16 or F32, or NULL for ones. The sum of a row's squares has to stay inside fp32's range.
+ *   h is written where `residual` is given, and may be x's or residual's own memory (the same rows), y x's.
+ * Errors: as above; GEMM_ERR_INVALID (eps negative or not finite), GEMM_ERR_UNSUPPORTED (rows beyond 2^31 - 64, n beyond 2^24).
+ */
+typedef struct {
+  int64_t rows, n;
+  gemm_dtype_t dtype, weight_dtype;
+  float eps;
+  int64_t ldx, ldr, ldh, ldy;
+} norm_rms_t;
+gemm_status_t norm_rms_run(const norm_rms_t* p, const void* x, const void* residual, const void* weight, void* h, void* y,
+                           void* stream);
+
+/* The same with y as an MX tensor of `bits` 4 or 8, quantised from its fp32 values (ldy is not used; n up to 2^22). */
+gemm_status_t norm_rms_mx_run(const norm_rms_t* p, int bits, const void* x, const void* residual, const void* weight,
+                              void* h, void* codes, void* scales, void* stream);
+
+/*
+ * Gradients of norm_rms_run: with g = dy * weight, r = 1 / sqrt(mean(h^2) + eps) and c = h * r,
+ *   dx = r * (g - c * mean(g * c)) + dh       (x's and the residual's alike; dh NULL: none reached h by itself)
+ *   dweight = sum over rows of dy * c         (NULL: not wanted)
+ * All sums are fp32 and in a fixed order; dx in `dtype` and dweight in `weight_dtype`, rounded once. dx may be dy's or
+ * dh's own memory. The workspace holds each workgroup's sums of dweight.
+ */
+typedef struct {
+  int64_t rows, n;
+  gemm_dtype_t dtype, weight_dtype;
+  float eps;
+  int64_t lddy, ldh, lddh, lddx;
+} norm_rms_grad_t;
+gemm_status_t norm_rms_grad_workspace_bytes(const norm_rms_grad_t* p, int wants_dweight, int64_t* out);
+gemm_status_t norm_rms_grad_run(const norm_rms_grad_t* p, const void* dy, const void* h, const void* weight, const void* dh,
+                                void* dx, void* dweight, void* workspace, int64_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SPT_MICROSCALE_H */

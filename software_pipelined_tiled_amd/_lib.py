@@ -26,6 +26,10 @@ EXPORTS = ("gemm_plan_create", "gemm_run", "gemm_run_noalloc", "gemm_plan_destro
 EXPERT_EXPORTS = ("experts_sort_workspace_bytes", "experts_sort", "experts_gather", "experts_combine", "experts_combine_grad",
                   "gemm_grouped_workspace_bytes", "gemm_grouped_run", "gemm_w4_packed_bytes", "gemm_w4_pack",
                   "gemm_w4_workspace_bytes", "gemm_w4_run")
+
+# every entry point include/microscale.h declares
+MX_EXPORTS = ("mx_bytes", "mx_quantize", "mx_dequantize", "mx_pack", "gemm_mx_workspace_bytes", "gemm_mx_run", "norm_rms_run",
+              "norm_rms_mx_run", "norm_rms_grad_workspace_bytes", "norm_rms_grad_run")
 GEMM_GROUPED_FORWARD, GEMM_GROUPED_GRAD_A, GEMM_GROUPED_GRAD_B = 0, 1, 2
 
 
@@ -65,6 +69,23 @@ class GemmW4(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("matrices", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("group", ctypes.c_int), ("has_zeros", ctypes.c_int), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
                 ("ldx", ctypes.c_int64), ("ldo", ctypes.c_int64), ("zero_rest", ctypes.c_int)]
+
+
+class GemmMx(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("a_bits", ctypes.c_int),
+                ("b_bits", ctypes.c_int), ("out_dtype", ctypes.c_int), ("ldc", ctypes.c_int64)]
+
+
+class NormRms(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64), ("ldh", ctypes.c_int64),
+                ("ldy", ctypes.c_int64)]
+
+
+class NormRmsGrad(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n", ctypes.c_int64), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("lddy", ctypes.c_int64), ("ldh", ctypes.c_int64), ("lddh", ctypes.c_int64),
+                ("lddx", ctypes.c_int64)]
 
 
 _lib = None
@@ -127,7 +148,17 @@ def lib() -> ctypes.CDLL:
             ("gemm_w4_packed_bytes", [i64, i64, i64, i32, i32, P(i64)]),
             ("gemm_w4_pack", [vp, vp, vp, i64, i64, i64, i32, vp, vp]),
             ("gemm_w4_workspace_bytes", [P(GemmW4), i32, P(i64)]),
-            ("gemm_w4_run", [P(GemmW4), vp, vp, vp, vp, vp, i64, vp])):
+            ("gemm_w4_run", [P(GemmW4), vp, vp, vp, vp, vp, i64, vp]),
+            ("mx_bytes", [i64, i64, i32, P(i64), P(i64)]),
+            ("mx_quantize", [vp, i32, i64, i64, i64, i32, vp, vp, vp]),
+            ("mx_dequantize", [vp, vp, i32, i64, i64, vp, i32, i64, vp]),
+            ("mx_pack", [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp]),
+            ("gemm_mx_workspace_bytes", [P(GemmMx), P(i64)]),
+            ("gemm_mx_run", [P(GemmMx), vp, vp, vp, vp, vp, vp, i64, vp]),
+            ("norm_rms_run", [P(NormRms), vp, vp, vp, vp, vp, vp]),
+            ("norm_rms_mx_run", [P(NormRms), i32, vp, vp, vp, vp, vp, vp, vp]),
+            ("norm_rms_grad_workspace_bytes", [P(NormRmsGrad), i32, P(i64)]),
+            ("norm_rms_grad_run", [P(NormRmsGrad), vp, vp, vp, vp, vp, vp, vp, i64, vp])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = i32, args
     _lib = L
@@ -293,4 +324,24 @@ def gemm_w4_packed_bytes(matrices: int, n: int, k: int, group: int, has_zeros: b
 def gemm_w4_workspace_bytes(p: GemmW4, has_offsets: bool) -> int:
     n = ctypes.c_int64()
     _check(lib().gemm_w4_workspace_bytes(ctypes.byref(p), int(has_offsets), ctypes.byref(n)), "gemm_w4_workspace_bytes")
+    return n.value
+
+
+def mx_bytes(rows: int, k: int, bits: int) -> tuple[int, int]:
+    """Bytes of a microscaled tensor's codes and of its scales."""
+    c, s = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().mx_bytes(rows, k, bits, ctypes.byref(c), ctypes.byref(s)), "mx_bytes")
+    return c.value, s.value
+
+
+def gemm_mx_workspace_bytes(p: GemmMx) -> int:
+    n = ctypes.c_int64()
+    _check(lib().gemm_mx_workspace_bytes(ctypes.byref(p), ctypes.byref(n)), "gemm_mx_workspace_bytes")
+    return n.value
+
+
+def norm_rms_grad_workspace_bytes(p: NormRmsGrad, wants_dweight: bool) -> int:
+    n = ctypes.c_int64()
+    _check(lib().norm_rms_grad_workspace_bytes(ctypes.byref(p), int(wants_dweight), ctypes.byref(n)),
+           "norm_rms_grad_workspace_bytes")
     return n.value

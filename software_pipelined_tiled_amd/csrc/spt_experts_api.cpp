@@ -1,84 +1,19 @@
 // Host side of include/experts.h: argument checks, the choice of a kernel, launches. Nothing here
 // allocates or synchronises, and no state outlives a call but the devices' properties.
-#include <cstring>
-#include <mutex>
-
 #include "experts.h"
 #include "spt_experts.h"
+#include "spt_host.h"
 
 namespace {
 
-constexpr int64_t kMax32 = 0x7FFFFFFF;
+using namespace spt;
+
 constexpr int kMaxExperts = 1024;  // of the sort, whose workgroups count in LDS
 constexpr int64_t kMaxGroups = (int64_t)1 << 24;  // of the products: the search adds 64 to their number in 32 bits
 // Output tiles of a grouped product: 64 experts' counts add up in 32 bits whatever the offsets hold. Of the
 // smallest tiles these are 2^35 elements.
 constexpr int64_t kMaxUnits = (int64_t)1 << 24;
-constexpr int kMaxDevices = 64;
-// Bytes of one operand: byte counts and offsets stay inside 64 bits, and no memory is as large.
-constexpr int64_t kMaxBytes = (int64_t)1 << 56;
 constexpr int64_t kMaxGridY = 65535;
-constexpr int kCus = 256;  // the MI355X's, for choices that must not depend on the device in use
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
-bool is16(gemm_dtype_t d) { return d == GEMM_F16 || d == GEMM_BF16; }
-bool is_dtype(gemm_dtype_t d) { return is16(d) || d == GEMM_F32; }
-
-// Compute units of the current device; GEMM_ERR_HIP unless it is a gfx950.
-gemm_status_t device_cus(int* cu) {
-  static std::mutex mu;
-  static int known[kMaxDevices];
-  int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) {
-    (void)hipGetLastError();
-    return GEMM_ERR_HIP;
-  }
-  if (dev < 0 || dev >= kMaxDevices) return GEMM_ERR_UNSUPPORTED;
-  std::lock_guard<std::mutex> lock(mu);
-  if (known[dev] == 0) {
-    hipDeviceProp_t prop;
-    if (hipGetDeviceProperties(&prop, dev) != hipSuccess) {
-      (void)hipGetLastError();
-      return GEMM_ERR_HIP;
-    }
-    if (std::strncmp(prop.gcnArchName, "gfx950", 6) != 0) return GEMM_ERR_HIP;
-    known[dev] = prop.multiProcessorCount;
-  }
-  *cu = known[dev];
-  return GEMM_OK;
-}
-
-gemm_status_t launch(const void* fn, dim3 grid, int threads, int lds, void* arg, void* stream) {
-  void* kargs[] = {arg};
-  if (hipLaunchKernel(fn, grid, dim3(threads), kargs, lds, (hipStream_t)stream) != hipSuccess) {
-    (void)hipGetLastError();
-    return GEMM_ERR_HIP;
-  }
-  return GEMM_OK;
-}
-
-int stream_grid(int64_t threads) {
-  const int64_t b = ceil_div(threads, 256);
-  return (int)(b < 1 ? 1 : (b > 8192 ? 8192 : b));
-}
-
-// out = the planes of a cut sum, added in their order; with offsets, the experts' rows only
-gemm_status_t add_planes(const float* parts, void* out, const int32_t* offsets, int64_t experts, int64_t ldo, int64_t rows,
-                         int64_t n, int64_t splits, int out_dtype, void* stream) {
-  spt::PlaneArgs r;
-  r.parts = parts;
-  r.out = (char*)out;
-  r.offsets = offsets;
-  r.ldo = ldo;
-  r.plane = rows * n;
-  r.rows = (int)rows;
-  r.experts = (int)experts;
-  r.n = (int)n;
-  r.splits = (int)splits;
-  r.out_dtype = out_dtype;
-  return launch(spt::add_planes_fn(), dim3(stream_grid(r.plane)), 256, 0, &r, stream);
-}
 
 // ---------------------------------------------------------------------------------- sort
 // One workgroup sorts up to kSortOne slots by itself (4096 slots of 64 experts: 6.7 us in one launch, 6.9 in

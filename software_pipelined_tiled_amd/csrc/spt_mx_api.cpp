@@ -1,0 +1,322 @@
+// Host side of include/microscale.h: argument checks, the choice of a kernel, launches. Nothing here allocates or
+// synchronises, and no state outlives a call but the devices' properties.
+#include <cmath>
+
+#include "microscale.h"
+#include "spt_host.h"
+#include "spt_mx.h"
+
+namespace {
+
+using namespace spt;
+
+constexpr int64_t kMaxRows = kMax32 - 63;             // their number rounded up to 64 stays inside 32 bits
+constexpr int64_t kMaxK = (int64_t)1 << 22;           // 256 rows of it stay inside a buffer's 32-bit offsets
+constexpr int64_t kMaxNorm = (int64_t)1 << 24;
+constexpr int64_t kMaxLdc = (int64_t)1 << 20;
+constexpr int64_t kMaxTiles = (int64_t)1 << 24;       // of 64 x 64
+
+bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }
+bool whole16(const void* p, int64_t ld, gemm_dtype_t dtype) { return on16(p) && ld * (dtype == GEMM_F32 ? 4 : 2) % 16 == 0; }
+
+gemm_status_t check_mx(int64_t rows, int64_t k, int bits) {
+  if (rows < 0 || k < 0 || (bits != 4 && bits != 8)) return GEMM_ERR_INVALID;
+  if (rows > kMaxRows || k > kMaxK) return GEMM_ERR_UNSUPPORTED;
+  return GEMM_OK;
+}
+
+// Units of 64 rows by 512 columns, and the workgroups that walk over them.
+struct Units {
+  int64_t units;
+  unsigned grid;
+};
+Units mx_units(int64_t rows, int64_t blocks) {
+  Units u;
+  u.units = ceil_div(rows, kMxScaleRows) * ceil_div(blocks, 16);
+  u.grid = (unsigned)(u.units < 65536 ? u.units : 65536);
+  return u;
+}
+
+// ---------------------------------------------------------------------------------- products
+struct MxShape {
+  MxEntry entry;
+  bool exact;
+  int64_t tiles_m, tiles_n, ktiles, splits, per, ws;
+};
+
+gemm_status_t mx_shape(const gemm_mx_t* p, MxShape* s) {
+  if (!p || !is_dtype(p->out_dtype) || p->ldc < p->n) return GEMM_ERR_INVALID;
+  gemm_status_t st = check_mx(p->m, p->k, p->a_bits);
+  if (st == GEMM_OK) st = check_mx(p->n, p->k, p->b_bits);
+  if (st != GEMM_OK) return st;
+  if ((p->a_bits == 4 && p->b_bits == 8) || p->ldc >= kMaxLdc) return GEMM_ERR_UNSUPPORTED;
+  const int64_t small = ceil_div(p->m, 64) * ceil_div(p->n, 64);
+  if (small > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
+  s->exact = p->out_dtype == GEMM_F32 && p->a_bits == 8;
+  s->entry = mx_tile_entry(p->a_bits, p->b_bits, s->exact);
+  s->tiles_m = ceil_div(p->m, s->entry.bm);
+  s->tiles_n = ceil_div(p->n, s->entry.bn);
+  s->ktiles = ceil_div(mx_blocks(p->k) / 4, s->entry.ksteps);
+  const int64_t tiles = s->tiles_m * s->tiles_n;
+  s->splits = 1;
+  if (tiles > 0 && tiles < kCus) {
+    const int64_t fit = kCus / tiles, most = s->ktiles / 4;
+    s->splits = fit < most ? fit : most;
+    if (s->splits < 1) s->splits = 1;
+  }
+  s->per = ceil_div(s->ktiles, s->splits);
+  s->splits = s->per > 0 ? ceil_div(s->ktiles, s->per) : 1;
+  s->ws = s->splits > 1 ? s->splits * p->m * p->n * 4 : 0;
+  return GEMM_OK;
+}
+
+// ---------------------------------------------------------------------------------- norm
+// Pieces of eight values a thread keeps, and threads of a workgroup. 0 pieces: a row too long for registers.
+struct NormShape {
+  int c, threads;
+  int64_t per, grid;
+};
+NormShape norm_shape(int64_t rows, int64_t n, int per_cu) {
+  NormShape s;
+  const int64_t pieces = ceil_div(n, 8);
+  s.c = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : pieces <= 4096 ? 4 : 0;
+  s.threads = s.c ? (int)round_up(ceil_div(pieces, s.c), 64) : 1024;
+  const int64_t fit = (int64_t)kCus * per_cu;
+  s.per = ceil_div(rows, fit);
+  s.grid = s.per > 0 ? ceil_div(rows, s.per) : 0;
+  return s;
+}
+
+gemm_status_t check_norm(const norm_rms_t* p) {
+  if (!p || p->rows < 0 || p->n < 0 || !is_dtype(p->dtype) || !is_dtype(p->weight_dtype)) return GEMM_ERR_INVALID;
+  if (!(p->eps >= 0.f) || !std::isfinite(p->eps)) return GEMM_ERR_INVALID;
+  if (p->rows > kMaxRows || p->n > kMaxNorm) return GEMM_ERR_UNSUPPORTED;
+  return GEMM_OK;
+}
+
+gemm_status_t run_norm(const norm_rms_t* p, int out, const void* x, const void* residual, const void* weight, void* h,
+                       void* y, void* scales, void* stream) {
+  gemm_status_t st = check_norm(p);
+  if (st != GEMM_OK) return st;
+  if (out && p->n > kMaxK) return GEMM_ERR_UNSUPPORTED;
+  if (p->ldx < p->n || (residual && (p->ldr < p->n || p->ldh < p->n)) || (!out && p->ldy < p->n)) return GEMM_ERR_INVALID;
+  if (p->rows == 0 || p->n == 0) return GEMM_OK;
+  if (!x || !y || (residual && !h) || (out && (!scales || !on16(y) || !on16(scales)))) return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  NormArgs a{};
+  a.x = (const char*)x;
+  a.r = (const char*)residual;
+  a.w = (const char*)weight;
+  a.h = (char*)h;
+  a.y = (char*)y;
+  a.scales = (unsigned char*)scales;
+  a.rows = p->rows; a.ldx = p->ldx; a.ldr = p->ldr; a.ldh = p->ldh; a.ldy = p->ldy;
+  a.n = (int)p->n;
+  a.blocks = (int)mx_blocks(p->n);
+  a.wtype = (int)p->weight_dtype;
+  a.eps = p->eps;
+  a.vec = (whole16(x, p->ldx, p->dtype) ? 1 : 0) | (whole16(residual, p->ldr, p->dtype) ? 2 : 0) |
+          (whole16(h, p->ldh, p->dtype) ? 4 : 0) | (whole16(y, p->ldy, p->dtype) ? 8 : 0) | (on16(weight) ? 16 : 0);
+  const NormShape s = norm_shape(p->rows, out ? mx_blocks(p->n) * kMxBlock : p->n, 8);
+  a.per = s.per;
+  return launch(norm_fn((int)p->dtype, out, s.c), dim3((unsigned)s.grid), s.threads, 0, &a, stream);
+}
+
+gemm_status_t check_grad(const norm_rms_grad_t* p) {
+  if (!p) return GEMM_ERR_INVALID;
+  norm_rms_t f{};
+  f.rows = p->rows; f.n = p->n; f.dtype = p->dtype; f.weight_dtype = p->weight_dtype; f.eps = p->eps;
+  return check_norm(&f);
+}
+NormShape grad_shape(const norm_rms_grad_t* p) { return norm_shape(p->rows, p->n, 4); }
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t mx_bytes(int64_t rows, int64_t k, int bits, int64_t* codes, int64_t* scales) {
+  if (!codes || !scales) return GEMM_ERR_INVALID;
+  const gemm_status_t st = check_mx(rows, k, bits);
+  if (st != GEMM_OK) return st;
+  *codes = rows * mx_row_bytes(k, bits);
+  *scales = round_up(rows, kMxScaleRows) * mx_blocks(k);
+  return GEMM_OK;
+}
+
+gemm_status_t mx_quantize(const void* x, gemm_dtype_t dtype, int64_t rows, int64_t k, int64_t ldx, int bits, void* codes,
+                          void* scales, void* stream) {
+  gemm_status_t st = check_mx(rows, k, bits);
+  if (st != GEMM_OK) return st;
+  if (!is_dtype(dtype) || ldx < k) return GEMM_ERR_INVALID;
+  if (rows == 0 || k == 0) return GEMM_OK;
+  if (!x || !codes || !scales || !on16(codes) || !on16(scales)) return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  MxQuantArgs a;
+  a.x = (const char*)x;
+  a.codes = (unsigned char*)codes;
+  a.scales = (unsigned char*)scales;
+  a.rows = rows; a.ldx = ldx;
+  a.k = (int)k;
+  a.blocks = (int)mx_blocks(k);
+  const Units u = mx_units(rows, a.blocks);
+  a.units = u.units;
+  a.vec = whole16(x, ldx, dtype);
+  return launch(mx_quantize_fn((int)dtype, bits), dim3(u.grid), 256, 0, &a, stream);
+}
+
+gemm_status_t mx_dequantize(const void* codes, const void* scales, int bits, int64_t rows, int64_t k, void* out,
+                            gemm_dtype_t dtype, int64_t ldo, void* stream) {
+  gemm_status_t st = check_mx(rows, k, bits);
+  if (st != GEMM_OK) return st;
+  if (!is_dtype(dtype) || ldo < k) return GEMM_ERR_INVALID;
+  if (rows == 0 || k == 0) return GEMM_OK;
+  if (!out || !codes || !scales || !on16(codes) || !on16(scales)) return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  MxValuesArgs a;
+  a.codes = (const unsigned char*)codes;
+  a.scales = (const unsigned char*)scales;
+  a.out = (char*)out;
+  a.rows = rows; a.ldo = ldo;
+  a.k = (int)k;
+  a.blocks = (int)mx_blocks(k);
+  const Units u = mx_units(rows, a.blocks);
+  a.units = u.units;
+  a.vec = whole16(out, ldo, dtype);
+  return launch(mx_values_fn((int)dtype, bits), dim3(u.grid), 256, 0, &a, stream);
+}
+
+gemm_status_t mx_pack(const void* codes, int64_t ldc, const void* scales, int64_t lds, int bits, int64_t rows, int64_t k,
+                      void* out_codes, void* out_scales, void* stream) {
+  gemm_status_t st = check_mx(rows, k, bits);
+  if (st != GEMM_OK) return st;
+  if (ldc < ceil_div(k * bits, 8) || lds < ceil_div(k, kMxBlock)) return GEMM_ERR_INVALID;
+  if (rows == 0 || k == 0) return GEMM_OK;
+  if (!codes || !scales || !out_codes || !out_scales || !on16(out_codes) || !on16(out_scales)) return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  MxPackArgs a;
+  a.codes = (const unsigned char*)codes;
+  a.scales = (const unsigned char*)scales;
+  a.out_codes = (unsigned char*)out_codes;
+  a.out_scales = (unsigned char*)out_scales;
+  a.rows = rows; a.ldc = ldc; a.lds = lds;
+  a.k = (int)k;
+  a.blocks = (int)mx_blocks(k);
+  a.bits = bits;
+  const Units u = mx_units(rows, a.blocks);
+  a.units = u.units;
+  return launch(mx_pack_fn(), dim3(u.grid), 256, 0, &a, stream);
+}
+
+gemm_status_t gemm_mx_workspace_bytes(const gemm_mx_t* p, int64_t* out) {
+  if (!out) return GEMM_ERR_INVALID;
+  MxShape s;
+  const gemm_status_t st = mx_shape(p, &s);
+  if (st == GEMM_OK) *out = s.ws;
+  return st;
+}
+
+gemm_status_t gemm_mx_run(const gemm_mx_t* p, const void* a_codes, const void* a_scales, const void* b_codes,
+                          const void* b_scales, void* C, void* workspace, int64_t workspace_bytes, void* stream) {
+  MxShape s;
+  gemm_status_t st = mx_shape(p, &s);
+  if (st != GEMM_OK) return st;
+  if (p->m == 0 || p->n == 0) return GEMM_OK;
+  if (!C || (p->k > 0 && (!a_codes || !a_scales || !b_codes || !b_scales))) return GEMM_ERR_INVALID;
+  if (!on16(a_codes) || !on16(a_scales) || !on16(b_codes) || !on16(b_scales)) return GEMM_ERR_INVALID;
+  if (s.ws > 0 && (!workspace || !on16(workspace) || workspace_bytes < s.ws)) return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  MxGemmArgs a{};
+  a.a = (const char*)a_codes;
+  a.as = (const char*)a_scales;
+  a.b = (const char*)b_codes;
+  a.bs = (const char*)b_scales;
+  a.c = s.splits > 1 ? (char*)workspace : (char*)C;
+  a.m = (int)p->m;
+  a.n = (int)p->n;
+  a.blocks = (int)mx_blocks(p->k);
+  a.ksteps = a.blocks / 4;
+  a.ldc = s.splits > 1 ? p->n : p->ldc;
+  a.out_dtype = s.splits > 1 ? (int)GEMM_F32 : (int)p->out_dtype;
+  a.tiles_m = (int)s.tiles_m;
+  a.tiles_n = (int)s.tiles_n;
+  a.group_m = 8;
+  a.splits = (int)s.splits;
+  a.per = (int)s.per;
+  a.plane = s.splits > 1 ? p->m * p->n : 0;
+  a.units = (int)(s.tiles_m * s.tiles_n * s.splits);
+  a.grid = a.units;
+  st = launch(s.entry.fn, dim3((unsigned)a.grid), s.entry.threads, 0, &a, stream);
+  if (st != GEMM_OK || s.splits == 1) return st;
+  return add_planes((const float*)workspace, C, nullptr, 0, p->ldc, p->m, p->n, s.splits, (int)p->out_dtype, stream);
+}
+
+gemm_status_t norm_rms_run(const norm_rms_t* p, const void* x, const void* residual, const void* weight, void* h, void* y,
+                           void* stream) {
+  return run_norm(p, 0, x, residual, weight, h, y, nullptr, stream);
+}
+
+gemm_status_t norm_rms_mx_run(const norm_rms_t* p, int bits, const void* x, const void* residual, const void* weight,
+                              void* h, void* codes, void* scales, void* stream) {
+  if (bits != 4 && bits != 8) return GEMM_ERR_INVALID;
+  return run_norm(p, bits, x, residual, weight, h, codes, scales, stream);
+}
+
+gemm_status_t norm_rms_grad_workspace_bytes(const norm_rms_grad_t* p, int wants_dweight, int64_t* out) {
+  if (!out) return GEMM_ERR_INVALID;
+  const gemm_status_t st = check_grad(p);
+  if (st == GEMM_OK) *out = wants_dweight ? grad_shape(p).grid * p->n * 4 : 0;
+  return st;
+}
+
+gemm_status_t norm_rms_grad_run(const norm_rms_grad_t* p, const void* dy, const void* h, const void* weight, const void* dh,
+                                void* dx, void* dweight, void* workspace, int64_t workspace_bytes, void* stream) {
+  gemm_status_t st = check_grad(p);
+  if (st != GEMM_OK) return st;
+  if (p->lddy < p->n || p->ldh < p->n || (dh && p->lddh < p->n) || (dx && p->lddx < p->n)) return GEMM_ERR_INVALID;
+  if (p->n == 0 || (!dx && !dweight)) return GEMM_OK;
+  if (p->rows > 0 && (!dy || !h)) return GEMM_ERR_INVALID;
+  const NormShape s = grad_shape(p);
+  const int64_t need = dweight ? s.grid * p->n * 4 : 0;
+  if (need > 0 && (!workspace || !on16(workspace) || workspace_bytes < need)) return GEMM_ERR_INVALID;
+  int cu = 0;
+  st = device_cus(&cu);
+  if (st != GEMM_OK) return st;
+  if (p->rows > 0) {
+    NormGradArgs a{};
+    a.dy = (const char*)dy;
+    a.h = (const char*)h;
+    a.w = (const char*)weight;
+    a.dh = (const char*)dh;
+    a.dx = (char*)dx;
+    a.parts = dweight ? (float*)workspace : nullptr;
+    a.rows = p->rows; a.lddy = p->lddy; a.ldh = p->ldh; a.lddh = p->lddh; a.lddx = p->lddx;
+    a.n = (int)p->n;
+    a.wtype = (int)p->weight_dtype;
+    a.eps = p->eps;
+    a.per = s.per;
+    a.vec = (whole16(dy, p->lddy, p->dtype) ? 1 : 0) | (whole16(h, p->ldh, p->dtype) ? 2 : 0) |
+            (whole16(dh, p->lddh, p->dtype) ? 4 : 0) | (whole16(dx, p->lddx, p->dtype) ? 8 : 0) | (on16(weight) ? 16 : 0);
+    st = launch(norm_grad_fn((int)p->dtype, s.c), dim3((unsigned)s.grid), s.threads, 0, &a, stream);
+    if (st != GEMM_OK || !dweight) return st;
+  }
+  if (!dweight) return GEMM_OK;
+  NormPartsArgs r;
+  r.parts = (const float*)workspace;
+  r.out = (char*)dweight;
+  r.n = (int)p->n;
+  r.count = (int)s.grid;  // no rows: zeros
+  r.wtype = (int)p->weight_dtype;
+  return launch(norm_parts_fn(), dim3((unsigned)ceil_div(p->n, 16)), 256, 0, &r, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,201 @@
+// Device helpers of the microscaled operators and the norm: rows in pieces of eight values, conversions to and from
+// the formats, the scaled matrix instruction.
+#pragma once
+
+#include "spt_device.h"
+#include "spt_mx.h"
+
+namespace spt {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kTypeSize[3] = {2, 2, 4};  // f16, bf16, f32
+
+template <int T>
+__device__ __forceinline__ float to_float(unsigned short v) {
+  if constexpr (T == 0) return (float)__builtin_bit_cast(_Float16, v);
+  else return __builtin_bit_cast(float, (unsigned)v << 16);
+}
+
+// The float nearest to `v` among type T's.
+template <int T>
+__device__ __forceinline__ float round_to(float v) {
+  if constexpr (T == 2) return v;
+  else if constexpr (T == 0) return (float)(_Float16)v;
+  else return (float)(__bf16)v;
+}
+
+// Eight values at `p`, of which `left` are there (the others become zeros). vec: p is on 16 bytes.
+template <int T>
+__device__ __forceinline__ void load8(const char* p, int left, bool vec, float (&v)[8]) {
+  if (left >= 8 && vec) {
+    if constexpr (T == 2) {
+      const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 16);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
+    } else {
+      const u32x4 q = *(const u32x4*)p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = to_float<T>((unsigned short)(q[e] & 0xFFFFu));
+        v[2 * e + 1] = to_float<T>((unsigned short)(q[e] >> 16));
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    v[e] = 0.f;
+    if (e < left) {
+      if constexpr (T == 2) v[e] = ((const float*)p)[e];
+      else v[e] = to_float<T>(((const unsigned short*)p)[e]);
+    }
+  }
+}
+
+template <int T>
+__device__ __forceinline__ void put8(char* p, int left, bool vec, const float (&v)[8]) {
+  if constexpr (T == 2) {
+    if (left >= 8 && vec) {
+      *(f32x4*)p = f32x4{v[0], v[1], v[2], v[3]};
+      *(f32x4*)(p + 16) = f32x4{v[4], v[5], v[6], v[7]};
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) ((float*)p)[e] = v[e];
+  } else {
+    u32x4 q;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = T == 1 ? pack_bf16(v[2 * e], v[2 * e + 1]) : pack_f16(v[2 * e], v[2 * e + 1]);
+    if (left >= 8 && vec) {
+      *(u32x4*)p = q;
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) ((unsigned short*)p)[e] = (unsigned short)(q[e >> 1] >> (16 * (e & 1)));
+  }
+}
+
+// Eight values of any type (a weight's): the type is the launch's, so the branch is the same for all lanes.
+__device__ __forceinline__ void load8_any(const char* p, int type, int64_t at, int left, bool vec, float (&v)[8]) {
+  if (type == 2) load8<2>(p + at * 4, left, vec, v);
+  else if (type == 1) load8<1>(p + at * 2, left, vec, v);
+  else load8<0>(p + at * 2, left, vec, v);
+}
+
+// ------------------------------------------------------------------------------ formats
+// A block's scale byte from eight values of each of its four lanes: the exponent of the largest magnitude less the
+// format's largest one; 255 with an infinity or NaN among them, whose bits compare as larger than any number's.
+template <int BITS>
+__device__ __forceinline__ unsigned mx_scale_of(const float (&v)[8]) {
+  unsigned m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const unsigned u = __builtin_bit_cast(unsigned, v[e]) & 0x7FFFFFFFu;
+    m = u > m ? u : m;
+  }
+  const unsigned a = (unsigned)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, true);  // quad lanes 1 0 3 2
+  m = a > m ? a : m;
+  const unsigned b = (unsigned)__builtin_amdgcn_mov_dpp((int)m, 0x4E, 0xF, 0xF, true);  // quad lanes 2 3 0 1
+  m = b > m ? b : m;
+  const int field = (int)(m >> 23), s = field - (BITS == 4 ? 2 : 8);
+  return field == 255 ? 255u : (unsigned)(s < 0 ? 0 : s);
+}
+
+// 2^(s - 127) for a byte s below 255.
+__device__ __forceinline__ float mx_scale(unsigned s) { return __builtin_bit_cast(float, s ? s << 23 : 0x00400000u); }
+
+// Eight values as codes, in 4 bytes (bits 4: the first word) or 8. The conversions divide by the scale and round to
+// nearest, ties to even; the 4-bit one saturates, the 8-bit one does not, so its input is held to 448 scales before.
+template <int BITS>
+__device__ __forceinline__ u32x2 mx_codes(const float (&v)[8], unsigned s) {
+  if (s == 255) return u32x2{0, 0};
+  const float f = mx_scale(s);
+  if constexpr (BITS == 4) {
+    unsigned q = 0;
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], f, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], f, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], f, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], f, 3);
+    return u32x2{q, 0};
+  } else {
+    const float top = 448.f * f;
+    float c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = __builtin_amdgcn_fmed3f(v[e], -top, top);
+    u32x2 r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      s16x2 p = {0, 0};
+      p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, c[4 * h], c[4 * h + 1], f, false);
+      p = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(p, c[4 * h + 2], c[4 * h + 3], f, true);
+      r[h] = __builtin_bit_cast(unsigned, p);
+    }
+    return r;
+  }
+}
+
+// The eight values of codes; scale byte 255 makes them NaN. Unscaled values are exact, and so is ldexp up to fp32's own
+// rounding of what lies below its normal numbers.
+template <int BITS>
+__device__ __forceinline__ void mx_values(u32x2 q, unsigned s, float (&v)[8]) {
+  if constexpr (BITS == 4) {
+    static_for<4>([&](auto i_c) SPT_INLINE {
+      constexpr int i = decltype(i_c)::value;
+      const f32x2 p = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[0], 1.f, i);
+      v[2 * i] = p[0];
+      v[2 * i + 1] = p[1];
+    });
+  } else {
+    static_for<4>([&](auto i_c) SPT_INLINE {
+      constexpr int i = decltype(i_c)::value;
+      const f32x2 p = __builtin_amdgcn_cvt_pk_f32_fp8((int)q[i >> 1], (i & 1) != 0);
+      v[2 * i] = p[0];
+      v[2 * i + 1] = p[1];
+    });
+  }
+  const float nan = __builtin_bit_cast(float, 0x7FC00000u);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = s == 255 ? nan : __builtin_ldexpf(v[e], (int)s - 127);
+}
+
+// ------------------------------------------------------------------------------ matrix instructions
+// D[i][j] += sum over 128 k of X[i][k] Y[j][k], 16 x 16, each operand's 32-blocks scaled. Lane l supplies row l mod 16.
+// In 4 bits its 16 bytes are block l / 16; in 8 bits its first 16 bytes are k = 16 (l / 16) .. +15 and the others 64
+// further on. Byte SX (SY) of its scale word belongs to block l / 16 in both. It holds D[4 (l / 16) + e][l mod 16].
+template <int FX, int FY, int SX, int SY>
+__device__ __forceinline__ f32x4 mfma_mx(i32x8 x, i32x8 y, f32x4 c, unsigned sx, unsigned sy) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, FX == 8 ? 0 : 4, FY == 8 ? 0 : 4, SX, (int)sx, SY, (int)sy);
+}
+
+template <int F>
+__device__ __forceinline__ i32x8 mx_operand(u32x4 lo, u32x4 hi) {
+  if constexpr (F == 8) return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  else return __builtin_shufflevector(__builtin_bit_cast(__attribute__((ext_vector_type(4))) int, lo), __builtin_bit_cast(__attribute__((ext_vector_type(4))) int, lo), 0, 1, 2, 3, -1, -1, -1, -1);
+}
+
+// Eight of a lane's 32 values (part P) of one block as bf16, scaled: 8 bits in words 2P, 2P + 1, 4 bits in word P.
+template <int F, int P>
+__device__ __forceinline__ u32x4 mx_bf16(i32x8 x, unsigned byte) {
+  const float f = byte == 255 ? __builtin_bit_cast(float, 0x7FC00000u) : mx_scale(byte);
+  u32x4 r;
+  if constexpr (F == 8) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      r[2 * w] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)x[2 * P + w], f, false));
+      r[2 * w + 1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((unsigned)x[2 * P + w], f, true));
+    }
+  } else {
+    static_for<4>([&](auto i_c) SPT_INLINE {
+      constexpr int i = decltype(i_c)::value;
+      r[i] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4((unsigned)x[P], f, i));
+    });
+  }
+  return r;
+}
+
+}  // namespace spt

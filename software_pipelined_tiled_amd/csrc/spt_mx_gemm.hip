@@ -1,0 +1,216 @@
+// Products of microscaled operands in 128 x 128 tiles: C = A . B^T through a ring of LDS stages.
+//
+// Four waves, 2 x 2, of 64 x 64 outputs each: 4 x 4 blocks of v_mfma_scale_f32_16x16x128_f8f6f4. A K-tile is 128 values
+// of k, 256 where both operands have 4 bits, so that its rows are 128 bytes of each operand (64 of a 4-bit one
+// beside an 8-bit one). The layout in LDS is the dense kernels': rows of eight (four) 16-byte chunks, chunk c of row r at
+// c XOR (r mod 8) (at c XOR ((r / 2) mod 4) in 64-byte rows), which the direct global->LDS loads make by choosing
+// each lane's source.
+//
+// Rows are staged permuted: row r of fragment f is operand row 4r + f of the wave's 64. A lane's four fragments are
+// then four neighbouring rows, whose scales of one block are one aligned word in memory (hence scales in blocks of
+// 64 rows); the instruction's operand select picks the fragment's byte, so no instruction unpacks scales. And a
+// lane's results are four neighbouring columns, a quarter-wave's 128 bytes or more of a row.
+//
+// EXACT (8-bit operands with fp32 results): a lane reads both chunks of one 32-block instead, converts them to bf16 with
+// their scale, and runs four 16x16x32 bf16 instructions, whose sums lose nothing.
+//
+// Scales go through LDS too (1 KiB a stage; 2 with 256 values of k): each wave loads those of one 64-row block.
+#include "spt_mx_device.h"
+
+namespace spt {
+
+template <int F, int KS>
+constexpr int mx_lds_row() { return F == 8 || KS == 2 ? 128 : 64; }
+
+template <int FA, int FB, bool EXACT, int S>
+__global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
+  constexpr int KS = FA == 4 && FB == 4 ? 2 : 1;  // k-steps of a K-tile
+  constexpr int RA = mx_lds_row<FA, KS>(), RB = mx_lds_row<FB, KS>();
+  constexpr int A_BYTES = 128 * RA, B_BYTES = 128 * RB, SC = KS * 256;  // SC: scales of 64 rows
+  constexpr int STAGE = A_BYTES + B_BYTES + 4 * SC;
+  constexpr int LA = A_BYTES / 4096, LB = B_BYTES / 4096, LW = LA + LB + 1;  // loads of a wave
+  static_assert(S * STAGE <= 160 * 1024 && LW * (S - 1) < 64, "ring");
+  __shared__ __attribute__((aligned(1024))) char smem[S * STAGE];
+  const unsigned smem_base = lds_addr(smem);
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r16 = lane & 15, q4 = lane >> 4;
+  int tm, tn, part;
+  unit_decode(xcd_remap(blockIdx.x, args.grid), args.tiles_m, args.tiles_n, args.group_m, tm, tn, part);
+  const int row0 = tm * 128, col0 = tn * 128;
+  const int kt0 = part * args.per, kts = (args.ksteps + KS - 1) / KS;
+  const int kt1 = kt0 + args.per < kts ? kt0 + args.per : kts;
+
+  // Rows past the operand's last lie at or beyond the descriptor's end and read zero.
+  const int64_t rba = (int64_t)args.blocks * (4 * FA), rbb = (int64_t)args.blocks * (4 * FB);
+  const int lda = (int)rba, ldb = (int)rbb;
+  const __amdgpu_buffer_rsrc_t ra = make_rsrc(args.a + row0 * rba, (uint64_t)(args.m - row0) * rba);
+  const __amdgpu_buffer_rsrc_t rb = make_rsrc(args.b + col0 * rbb, (uint64_t)(args.n - col0) * rbb);
+  const int sbytes = args.blocks * kMxScaleRows;  // of 64 rows
+  const bool for_a = wave < 2;                    // whose scales this wave loads
+  const int sblock = (for_a ? row0 : col0) / 64 + (wave & 1);
+  const int sblocks = ((for_a ? args.m : args.n) + 63) / 64;
+  const __amdgpu_buffer_rsrc_t rs =
+      make_rsrc((for_a ? args.as : args.bs) + (int64_t)sblock * sbytes, sblock < sblocks ? (uint64_t)sbytes : 0);
+
+  // This lane's source in a load instruction of 1 KiB: instruction i fills LDS rows 8i .. 8i + 7 (128-byte rows) or
+  // 16i .. 16i + 15; the row splits into a part of the lane and one of the instruction.
+  auto lane_src = [&](int rowbytes, int ld, int f, unsigned& off, int& kbyte) SPT_INLINE {
+    const int row = rowbytes == 128 ? 4 * (lane >> 3) : 4 * (lane >> 2);
+    const int chunk = rowbytes == 128 ? (lane & 7) ^ (lane >> 3) : (lane & 3) ^ ((lane >> 3) & 3);
+    kbyte = chunk * 16;
+    off = (unsigned)(row * ld) + (unsigned)kbyte;
+  };
+  auto instr_row = [&](int rowbytes, int i) SPT_INLINE {
+    return rowbytes == 128 ? 64 * (i >> 3) + 32 * (i & 1) + ((i & 7) >> 1) : 64 * (i >> 2) + (i & 3);
+  };
+  unsigned a_off, b_off;
+  int a_kb, b_kb;
+  lane_src(RA, lda, FA, a_off, a_kb);
+  lane_src(RB, ldb, FB, b_off, b_kb);
+
+  auto issue = [&](int kt, int slot) SPT_INLINE {
+    const bool real = kt < kt1;
+    const unsigned base = smem_base + (unsigned)(slot * STAGE);
+    const int ka = kt * (KS * 16 * FA), kb = kt * (KS * 16 * FB);  // a k-step is 16 F bytes of a row
+    // with 256 values a K-tile the row's end may lie inside
+    const unsigned va = real && (KS == 1 || ka + a_kb < lda) ? a_off : kOOB;
+    const unsigned vb = real && (KS == 1 || kb + b_kb < ldb) ? b_off : kOOB;
+#pragma unroll
+    for (int j = 0; j < LA; ++j) {
+      const int i = LA * wave + j;
+      dma16_unseen(ra, base + i * 1024, va == kOOB ? kOOB : va + (unsigned)(instr_row(RA, i) * lda), (unsigned)ka);
+    }
+#pragma unroll
+    for (int j = 0; j < LB; ++j) {
+      const int i = LB * wave + j;
+      dma16_unseen(rb, base + A_BYTES + i * 1024, vb == kOOB ? kOOB : vb + (unsigned)(instr_row(RB, i) * ldb), (unsigned)kb);
+    }
+    // 64 rows by 4 KS blocks lie together: 256 KS bytes by a quarter or half of the lanes
+    if (lane < 16 * KS) {
+      const int at = kt * (KS * 256) + lane * 16;
+      dma16_unseen(rs, base + A_BYTES + B_BYTES + wave * SC, real && at < sbytes ? (unsigned)at : kOOB, 0);
+    }
+  };
+
+  f32x4 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  // Chunk `c` of fragment f's row, operand rows at `p`.
+  auto chunk = [&](const char* p, int rowbytes, int f, int c) SPT_INLINE {
+    const int row = 16 * f + r16;
+    const int at = rowbytes == 128 ? row * 128 + ((c ^ (r16 & 7)) << 4) : row * 64 + ((c ^ ((r16 >> 1) & 3)) << 4);
+    return *(const u32x4*)(p + at);
+  };
+  auto compute = [&](int slot) SPT_INLINE {
+    const char* st = smem + opaque_s32(slot * STAGE);
+    const char* pa = st + wm * 64 * RA;
+    const char* pb = st + A_BYTES + wn * 64 * RB;
+    const char* sa = st + A_BYTES + B_BYTES + wm * SC;
+    const char* sb = st + A_BYTES + B_BYTES + (2 + wn) * SC;
+    static_for<KS>([&](auto s_c) SPT_INLINE {
+      constexpr int s = decltype(s_c)::value;
+      const unsigned wa = *(const unsigned*)(sa + (4 * s + q4) * 64 + 4 * r16);
+      const unsigned wb = *(const unsigned*)(sb + (4 * s + q4) * 64 + 4 * r16);
+      i32x8 x[4], y[4];
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        if constexpr (FA == 8) x[f] = mx_operand<8>(chunk(pa, RA, f, EXACT ? 2 * q4 : q4), chunk(pa, RA, f, EXACT ? 2 * q4 + 1 : 4 + q4));
+        else x[f] = mx_operand<4>(chunk(pa, RA, f, 4 * s + q4), u32x4{});
+        if constexpr (FB == 8) y[f] = mx_operand<8>(chunk(pb, RB, f, EXACT ? 2 * q4 : q4), chunk(pb, RB, f, EXACT ? 2 * q4 + 1 : 4 + q4));
+        else y[f] = mx_operand<4>(chunk(pb, RB, f, 4 * s + q4), u32x4{});
+      }
+      if constexpr (EXACT) {
+        static_for<4>([&](auto p_c) SPT_INLINE {
+          constexpr int p = decltype(p_c)::value;
+          u32x4 xb[4], yb[4];
+          static_for<4>([&](auto f_c) SPT_INLINE {
+            constexpr int f = decltype(f_c)::value;
+            xb[f] = mx_bf16<FA, p>(x[f], (wa >> (8 * f)) & 255u);
+            yb[f] = mx_bf16<FB, p>(y[f], (wb >> (8 * f)) & 255u);
+          });
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<__bf16>(xb[i], yb[j], acc[i][j]);
+        });
+      } else {
+        static_for<16>([&](auto m_c) SPT_INLINE {
+          constexpr int i = decltype(m_c)::value / 4, j = decltype(m_c)::value % 4;
+          acc[i][j] = mfma_mx<FA, FB, i, j>(x[i], y[j], acc[i][j], wa, wb);
+        });
+      }
+    });
+  };
+
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) issue(kt0 + i, i);
+  int slot = 0;
+  for (int kt = kt0; kt < kt1; ++kt) {
+    wait_vmcnt<LW * (S - 2)>();  // this wave's share of K-tile kt has landed
+    barrier_sync();              // everyone's has, and everyone has read K-tile kt - 1
+    issue(kt + S - 1, slot == 0 ? S - 1 : slot - 1);
+    compute(slot);
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+  wait_vmcnt<0>();
+
+  // A lane holds columns 4 r16 .. +3 of rows 16 q4 + 4e + f.
+  const int es = args.out_dtype == 2 ? 4 : 2;
+  char* out = args.c + part * args.plane * 4;
+  const __amdgpu_buffer_rsrc_t rc = make_rsrc(out + (row0 * args.ldc + col0) * es, ~0ull);
+  const int col = 64 * wn + 4 * r16;
+  const bool whole = col0 + col + 4 <= args.n;
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int row = 64 * wm + 16 * q4 + 4 * e + f;
+      if (row0 + row >= args.m) continue;
+      const unsigned off = (unsigned)(row * (int)args.ldc + col) * (unsigned)es;
+      float v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = acc[f][j][e];
+      if (args.out_dtype == 2) {
+        if (whole) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), rc, off, 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col0 + col + j < args.n) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v[j]), rc, off + 4 * j, 0, 0);
+        }
+      } else {
+        u32x2 p;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) p[j] = args.out_dtype == 1 ? pack_bf16(v[2 * j], v[2 * j + 1]) : pack_f16(v[2 * j], v[2 * j + 1]);
+        if (whole) {
+          __builtin_amdgcn_raw_buffer_store_b64(p, rc, off, 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (col0 + col + j < args.n)
+              __builtin_amdgcn_raw_buffer_store_b16((unsigned short)(p[j >> 1] >> (16 * (j & 1))), rc, off + 2 * j, 0, 0);
+        }
+      }
+    }
+}
+
+MxEntry mx_tile_entry(int fa, int fb, bool exact) {
+  MxEntry e{nullptr, 128, 128, 256, 1, 1};
+  if (fa == 4) {
+    e.fn = (const void*)&mx_tile_kernel<4, 4, false, 4>;
+    e.ksteps = 2;
+  } else if (fb == 4) {
+    e.fn = exact ? (const void*)&mx_tile_kernel<8, 4, true, 4> : (const void*)&mx_tile_kernel<8, 4, false, 4>;
+  } else {
+    e.fn = exact ? (const void*)&mx_tile_kernel<8, 8, true, 4> : (const void*)&mx_tile_kernel<8, 8, false, 4>;
+  }
+  return e;
+}
+
+}  // namespace spt
