@@ -23,9 +23,10 @@ COMMON = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
           "-I" + INCLUDE, "-I" + CSRC]
 # per-source extra flags
 _VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-EXTRA = {"spt_probe.hip": _VGPR_FORM, "spt_mx_gemm.hip": _VGPR_FORM}
+EXTRA = {"spt_probe.hip": _VGPR_FORM, "spt_mx_gemm.hip": _VGPR_FORM, "spt_mx_skinny.hip": _VGPR_FORM,
+         "spt_mx_pp.hip": _VGPR_FORM}
 SOURCES = ["spt_gemm.hip", "spt_gemm_pp.hip", "spt_gemm_reg.hip", "spt_splitk_stage.hip", "spt_probe.hip", "spt_grouped.hip", "spt_grouped_pp.hip",
-           "spt_route.hip", "spt_w4.hip", "spt_mx.hip", "spt_mx_gemm.hip", "spt_norm.hip", "spt_api.cpp", "spt_experts_api.cpp", "spt_mx_api.cpp"]
+           "spt_route.hip", "spt_w4.hip", "spt_mx.hip", "spt_mx_gemm.hip", "spt_mx_pp.hip", "spt_mx_skinny.hip", "spt_norm.hip", "spt_api.cpp", "spt_experts_api.cpp", "spt_mx_api.cpp"]
 
 
 def _compile(src: str, verbose: bool) -> str:

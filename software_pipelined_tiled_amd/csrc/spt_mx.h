@@ -23,7 +23,6 @@ struct MxQuantArgs {
   int64_t rows, ldx;
   int k, blocks;        // blocks of a row
   int64_t units;        // 64 rows by 512 columns
-  int vec;              // rows of whole 16-byte pieces
 };
 struct MxValuesArgs {
   const unsigned char* codes;
@@ -32,7 +31,6 @@ struct MxValuesArgs {
   int64_t rows, ldo;
   int k, blocks;
   int64_t units;
-  int vec;
 };
 struct MxPackArgs {
   const unsigned char* codes;
@@ -76,7 +74,6 @@ struct NormArgs {
   int n, blocks, wtype;
   float eps;
   int64_t per;          // rows of a workgroup
-  int vec;              // bits: x, r, h, y in rows of whole 16-byte pieces; weight so
 };
 struct NormGradArgs {
   const char* dy;
@@ -89,7 +86,6 @@ struct NormGradArgs {
   int n, wtype;
   float eps;
   int64_t per;
-  int vec;              // bits: dy, h, dh, dx; weight
 };
 struct NormPartsArgs {
   const float* parts;
@@ -100,7 +96,9 @@ struct NormPartsArgs {
 const void* mx_quantize_fn(int dtype, int bits);
 const void* mx_values_fn(int dtype, int bits);
 const void* mx_pack_fn();
-// out: 0 the input's type, else bits; c: 16-byte pieces a thread keeps in registers (1, 2, 4), 0: any length
+constexpr int kNormThreads = 512;
+// out: 0 the input's type, else bits; c: pieces of eight values a thread keeps in registers (1, 2, 4, and 8 without
+// gradients), 0: rows of any length
 const void* norm_fn(int dtype, int out, int c);
 const void* norm_grad_fn(int dtype, int c);
 const void* norm_parts_fn();
@@ -111,5 +109,9 @@ struct MxEntry {
 };
 // fa, fb: bits; exact: products through bf16
 MxEntry mx_tile_entry(int fa, int fb, bool exact);
+// out: 0 f16, 1 bf16, 2 f32
+MxEntry mx_pp_entry(int fa, int fb, int out);
+// mt, nf: blocks of 16 rows and of 16 columns of a workgroup (1, 2, 4)
+MxEntry mx_skinny_entry(int fa, int fb, bool exact, int mt, int nf);
 
 }  // namespace spt

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(MxQuantArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = base + 4 * j;
-        load8<T>(a.x + ((row0 + i) * a.ldx + col) * kTypeSize[T], i < rows ? a.k - col : 0, a.vec, v[j]);
+        load8<T>(a.x + ((row0 + i) * a.ldx + col) * kTypeSize[T], i < rows ? a.k - col : 0, v[j]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(256) mx_values_kernel(MxValuesArgs a) {
         else q[0] = *(const unsigned*)p;
         float v[8];
         mx_values<BITS>(q, sc[(lane >> 2) * kMxScaleRows + i], v);
-        put8<T>(a.out + ((row0 + i) * a.ldo + col) * kTypeSize[T], a.k - col, a.vec, v);
+        put8<T>(a.out + ((row0 + i) * a.ldo + col) * kTypeSize[T], a.k - col, v);
       }
     }
     __syncthreads();

@@ -17,7 +17,6 @@ constexpr int64_t kMaxLdc = (int64_t)1 << 20;
 constexpr int64_t kMaxTiles = (int64_t)1 << 24;       // of 64 x 64
 
 bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }
-bool whole16(const void* p, int64_t ld, gemm_dtype_t dtype) { return on16(p) && ld * (dtype == GEMM_F32 ? 4 : 2) % 16 == 0; }
 
 gemm_status_t check_mx(int64_t rows, int64_t k, int bits) {
   if (rows < 0 || k < 0 || (bits != 4 && bits != 8)) return GEMM_ERR_INVALID;
@@ -40,7 +39,7 @@ Units mx_units(int64_t rows, int64_t blocks) {
 // ---------------------------------------------------------------------------------- products
 struct MxShape {
   MxEntry entry;
-  bool exact;
+  bool exact, pp;  // pp: the two-group kernel, which walks over its tiles
   int64_t tiles_m, tiles_n, ktiles, splits, per, ws;
 };
 
@@ -52,21 +51,37 @@ gemm_status_t mx_shape(const gemm_mx_t* p, MxShape* s) {
   if ((p->a_bits == 4 && p->b_bits == 8) || p->ldc >= kMaxLdc) return GEMM_ERR_UNSUPPORTED;
   const int64_t small = ceil_div(p->m, 64) * ceil_div(p->n, 64);
   if (small > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
+  s->pp = false;
   s->exact = p->out_dtype == GEMM_F32 && p->a_bits == 8;
-  s->entry = mx_tile_entry(p->a_bits, p->b_bits, s->exact);
+  const int64_t ksteps = mx_blocks(p->k) / 4;
+  int64_t shortest;  // k-steps that a part of a sum has at least, in K-tiles
+  if (p->m <= 64) {
+    const int mt = p->m <= 16 ? 1 : p->m <= 32 ? 2 : 4;
+    const int nf = p->n >= 64 * kCus ? 4 : p->n >= 32 * kCus ? 2 : 1;
+    s->entry = mx_skinny_entry(p->a_bits, p->b_bits, s->exact, mt, nf);
+    shortest = 16;
+  } else if (!s->exact && ceil_div(p->m, 256) * ceil_div(p->n, 256) >= kCus / 2) {
+    s->pp = true;
+    shortest = 8;
+  } else {
+    s->entry = mx_tile_entry(p->a_bits, p->b_bits, s->exact);
+    shortest = 4;
+  }
+  if (s->pp) s->entry = mx_pp_entry(p->a_bits, p->b_bits, (int)p->out_dtype);
   s->tiles_m = ceil_div(p->m, s->entry.bm);
   s->tiles_n = ceil_div(p->n, s->entry.bn);
-  s->ktiles = ceil_div(mx_blocks(p->k) / 4, s->entry.ksteps);
+  s->ktiles = ceil_div(ksteps, s->entry.ksteps);
   const int64_t tiles = s->tiles_m * s->tiles_n;
   s->splits = 1;
   if (tiles > 0 && tiles < kCus) {
-    const int64_t fit = kCus / tiles, most = s->ktiles / 4;
+    const int64_t fit = kCus / tiles, most = s->ktiles / shortest;
     s->splits = fit < most ? fit : most;
     if (s->splits < 1) s->splits = 1;
   }
   s->per = ceil_div(s->ktiles, s->splits);
   s->splits = s->per > 0 ? ceil_div(s->ktiles, s->per) : 1;
   s->ws = s->splits > 1 ? s->splits * p->m * p->n * 4 : 0;
+  if (s->pp && s->splits > 1) s->entry = mx_pp_entry(p->a_bits, p->b_bits, (int)GEMM_F32);
   return GEMM_OK;
 }
 
@@ -76,11 +91,12 @@ struct NormShape {
   int c, threads;
   int64_t per, grid;
 };
-NormShape norm_shape(int64_t rows, int64_t n, int per_cu) {
+NormShape norm_shape(int64_t rows, int64_t n, int most, int per_cu) {
   NormShape s;
   const int64_t pieces = ceil_div(n, 8);
-  s.c = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : pieces <= 4096 ? 4 : 0;
-  s.threads = s.c ? (int)round_up(ceil_div(pieces, s.c), 64) : 1024;
+  s.c = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 4;
+  if (pieces > s.c * kNormThreads) s.c = most == 8 && pieces <= 8 * kNormThreads ? 8 : 0;
+  s.threads = s.c ? (int)round_up(ceil_div(pieces, s.c), 64) : kNormThreads;
   const int64_t fit = (int64_t)kCus * per_cu;
   s.per = ceil_div(rows, fit);
   s.grid = s.per > 0 ? ceil_div(rows, s.per) : 0;
@@ -117,9 +133,7 @@ gemm_status_t run_norm(const norm_rms_t* p, int out, const void* x, const void* 
   a.blocks = (int)mx_blocks(p->n);
   a.wtype = (int)p->weight_dtype;
   a.eps = p->eps;
-  a.vec = (whole16(x, p->ldx, p->dtype) ? 1 : 0) | (whole16(residual, p->ldr, p->dtype) ? 2 : 0) |
-          (whole16(h, p->ldh, p->dtype) ? 4 : 0) | (whole16(y, p->ldy, p->dtype) ? 8 : 0) | (on16(weight) ? 16 : 0);
-  const NormShape s = norm_shape(p->rows, out ? mx_blocks(p->n) * kMxBlock : p->n, 8);
+  const NormShape s = norm_shape(p->rows, out ? mx_blocks(p->n) * kMxBlock : p->n, 8, 8);
   a.per = s.per;
   return launch(norm_fn((int)p->dtype, out, s.c), dim3((unsigned)s.grid), s.threads, 0, &a, stream);
 }
@@ -130,7 +144,7 @@ gemm_status_t check_grad(const norm_rms_grad_t* p) {
   f.rows = p->rows; f.n = p->n; f.dtype = p->dtype; f.weight_dtype = p->weight_dtype; f.eps = p->eps;
   return check_norm(&f);
 }
-NormShape grad_shape(const norm_rms_grad_t* p) { return norm_shape(p->rows, p->n, 4); }
+NormShape grad_shape(const norm_rms_grad_t* p) { return norm_shape(p->rows, p->n, 4, 4); }
 
 }  // namespace
 
@@ -164,7 +178,6 @@ gemm_status_t mx_quantize(const void* x, gemm_dtype_t dtype, int64_t rows, int64
   a.blocks = (int)mx_blocks(k);
   const Units u = mx_units(rows, a.blocks);
   a.units = u.units;
-  a.vec = whole16(x, ldx, dtype);
   return launch(mx_quantize_fn((int)dtype, bits), dim3(u.grid), 256, 0, &a, stream);
 }
 
@@ -187,7 +200,6 @@ gemm_status_t mx_dequantize(const void* codes, const void* scales, int bits, int
   a.blocks = (int)mx_blocks(k);
   const Units u = mx_units(rows, a.blocks);
   a.units = u.units;
-  a.vec = whole16(out, ldo, dtype);
   return launch(mx_values_fn((int)dtype, bits), dim3(u.grid), 256, 0, &a, stream);
 }
 
@@ -254,7 +266,8 @@ gemm_status_t gemm_mx_run(const gemm_mx_t* p, const void* a_codes, const void* a
   a.per = (int)s.per;
   a.plane = s.splits > 1 ? p->m * p->n : 0;
   a.units = (int)(s.tiles_m * s.tiles_n * s.splits);
-  a.grid = a.units;
+  a.grid = s.pp && a.units > cu ? cu : a.units;
+  a.nt = s.splits == 1;
   st = launch(s.entry.fn, dim3((unsigned)a.grid), s.entry.threads, 0, &a, stream);
   if (st != GEMM_OK || s.splits == 1) return st;
   return add_planes((const float*)workspace, C, nullptr, 0, p->ldc, p->m, p->n, s.splits, (int)p->out_dtype, stream);
@@ -304,8 +317,6 @@ gemm_status_t norm_rms_grad_run(const norm_rms_grad_t* p, const void* dy, const 
     a.wtype = (int)p->weight_dtype;
     a.eps = p->eps;
     a.per = s.per;
-    a.vec = (whole16(dy, p->lddy, p->dtype) ? 1 : 0) | (whole16(h, p->ldh, p->dtype) ? 2 : 0) |
-            (whole16(dh, p->lddh, p->dtype) ? 4 : 0) | (whole16(dx, p->lddx, p->dtype) ? 8 : 0) | (on16(weight) ? 16 : 0);
     st = launch(norm_grad_fn((int)p->dtype, s.c), dim3((unsigned)s.grid), s.threads, 0, &a, stream);
     if (st != GEMM_OK || !dweight) return st;
   }

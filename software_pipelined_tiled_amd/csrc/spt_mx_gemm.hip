@@ -117,13 +117,14 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
       constexpr int s = decltype(s_c)::value;
       const unsigned wa = *(const unsigned*)(sa + (4 * s + q4) * 64 + 4 * r16);
       const unsigned wb = *(const unsigned*)(sb + (4 * s + q4) * 64 + 4 * r16);
-      i32x8 x[4], y[4];
+      constexpr int CA = FA / 4, CB = FB / 4;  // chunks of a lane
+      u32x4 x[4][CA], y[4][CB];
 #pragma unroll
       for (int f = 0; f < 4; ++f) {
-        if constexpr (FA == 8) x[f] = mx_operand<8>(chunk(pa, RA, f, EXACT ? 2 * q4 : q4), chunk(pa, RA, f, EXACT ? 2 * q4 + 1 : 4 + q4));
-        else x[f] = mx_operand<4>(chunk(pa, RA, f, 4 * s + q4), u32x4{});
-        if constexpr (FB == 8) y[f] = mx_operand<8>(chunk(pb, RB, f, EXACT ? 2 * q4 : q4), chunk(pb, RB, f, EXACT ? 2 * q4 + 1 : 4 + q4));
-        else y[f] = mx_operand<4>(chunk(pb, RB, f, 4 * s + q4), u32x4{});
+#pragma unroll
+        for (int h = 0; h < CA; ++h) x[f][h] = chunk(pa, RA, f, FA == 4 ? 4 * s + q4 : EXACT ? 2 * q4 + h : q4 + 4 * h);
+#pragma unroll
+        for (int h = 0; h < CB; ++h) y[f][h] = chunk(pb, RB, f, FB == 4 ? 4 * s + q4 : EXACT ? 2 * q4 + h : q4 + 4 * h);
       }
       if constexpr (EXACT) {
         static_for<4>([&](auto p_c) SPT_INLINE {
@@ -131,8 +132,8 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
           u32x4 xb[4], yb[4];
           static_for<4>([&](auto f_c) SPT_INLINE {
             constexpr int f = decltype(f_c)::value;
-            xb[f] = mx_bf16<FA, p>(x[f], (wa >> (8 * f)) & 255u);
-            yb[f] = mx_bf16<FB, p>(y[f], (wb >> (8 * f)) & 255u);
+            xb[f] = mx_bf16<FA, p>(x[f][0], x[f][CA - 1], (wa >> (8 * f)) & 255u);
+            yb[f] = mx_bf16<FB, p>(y[f][0], y[f][CB - 1], (wb >> (8 * f)) & 255u);
           });
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
       } else {
         static_for<16>([&](auto m_c) SPT_INLINE {
           constexpr int i = decltype(m_c)::value / 4, j = decltype(m_c)::value % 4;
-          acc[i][j] = mfma_mx<FA, FB, i, j>(x[i], y[j], acc[i][j], wa, wb);
+          acc[i][j] = mfma_mx<FA, FB, i, j>(mx_operand<FA>(x[i][0], x[i][CA - 1]), mx_operand<FB>(y[j][0], y[j][CB - 1]), acc[i][j], wa, wb);
         });
       }
     });

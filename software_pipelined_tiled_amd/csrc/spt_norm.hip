@@ -40,11 +40,10 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* red, int turn) {
 
 // C: pieces of eight values a thread holds of a row (0: rows of any length, in two passes). OUT: 0 y in type T, 4 or 8: MX.
 template <int T, int OUT, int C>
-__global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
   __shared__ float red[2 * 16];
   constexpr int ES = kTypeSize[T], KEEP = C ? C : 1;
   const int nt = blockDim.x, n = a.n;
-  const bool vx = a.vec & 1, vr = a.vec & 2, vh = a.vec & 4, vy = a.vec & 8, vw = a.vec & 16;
   const int pieces = OUT ? a.blocks * (kMxBlock / 8) : (n + 7) / 8;  // an MX row's padding is written too
   const int64_t first = (int64_t)blockIdx.x * a.per, last = first + a.per < a.rows ? first + a.per : a.rows;
   const float inv_n = 1.f / (float)n;
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
   float w[KEEP][8];
   auto weight = [&](int col, float (&o)[8]) SPT_INLINE {
     if (a.w) {
-      load8_any(a.w, a.wtype, col, n - col, vw, o);
+      load8_any(a.w, a.wtype, col, n - col, o);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = 1.f;
@@ -60,13 +59,13 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
   };
   // h's eight values at `col`, written where a residual is added
   auto h_at = [&](int64_t row, int col, float (&o)[8]) SPT_INLINE {
-    load8<T>(a.x + (row * a.ldx + col) * ES, n - col, vx, o);
+    load8<T>(a.x + (row * a.ldx + col) * ES, n - col, o);
     if (a.r) {
       float r[8];
-      load8<T>(a.r + (row * a.ldr + col) * ES, n - col, vr, r);
+      load8<T>(a.r + (row * a.ldr + col) * ES, n - col, r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = round_to<T>(o[e] + r[e]);
-      put8<T>(a.h + (row * a.ldh + col) * ES, n - col, vh, o);
+      put8<T>(a.h + (row * a.ldh + col) * ES, n - col, o);
     }
   };
   auto result = [&](int64_t row, int piece, const float (&h)[8], const float (&wt)[8], float rstd) SPT_INLINE {
@@ -75,7 +74,7 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = h[e] * rstd * wt[e];
     if constexpr (OUT == 0) {
-      put8<T>(a.y + (row * a.ldy + col) * ES, n - col, vy, y);
+      put8<T>(a.y + (row * a.ldy + col) * ES, n - col, y);
     } else {
       // columns behind n have to be zeros also where the row's factor is not finite
 #pragma unroll
@@ -128,9 +127,8 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
       // what this thread wrote to h, or read from x, a pass before
       const char* src = a.r ? a.h : a.x;
       const int64_t ld = a.r ? a.ldh : a.ldx;
-      const bool vs = a.r ? vh : vx;
       for (int p = threadIdx.x; p < pieces; p += nt) {
-        load8<T>(src + (row * ld + p * 8) * ES, n - p * 8, vs, h[0]);
+        load8<T>(src + (row * ld + p * 8) * ES, n - p * 8, h[0]);
         weight(p * 8, w[0]);
         result(row, p, h[0], w[0], rstd);
       }
@@ -139,18 +137,17 @@ __global__ void __launch_bounds__(1024) norm_kernel(NormArgs a) {
 }
 
 template <int T, int C>
-__global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradArgs a) {
+__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(NormGradArgs a) {
   __shared__ float red[2 * 2 * 16];
   constexpr int ES = kTypeSize[T], KEEP = C ? C : 1;
   const int nt = blockDim.x, n = a.n;
-  const bool vdy = a.vec & 1, vh = a.vec & 2, vdh = a.vec & 4, vdx = a.vec & 8, vw = a.vec & 16;
   const int64_t first = (int64_t)blockIdx.x * a.per, last = first + a.per < a.rows ? first + a.per : a.rows;
   const float inv_n = 1.f / (float)n;
   float* plane = a.parts ? a.parts + (int64_t)blockIdx.x * n : nullptr;
 
   auto weight = [&](int col, float (&o)[8]) SPT_INLINE {
     if (a.w) {
-      load8_any(a.w, a.wtype, col, n - col, vw, o);
+      load8_any(a.w, a.wtype, col, n - col, o);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[e] = 1.f;
@@ -169,14 +166,14 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradArgs a) {
   auto grad = [&](int64_t row, int col, const float (&dy)[8], const float (&h)[8], const float (&wt)[8], float rstd, float f) SPT_INLINE {
     float d[8];
     if (a.dh) {
-      load8<T>(a.dh + (row * a.lddh + col) * ES, n - col, vdh, d);
+      load8<T>(a.dh + (row * a.lddh + col) * ES, n - col, d);
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] += rstd * (dy[e] * wt[e] - h[e] * f);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] = rstd * (dy[e] * wt[e] - h[e] * f);
     }
-    put8<T>(a.dx + (row * a.lddx + col) * ES, n - col, vdx, d);
+    put8<T>(a.dx + (row * a.lddx + col) * ES, n - col, d);
   };
   int turn = 0;
   for (int64_t row = first; row < last; ++row, turn ^= 1) {
@@ -192,15 +189,15 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int col = (c * nt + (int)threadIdx.x) * 8;
-        load8<T>(a.dy + (row * a.lddy + col) * ES, n - col, vdy, dy[c]);
-        load8<T>(a.h + (row * a.ldh + col) * ES, n - col, vh, h[c]);
+        load8<T>(a.dy + (row * a.lddy + col) * ES, n - col, dy[c]);
+        load8<T>(a.h + (row * a.ldh + col) * ES, n - col, h[c]);
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) add(dy[c], h[c], w[c]);
     } else {
       for (int p = threadIdx.x; p * 8 < n; p += nt) {
-        load8<T>(a.dy + (row * a.lddy + p * 8) * ES, n - p * 8, vdy, dy[0]);
-        load8<T>(a.h + (row * a.ldh + p * 8) * ES, n - p * 8, vh, h[0]);
+        load8<T>(a.dy + (row * a.lddy + p * 8) * ES, n - p * 8, dy[0]);
+        load8<T>(a.h + (row * a.ldh + p * 8) * ES, n - p * 8, h[0]);
         weight(p * 8, w[0]);
         add(dy[0], h[0], w[0]);
       }
@@ -219,8 +216,8 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradArgs a) {
     } else {
       for (int p = threadIdx.x; p * 8 < n; p += nt) {
         const int col = p * 8;
-        load8<T>(a.dy + (row * a.lddy + col) * ES, n - col, vdy, dy[0]);
-        load8<T>(a.h + (row * a.ldh + col) * ES, n - col, vh, h[0]);
+        load8<T>(a.dy + (row * a.lddy + col) * ES, n - col, dy[0]);
+        load8<T>(a.h + (row * a.ldh + col) * ES, n - col, h[0]);
         weight(col, w[0]);
         if (a.dx) grad(row, col, dy[0], h[0], w[0], rstd, f);
         if (plane) {  // the plane's columns are this thread's alone
@@ -236,7 +233,7 @@ __global__ void __launch_bounds__(1024) norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int col = (c * nt + (int)threadIdx.x) * 8;
-        put8<2>((char*)(plane + col), n - col, n % 4 == 0, dw[c]);
+        put8<2>((char*)(plane + col), n - col, dw[c]);
       }
     }
   }
@@ -277,7 +274,7 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(NormPartsArgs a) {
 template <int T, int OUT>
 static const void* norm_pick(int c) {
   return c == 1 ? (const void*)&norm_kernel<T, OUT, 1> : c == 2 ? (const void*)&norm_kernel<T, OUT, 2>
-       : c == 4 ? (const void*)&norm_kernel<T, OUT, 4> : (const void*)&norm_kernel<T, OUT, 0>;
+       : c == 4 ? (const void*)&norm_kernel<T, OUT, 4> : c == 8 ? (const void*)&norm_kernel<T, OUT, 8> : (const void*)&norm_kernel<T, OUT, 0>;
 }
 template <int T>
 static const void* norm_pick_out(int out, int c) {

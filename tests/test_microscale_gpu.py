@@ -247,7 +247,7 @@ def reference(a, b):
 FORMATS = [(8, 8), (4, 4), (8, 4)]
 SHAPES = [(1, 1, 1), (1, 64, 128), (3, 5, 33), (2, 130, 31), (16, 16, 256), (17, 200, 300), (33, 63, 129), (64, 64, 64), (65, 127, 640),
           (127, 129, 257), (128, 128, 384), (130, 260, 1000), (256, 256, 512), (257, 511, 777), (300, 300, 100), (1, 1000, 4096),
-          (5, 70, 9000), (40, 96, 12345), (100, 33, 5000), (513, 770, 1300)]
+          (5, 70, 9000), (40, 96, 12345), (100, 33, 5000), (513, 770, 1300), (4000, 2100, 300), (2049, 4099, 700)]
 
 
 @pytest.mark.parametrize("fa,fb", FORMATS)
