@@ -91,6 +91,15 @@ __device__ __forceinline__ void dma16_unseen(__amdgpu_buffer_rsrc_t r, unsigned 
                : "memory", "m0");
 }
 
+// The same with 4 bytes a lane: 256 bytes of LDS from `lds` on.
+__device__ __forceinline__ void dma4_unseen(__amdgpu_buffer_rsrc_t r, unsigned lds, unsigned voffset, unsigned soffset) {
+  const unsigned m0 = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "s"(m0), "v"(voffset), "s"(r), "s"(soffset)
+               : "memory", "m0");
+}
+
 // The same with the non-temporal hint, for an operand whose every byte one workgroup reads once.
 __device__ __forceinline__ void dma16_unseen_stream(__amdgpu_buffer_rsrc_t r, unsigned lds, unsigned voffset,
                                                     unsigned soffset) {

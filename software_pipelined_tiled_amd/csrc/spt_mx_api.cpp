@@ -64,7 +64,7 @@ gemm_status_t mx_shape(const gemm_mx_t* p, MxShape* s) {
     s->pp = true;
     shortest = 8;
   } else {
-    s->entry = mx_tile_entry(p->a_bits, p->b_bits, s->exact);
+    s->entry = mx_tile_entry(p->a_bits, p->b_bits, s->exact, 128, 2);
     shortest = 4;
   }
   if (s->pp) s->entry = mx_pp_entry(p->a_bits, p->b_bits, (int)p->out_dtype);

@@ -22,14 +22,15 @@ namespace spt {
 template <int F, int KS>
 constexpr int mx_lds_row() { return F == 8 || KS == 2 ? 128 : 64; }
 
-template <int FA, int FB, bool EXACT, int S>
-__global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
+template <int FA, int FB, bool EXACT, int FM, int PC>
+__global__ void __launch_bounds__(256, PC) mx_tile_kernel(MxGemmArgs args) {
   constexpr int KS = FA == 4 && FB == 4 ? 2 : 1;  // k-steps of a K-tile
   constexpr int RA = mx_lds_row<FA, KS>(), RB = mx_lds_row<FB, KS>();
-  constexpr int A_BYTES = 128 * RA, B_BYTES = 128 * RB, SC = KS * 256;  // SC: scales of 64 rows
+  constexpr int BM = 32 * FM, A_BYTES = BM * RA, B_BYTES = 128 * RB, SC = KS * 256;  // SC: scales of 64 rows
   constexpr int STAGE = A_BYTES + B_BYTES + 4 * SC;
+  constexpr int FIT = 160 * 1024 / PC / STAGE, S = FIT < 8 ? FIT : 8;  // stages
   constexpr int LA = A_BYTES / 4096, LB = B_BYTES / 4096, LW = LA + LB + 1;  // loads of a wave
-  static_assert(S * STAGE <= 160 * 1024 && LW * (S - 1) < 64, "ring");
+  static_assert(S >= 2 && LW * (S - 1) < 64, "ring");
   __shared__ __attribute__((aligned(1024))) char smem[S * STAGE];
   const unsigned smem_base = lds_addr(smem);
 
@@ -39,7 +40,7 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
   const int r16 = lane & 15, q4 = lane >> 4;
   int tm, tn, part;
   unit_decode(xcd_remap(blockIdx.x, args.grid), args.tiles_m, args.tiles_n, args.group_m, tm, tn, part);
-  const int row0 = tm * 128, col0 = tn * 128;
+  const int row0 = tm * BM, col0 = tn * 128;
   const int kt0 = part * args.per, kts = (args.ksteps + KS - 1) / KS;
   const int kt1 = kt0 + args.per < kts ? kt0 + args.per : kts;
 
@@ -49,27 +50,27 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(args.a + row0 * rba, (uint64_t)(args.m - row0) * rba);
   const __amdgpu_buffer_rsrc_t rb = make_rsrc(args.b + col0 * rbb, (uint64_t)(args.n - col0) * rbb);
   const int sbytes = args.blocks * kMxScaleRows;  // of 64 rows
-  const bool for_a = wave < 2;                    // whose scales this wave loads
+  const bool for_a = wave < 2;                    // whose scales this wave loads (with one block of A wave 1's are not read)
   const int sblock = (for_a ? row0 : col0) / 64 + (wave & 1);
   const int sblocks = ((for_a ? args.m : args.n) + 63) / 64;
   const __amdgpu_buffer_rsrc_t rs =
       make_rsrc((for_a ? args.as : args.bs) + (int64_t)sblock * sbytes, sblock < sblocks ? (uint64_t)sbytes : 0);
 
   // This lane's source in a load instruction of 1 KiB: instruction i fills LDS rows 8i .. 8i + 7 (128-byte rows) or
-  // 16i .. 16i + 15; the row splits into a part of the lane and one of the instruction.
-  auto lane_src = [&](int rowbytes, int ld, int f, unsigned& off, int& kbyte) SPT_INLINE {
-    const int row = rowbytes == 128 ? 4 * (lane >> 3) : 4 * (lane >> 2);
+  // 16i .. 16i + 15; the row splits into a part of the lane and one of the instruction. fr: fragments of a wave.
+  auto lane_src = [&](int rowbytes, int ld, int fr, unsigned& off, int& kbyte) SPT_INLINE {
+    const int row = fr * (rowbytes == 128 ? lane >> 3 : lane >> 2);
     const int chunk = rowbytes == 128 ? (lane & 7) ^ (lane >> 3) : (lane & 3) ^ ((lane >> 3) & 3);
     kbyte = chunk * 16;
     off = (unsigned)(row * ld) + (unsigned)kbyte;
   };
-  auto instr_row = [&](int rowbytes, int i) SPT_INLINE {
-    return rowbytes == 128 ? 64 * (i >> 3) + 32 * (i & 1) + ((i & 7) >> 1) : 64 * (i >> 2) + (i & 3);
+  auto instr_row = [&](int rowbytes, int fr, int i) SPT_INLINE {
+    return rowbytes == 128 ? 16 * fr * (i / (2 * fr)) + 8 * fr * (i & 1) + (i >> 1) % fr : 16 * fr * (i / fr) + i % fr;
   };
   unsigned a_off, b_off;
   int a_kb, b_kb;
-  lane_src(RA, lda, FA, a_off, a_kb);
-  lane_src(RB, ldb, FB, b_off, b_kb);
+  lane_src(RA, lda, FM, a_off, a_kb);
+  lane_src(RB, ldb, 4, b_off, b_kb);
 
   auto issue = [&](int kt, int slot) SPT_INLINE {
     const bool real = kt < kt1;
@@ -81,12 +82,13 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
 #pragma unroll
     for (int j = 0; j < LA; ++j) {
       const int i = LA * wave + j;
-      dma16_unseen(ra, base + i * 1024, va == kOOB ? kOOB : va + (unsigned)(instr_row(RA, i) * lda), (unsigned)ka);
+      dma16_unseen(ra, base + i * 1024, va == kOOB ? kOOB : va + (unsigned)(instr_row(RA, FM, i) * lda), (unsigned)ka);
     }
 #pragma unroll
     for (int j = 0; j < LB; ++j) {
       const int i = LB * wave + j;
-      dma16_unseen(rb, base + A_BYTES + i * 1024, vb == kOOB ? kOOB : vb + (unsigned)(instr_row(RB, i) * ldb), (unsigned)kb);
+      if constexpr (FM < 4 && PC == 3) dma16_unseen_stream(rb, base + A_BYTES + i * 1024, vb == kOOB ? kOOB : vb + (unsigned)(instr_row(RB, 4, i) * ldb), (unsigned)kb);
+      else dma16_unseen(rb, base + A_BYTES + i * 1024, vb == kOOB ? kOOB : vb + (unsigned)(instr_row(RB, 4, i) * ldb), (unsigned)kb);
     }
     // 64 rows by 4 KS blocks lie together: 256 KS bytes by a quarter or half of the lanes
     if (lane < 16 * KS) {
@@ -95,9 +97,9 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
     }
   };
 
-  f32x4 acc[4][4];
+  f32x4 acc[FM][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
@@ -109,39 +111,41 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
   };
   auto compute = [&](int slot) SPT_INLINE {
     const char* st = smem + opaque_s32(slot * STAGE);
-    const char* pa = st + wm * 64 * RA;
+    const char* pa = st + wm * 16 * FM * RA;
     const char* pb = st + A_BYTES + wn * 64 * RB;
-    const char* sa = st + A_BYTES + B_BYTES + wm * SC;
+    const int arow = (row0 & 63) + wm * 16 * FM;
+    const char* sa = st + A_BYTES + B_BYTES + (arow >> 6) * SC + (arow & 63) + FM * r16;
     const char* sb = st + A_BYTES + B_BYTES + (2 + wn) * SC;
     static_for<KS>([&](auto s_c) SPT_INLINE {
       constexpr int s = decltype(s_c)::value;
-      const unsigned wa = *(const unsigned*)(sa + (4 * s + q4) * 64 + 4 * r16);
+      const unsigned wa = FM == 4 ? *(const unsigned*)(sa + (4 * s + q4) * 64) : FM == 2 ? *(const unsigned short*)(sa + (4 * s + q4) * 64) : *(const unsigned char*)(sa + (4 * s + q4) * 64);
       const unsigned wb = *(const unsigned*)(sb + (4 * s + q4) * 64 + 4 * r16);
       constexpr int CA = FA / 4, CB = FB / 4;  // chunks of a lane
-      u32x4 x[4][CA], y[4][CB];
+      u32x4 x[FM][CA], y[4][CB];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-#pragma unroll
-        for (int h = 0; h < CA; ++h) x[f][h] = chunk(pa, RA, f, FA == 4 ? 4 * s + q4 : EXACT ? 2 * q4 + h : q4 + 4 * h);
+      for (int f = 0; f < 4; ++f)
 #pragma unroll
         for (int h = 0; h < CB; ++h) y[f][h] = chunk(pb, RB, f, FB == 4 ? 4 * s + q4 : EXACT ? 2 * q4 + h : q4 + 4 * h);
-      }
+#pragma unroll
+      for (int f = 0; f < FM; ++f)
+#pragma unroll
+        for (int h = 0; h < CA; ++h) x[f][h] = chunk(pa, RA, f, FA == 4 ? 4 * s + q4 : EXACT ? 2 * q4 + h : q4 + 4 * h);
       if constexpr (EXACT) {
         static_for<4>([&](auto p_c) SPT_INLINE {
           constexpr int p = decltype(p_c)::value;
-          u32x4 xb[4], yb[4];
+          u32x4 xb[FM], yb[4];
           static_for<4>([&](auto f_c) SPT_INLINE {
             constexpr int f = decltype(f_c)::value;
-            xb[f] = mx_bf16<FA, p>(x[f][0], x[f][CA - 1], (wa >> (8 * f)) & 255u);
             yb[f] = mx_bf16<FB, p>(y[f][0], y[f][CB - 1], (wb >> (8 * f)) & 255u);
+            if constexpr (f < FM) xb[f] = mx_bf16<FA, p>(x[f][0], x[f][CA - 1], (wa >> (8 * f)) & 255u);
           });
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[i][j] = mfma16<__bf16>(xb[i], yb[j], acc[i][j]);
         });
       } else {
-        static_for<16>([&](auto m_c) SPT_INLINE {
+        static_for<4 * FM>([&](auto m_c) SPT_INLINE {
           constexpr int i = decltype(m_c)::value / 4, j = decltype(m_c)::value % 4;
           acc[i][j] = mfma_mx<FA, FB, i, j>(mx_operand<FA>(x[i][0], x[i][CA - 1]), mx_operand<FB>(y[j][0], y[j][CB - 1]), acc[i][j], wa, wb);
         });
@@ -161,17 +165,17 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
   }
   wait_vmcnt<0>();
 
-  // A lane holds columns 4 r16 .. +3 of rows 16 q4 + 4e + f.
+  // A lane holds columns 4 r16 .. +3 of rows FM (4 q4 + e) + f.
   const int es = args.out_dtype == 2 ? 4 : 2;
   char* out = args.c + part * args.plane * 4;
   const __amdgpu_buffer_rsrc_t rc = make_rsrc(out + (row0 * args.ldc + col0) * es, ~0ull);
   const int col = 64 * wn + 4 * r16;
   const bool whole = col0 + col + 4 <= args.n;
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
+  for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int row = 64 * wm + 16 * q4 + 4 * e + f;
+      const int row = 16 * FM * wm + FM * (4 * q4 + e) + f;
       if (row0 + row >= args.m) continue;
       const unsigned off = (unsigned)(row * (int)args.ldc + col) * (unsigned)es;
       float v[4];
@@ -201,16 +205,16 @@ __global__ void __launch_bounds__(256) mx_tile_kernel(MxGemmArgs args) {
     }
 }
 
-MxEntry mx_tile_entry(int fa, int fb, bool exact) {
-  MxEntry e{nullptr, 128, 128, 256, 1, 1};
-  if (fa == 4) {
-    e.fn = (const void*)&mx_tile_kernel<4, 4, false, 4>;
-    e.ksteps = 2;
-  } else if (fb == 4) {
-    e.fn = exact ? (const void*)&mx_tile_kernel<8, 4, true, 4> : (const void*)&mx_tile_kernel<8, 4, false, 4>;
-  } else {
-    e.fn = exact ? (const void*)&mx_tile_kernel<8, 8, true, 4> : (const void*)&mx_tile_kernel<8, 8, false, 4>;
-  }
+template <int FA, int FB, bool EXACT>
+static const void* tile_pick(int bm, int per_cu) {
+  if (per_cu == 3) return bm == 64 ? (const void*)&mx_tile_kernel<FA, FB, EXACT, 2, 3> : (const void*)&mx_tile_kernel<FA, FB, EXACT, 1, 3>;
+  return bm == 128 ? (const void*)&mx_tile_kernel<FA, FB, EXACT, 4, 2> : bm == 64 ? (const void*)&mx_tile_kernel<FA, FB, EXACT, 2, 2> : (const void*)&mx_tile_kernel<FA, FB, EXACT, 1, 2>;
+}
+MxEntry mx_tile_entry(int fa, int fb, bool exact, int bm, int per_cu) {
+  MxEntry e{nullptr, bm, 128, 256, fa == 4 ? 2 : 1, per_cu};
+  if (fa == 4) e.fn = tile_pick<4, 4, false>(bm, per_cu);
+  else if (fb == 4) e.fn = exact ? tile_pick<8, 4, true>(bm, per_cu) : tile_pick<8, 4, false>(bm, per_cu);
+  else e.fn = exact ? tile_pick<8, 8, true>(bm, per_cu) : tile_pick<8, 8, false>(bm, per_cu);
   return e;
 }
 

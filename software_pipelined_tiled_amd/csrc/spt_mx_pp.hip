@@ -3,20 +3,22 @@
 // Eight waves, two per SIMD, in two groups of four. Between workgroup barriers one group runs the matrix
 // instructions of a K-tile while the other reads its fragments from LDS and issues the direct global->LDS loads of a later
 // one. A K-tile is 128 bytes of each row: 128 values of 8 bits or 256 of 4 (128 values, 64 bytes, of a 4-bit B beside an
-// 8-bit A). Per wave and K-tile that is 32 instructions of 32 cycles or 64 of 16: 1024 cycles either way, and the
-// same 24 KiB of LDS reads (16 in the mixed form), the balance of the dense kernel.
+// 8-bit A). Per wave and K-tile that is 32 instructions of 32 cycles or 64 of 16: 1024 cycles either way, and
+// 24 KiB of LDS reads (16 in the mixed form), the balance of the dense kernel.
 //   Group 0 computes rows 0 .. 127 of the tile and group 1 rows 128 .. 255; a group's waves are 2 x 2 of 64 x 128
 // outputs, so a group reads its own half of A's tile and both halves of B's. K-tile g is read in phases 2g (group 0) and 2g + 1
 // (group 1) and computed in phases 2g + 1 and 2g + 2.
 //
 // Four rings of half tiles (128 rows, 16 KiB and up to 1 KiB of scales; 153 KiB in all, where whole tiles in five slots fill
-// the 160 KiB and leave the scales no room):
-//   group 0, phase 2g:     A low (g + 1), 2 slots; B low (g + 1), 2 slots
-//   group 1, phase 2g + 1: A high (g + 1), 2 slots; B high (g + 2), 3 slots
-// A slot is free again before its load is issued: A halves are read by their own group alone, the phase before last; B low
-// (g - 1) was last read in phase 2g - 1, B high (g - 1) as well. Each group waits for its loads at the end of its compute
-// phase, a barrier before anyone reads them: A low and B low (g + 1) at the end of phase 2g + 1, A high (g + 1) and B high (g + 2)
-// at the end of phase 2g + 2.
+// the 160 KiB and leave the scales no room). Each group loads the half of A that the other computes with, which is free a
+// phase earlier:
+//   group 0, phase 2g:     B low (g + 1), 2 slots; A high (g + 1), 2 slots
+//   group 1, phase 2g + 1: B high (g + 2), 3 slots; A low (g + 2), 2 slots
+// A slot's last reader is a barrier ahead of its load: A low (g) is read in phase 2g, A high (g) in 2g + 1, B (g) in both.
+// Waits come as late as they may, each with only younger loads still on their way and a barrier before the first reader:
+// for B low (g + 1) and the scales at the end of phase 2g + 1 (their loads go out first), for A high (g + 1) at the end of phase
+// 2g + 2, for B high and A low (g + 2) at the end of phase 2g + 3. Stores share the count, but loads return in order among
+// themselves, so a wait for all but the n youngest loads holds whatever stores lie between.
 //
 // The stream of K-tiles runs on across output tiles: a finished tile is stored in its group's next memory phase.
 // Rows are staged permuted, so that scales arrive as words and results as 8 neighbouring columns: row r of fragment f is row
@@ -34,7 +36,7 @@ __global__ void __launch_bounds__(512, 1) mx_pp_kernel(MxGemmArgs args) {
   constexpr int A_HALF = 128 * RA + 2 * SC, B_HALF = 128 * RB + 2 * SC;
   constexpr int A_LOW = 0, A_HIGH = 2 * A_HALF, B_LOW = 4 * A_HALF, B_HIGH = B_LOW + 2 * B_HALF;
   constexpr int LDS = B_HIGH + 3 * B_HALF;
-  constexpr int LA = 128 * RA / 4096, LB = 128 * RB / 4096, NL = LA + LB + 1;  // loads of a wave in a memory phase
+  constexpr int LA = 128 * RA / 4096, LB = 128 * RB / 4096, NL = LA + LB + KS;  // loads of a wave in a memory phase
   constexpr int FM = 4, FN = 8, CA = FA / 4, CB = FB / 4;                      // fragments; 16-byte chunks of a lane in a k-step
   static_assert(LDS <= 160 * 1024, "the rings fit a compute unit's LDS");
   __shared__ __attribute__((aligned(1024))) char smem[LDS];
@@ -50,40 +52,35 @@ __global__ void __launch_bounds__(512, 1) mx_pp_kernel(MxGemmArgs args) {
   const int sbytes = args.blocks * kMxScaleRows;  // of 64 rows
   const int u0 = xcd_remap(blockIdx.x, args.grid);
 
-  // One operand's stream of K-tiles, at a half tile of 128 rows: descriptors of the half's rows and of the scales that
-  // this wave loads (those of 64 rows). Wave-uniform; the tile change stays a branch.
+  // This group's stream of K-tiles: descriptors of its half of B's rows, of the other group's half of A's, and of the scales
+  // that this wave loads (those of 64 rows: waves 0 and 1 A's, 2 and 3 B's). Wave-uniform; the tile change stays a branch.
+  const int kts = (args.ksteps + KS - 1) / KS;
   struct Stream {
     int t, u, kt;
-    __amdgpu_buffer_rsrc_t r, s;
+    unsigned past;  // kOOB, past the last unit or past k in a part that is shorter than the others: moves a load out of range
+    __amdgpu_buffer_rsrc_t a, b, s;
   };
-  auto set = [&](Stream& st, auto a_c) SPT_INLINE {
-    constexpr bool kA = decltype(a_c)::value;
+  auto set = [&](Stream& st) SPT_INLINE {
     int tm = 0, tn = 0, part = 0;
     if (st.t < args.units) unit_decode(st.t, args.tiles_m, args.tiles_n, args.group_m, tm, tn, part);
-    const int rows = kA ? args.m : args.n, first = (kA ? tm : tn) * 256 + 128 * grp, left = rows - first;
-    const int ld = kA ? lda : ldb, block = first / 64 + (v & 1);
+    const int a0 = tm * 256 + 128 * (1 - grp), b0 = tn * 256 + 128 * grp;
     st.kt = part * KT;
-    st.r = make_rsrc((kA ? args.a : args.b) + (int64_t)first * ld, left > 0 ? (uint64_t)left * ld : 0);
-    st.s = make_rsrc((kA ? args.as : args.bs) + (int64_t)block * sbytes, block * 64 < rows ? (uint64_t)sbytes : 0);
+    st.a = make_rsrc(args.a + (int64_t)a0 * lda, a0 < args.m ? (uint64_t)(args.m - a0) * lda : 0);
+    st.b = make_rsrc(args.b + (int64_t)b0 * ldb, b0 < args.n ? (uint64_t)(args.n - b0) * ldb : 0);
+    const int s0 = (v < 2 ? a0 : b0) + 64 * (v & 1), rows = v < 2 ? args.m : args.n;
+    st.s = make_rsrc((v < 2 ? args.as : args.bs) + (int64_t)(s0 / 64) * sbytes, s0 < rows ? (uint64_t)sbytes : 0);
   };
-  auto begin = [&](auto a_c) SPT_INLINE {
-    Stream st;
-    st.t = u0;
-    st.u = 0;
-    set(st, a_c);
-    return st;
-  };
-  auto advance = [&](Stream& st, auto a_c) SPT_INLINE {
-    if (__builtin_expect(++st.u == KT, 0)) {
+  auto valid = [&](Stream& st) SPT_INLINE { st.past = st.t < args.units && st.kt < kts ? 0u : kOOB; };
+  auto enter = [&](Stream& st) SPT_INLINE {  // the next unit, where this one's K-tiles are done
+    if (__builtin_expect(st.u == KT, 0)) {
       st.u = 0;
       st.t += args.grid;
-      set(st, a_c);
+      set(st);
     }
   };
-  using a_ = std::true_type;
-  using b_ = std::false_type;
 
-  // This lane's source in a load of 1 KiB: LDS rows 8i .. 8i + 7 (128 bytes) or 16i .. 16i + 15 (64 bytes) of the half.
+  // This lane's source in a load of 1 KiB: LDS rows 8i .. 8i + 7 (128 bytes) or 16i .. 16i + 15 (64 bytes) of the half; the
+  // row splits into a part of the lane and one of the instruction.
   const int a_kbyte = ((lane & 7) ^ (lane >> 3)) * 16;
   const unsigned a_off = (unsigned)(4 * (lane >> 3) * lda + a_kbyte);
   const int b_kbyte = (RB == 128 ? (lane & 7) ^ (lane >> 3) : (lane & 3) ^ ((lane >> 3) & 3)) * 16;
@@ -91,43 +88,44 @@ __global__ void __launch_bounds__(512, 1) mx_pp_kernel(MxGemmArgs args) {
   auto a_row = [&](int i) SPT_INLINE { return 64 * (i >> 3) + 32 * (i & 1) + ((i & 7) >> 1); };
   auto b_row = [&](int i) SPT_INLINE { return RB == 128 ? 64 * (i & 1) + (i >> 1) : i; };
 
-  // A memory phase's loads, prepared once and issued one at a time between its reads: A's half at `a`, B's at `b` and the
-  // scales of one 64-row block of either, for the slots at LDS offsets `la` and `lb`.
+  // A memory phase's loads into the slots at LDS offsets la and lb: the scales, B's half, A's half.
+  const unsigned s_off = (unsigned)lane * 4;
   struct Loads {
-    __amdgpu_buffer_rsrc_t ra, rb, rs;
-    unsigned va, vb, vs, ka, kb, la, lb, ls;
+    unsigned va, vb, la, lb, half;
   };
-  auto prepare = [&](const Stream& a, const Stream& b, int la, int lb) SPT_INLINE {
+  auto prepare = [&](const Stream& st, int la, int lb) SPT_INLINE {
     Loads o;
-    const int kta = __builtin_amdgcn_readfirstlane(a.kt + a.u), ktb = __builtin_amdgcn_readfirstlane(b.kt + b.u);
-    o.ra = a.r;
-    o.rb = b.r;
-    o.rs = v < 2 ? a.s : b.s;
-    o.ka = (unsigned)(kta * (KS * 16 * FA));
-    o.kb = (unsigned)(ktb * (KS * 16 * FB));
-    // past the row's end (inside a K-tile of two k-steps, or a part that is shorter than the others), or past the last unit
-    o.va = a.t < args.units && (int)o.ka + a_kbyte < lda ? a_off : kOOB;
-    o.vb = b.t < args.units && (int)o.kb + b_kbyte < ldb ? b_off : kOOB;
-    const int at = (v < 2 ? kta : ktb) * SC + lane * 16;
-    o.vs = (v < 2 ? a.t : b.t) < args.units && at < sbytes ? (unsigned)at : kOOB;
-    o.la = smem_base + (unsigned)__builtin_amdgcn_readfirstlane(la);
-    o.lb = smem_base + (unsigned)__builtin_amdgcn_readfirstlane(lb);
-    o.ls = (v < 2 ? o.la + 128 * RA : o.lb + 128 * RB) + (v & 1) * SC;
+    o.va = a_off;
+    o.vb = b_off;
+    o.half = 0;
+    if constexpr (KS == 2) {  // a row may end inside the K-tile; where nothing is loaded anyway (kOOB twice would be 0 again) it does not
+      o.half = st.past == 0 && 2 * st.kt + 2 > args.ksteps ? kOOB : 0u;
+      o.va = o.half && a_kbyte >= 64 ? kOOB : o.va;
+      o.vb = o.half && b_kbyte >= 64 ? kOOB : o.vb;
+    }
+    o.la = smem_base + (unsigned)la;
+    o.lb = smem_base + (unsigned)lb;
     return o;
   };
-  auto load_one = [&](const Loads& o, auto j_c) SPT_INLINE {
+  auto load_scales = [&](const Stream& st, const Loads& o) SPT_INLINE {
+    const unsigned at = (v < 2 ? o.la + 128 * RA : o.lb + 128 * RB) + (v & 1) * SC;
+    dma4_unseen(st.s, at, s_off | st.past, (unsigned)(st.kt * SC));
+    if constexpr (KS == 2) dma4_unseen(st.s, at + 256, (s_off + 256) | st.past | o.half, (unsigned)(st.kt * SC));
+  };
+  auto load_one = [&](const Stream& st, const Loads& o, auto j_c) SPT_INLINE {
     constexpr int j = decltype(j_c)::value;
-    if constexpr (j < LA) {
-      const int i = LA * v + j;
-      dma16_unseen(o.ra, o.la + i * 1024, add_in_place(o.va, (unsigned)(a_row(i) * lda)), o.ka);
-    } else if constexpr (j < LA + LB) {
-      const int i = LB * v + j - LA;
-      dma16_unseen(o.rb, o.lb + i * 1024, add_in_place(o.vb, (unsigned)(b_row(i) * ldb)), o.kb);
+    if constexpr (j < LB) {
+      const int i = LB * v + j;
+      dma16_unseen(st.b, o.lb + i * 1024, add_in_place(o.vb, (unsigned)(b_row(i) * ldb) | st.past), (unsigned)(st.kt * (KS * 16 * FB)));
     } else {
-      if (lane < 16 * KS) dma16_unseen(o.rs, o.ls, o.vs, 0);
+      const int i = LA * v + j - LB;
+      dma16_unseen(st.a, o.la + i * 1024, add_in_place(o.va, (unsigned)(a_row(i) * lda) | st.past), (unsigned)(st.kt * (KS * 16 * FA)));
     }
   };
-  auto load_all = [&](const Loads& o) SPT_INLINE { static_for<NL>([&](auto j_c) SPT_INLINE { load_one(o, j_c); }); };
+  auto load_all = [&](const Stream& st, const Loads& o) SPT_INLINE {
+    load_scales(st, o);
+    static_for<LA + LB>([&](auto j_c) SPT_INLINE { load_one(st, o, j_c); });
+  };
 
   u32x4 x[FM][KS * CA], y[FN][KS * CB];  // the K-tile's fragments: A rows, B rows
   unsigned sx[KS];
@@ -145,7 +143,7 @@ __global__ void __launch_bounds__(512, 1) mx_pp_kernel(MxGemmArgs args) {
   };
   auto reads_at = [&](int a, int b) SPT_INLINE {
     Reads p;
-    const int ua = opaque_s32(__builtin_amdgcn_readfirstlane(a)), ub = opaque_s32(__builtin_amdgcn_readfirstlane(b));
+    const int ua = opaque_s32(a), ub = opaque_s32(b);
     p.pa = smem + ua + wm * 64 * RA;
     p.pb = smem + ub;
     p.sa = smem + ua + 128 * RA + wm * SC + q4 * 64 + 4 * r16;
@@ -169,31 +167,39 @@ __global__ void __launch_bounds__(512, 1) mx_pp_kernel(MxGemmArgs args) {
   };
   auto read_all = [&](const Reads& p) SPT_INLINE {
     static_for<NR>([&](auto i_c) SPT_INLINE { read_one(p, i_c); });
-    wait_lgkmcnt0();
   };
-  // A wave issues its loads at a limited rate: in one burst the reads would queue behind them.
-  auto read_with_loads = [&](const Reads& p, const Loads& o) SPT_INLINE {
+  // A wave issues its loads at a limited rate (1 KiB in about 56 cycles): in one burst the reads would queue behind them.
+  // Among the matrix instructions they hold those up as long (8192^3 8 x 8: 405 us).
+  auto read_with_loads = [&](const Reads& p, const Stream& st, const Loads& o) SPT_INLINE {
+    load_scales(st, o);
     static_for<NR>([&](auto i_c) SPT_INLINE {
       constexpr int i = decltype(i_c)::value;
-      static_for<NL>([&](auto l_c) SPT_INLINE {
+      static_for<LA + LB>([&](auto l_c) SPT_INLINE {
         constexpr int l = decltype(l_c)::value;
-        if constexpr (l * NR / NL == i) load_one(o, l_c);
+        if constexpr (l * NR / (LA + LB) == i) load_one(st, o, l_c);
       });
       read_one(p, i_c);
     });
-    wait_lgkmcnt0();
   };
+  // The products of the K-tile in registers, and nothing else: scalar instructions between them, a few at a time, made this phase
+  // 1013 -> 1250 cycles.
   auto compute = [&](auto first_c) SPT_INLINE {
     constexpr bool kFirst = decltype(first_c)::value;
     __builtin_amdgcn_s_setprio(1);
-    static_for<KS>([&](auto s_c) SPT_INLINE {
-      constexpr int s = decltype(s_c)::value;
-      static_for<FM * FN>([&](auto m_c) SPT_INLINE {
-        constexpr int m = decltype(m_c)::value, j = m / FM, i = ((j + s) & 1) ? FM - 1 - m % FM : m % FM;
-        acc[i][j] = mfma_mx<FA, FB, i, j % 4>(mx_operand<FA>(x[i][s * CA], x[i][s * CA + CA - 1]), mx_operand<FB>(y[j][s * CB], y[j][s * CB + CB - 1]),
-                                              (kFirst && s == 0) ? zero : acc[i][j], sx[s], sy[s][j / 4]);
-      });
+    static_for<KS * FM * FN>([&](auto m_c) SPT_INLINE {
+      constexpr int m = decltype(m_c)::value, s = m / (FM * FN), j = m % (FM * FN) / FM, i = ((j + s) & 1) ? FM - 1 - m % FM : m % FM;
+      acc[i][j] = mfma_mx<FA, FB, i, j % 4>(mx_operand<FA>(x[i][s * CA], x[i][s * CA + CA - 1]), mx_operand<FB>(y[j][s * CB], y[j][s * CB + CB - 1]),
+                                            (kFirst && s == 0) ? zero : acc[i][j], sx[s], sy[s][j / 4]);
     });
+    // The products belong here: without a use the compiler sinks them past the barrier to the sums' next use, in front of the
+    // group's own reads (8192^3 8 x 8: 455 us, 362 with it).
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        f32x4& c = acc[i][j];
+        asm volatile("" : "+v"(c));
+      }
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_setprio(0);
   };
@@ -231,85 +237,85 @@ __global__ void __launch_bounds__(512, 1) mx_pp_kernel(MxGemmArgs args) {
   int units_left = u0 < args.units ? (args.units - u0 - 1) / args.grid + 1 : 0;
   int done = -1;  // the unit whose stores are pending
   // Ring positions of K-tile g: parity for the rings of two, g mod 3 for B high.
-  auto a_slot = [&](int p) SPT_INLINE { return (grp ? A_HIGH : A_LOW) + (p & 1) * A_HALF; };
+  auto a_low = [&](int p) SPT_INLINE { return A_LOW + (p & 1) * A_HALF; };
+  auto a_high = [&](int p) SPT_INLINE { return A_HIGH + (p & 1) * A_HALF; };
   auto b_low = [&](int p) SPT_INLINE { return B_LOW + (p & 1) * B_HALF; };
   auto b_high = [&](int p3) SPT_INLINE { return B_HIGH + p3 * B_HALF; };
   auto next3 = [&](int p3) SPT_INLINE { return p3 == 2 ? 0 : p3 + 1; };
-  int p2 = 0, p3 = 0;  // of the K-tile that is read next
-
-  if (grp == 0) {
-    Stream a = begin(a_{}), b = begin(b_{});
-    load_all(prepare(a, b, a_slot(0), b_low(0)));
-    advance(a, a_{});
-    advance(b, b_{});
-    wait_vmcnt<0>();
+  Stream st;
+  st.t = u0;
+  st.u = 0;
+  set(st);
+  valid(st);
+  // What the next memory phase does: the slots of the K-tile it reads, and those of its loads.
+  int p2 = 0, p3 = 0, ra = 0, rb = 0, la = 0, lb = 0;
+  auto plan = [&]() SPT_INLINE {
+    ra = opaque_s32(grp ? a_high(p2) : a_low(p2));
+    rb = opaque_s32(wn ? b_high(p3) : b_low(p2));
+    la = opaque_s32(grp ? a_low(p2) : a_high(p2 + 1));
+    lb = opaque_s32(grp ? b_high(next3(next3(p3))) : b_low(p2 + 1));
+  };
+  // A group's memory phase and compute phase of one K-tile. A finished tile's stores go out between the loads and the reads.
+  // The next memory phase's scalar work is done while the reads are on their way.
+  auto step = [&](auto first_c, auto group0_c) SPT_INLINE {
+    const Loads o = prepare(st, la, lb);
+    const Reads r = reads_at(ra, rb);
+    const bool stores = decltype(first_c)::value && done >= 0;
+    if (stores) {
+      load_all(st, o);
+      wait_vmcnt<NL>();  // this group's loads of its last memory phase have landed
+      epilogue(done);
+      read_all(r);
+    } else {
+      read_with_loads(r, st, o);
+    }
+    ++st.u;
+    ++st.kt;
+    enter(st);
+    valid(st);
+    p2 ^= 1;
+    p3 = next3(p3);
+    plan();
+    wait_lgkmcnt0();
+    if (!stores) wait_vmcnt<NL>();
     barrier_sync();
-    auto step = [&](auto first_c) SPT_INLINE {
-      constexpr bool kFirst = decltype(first_c)::value;
-      const Loads o = prepare(a, b, a_slot(p2 + 1), b_low(p2 + 1));
-      const Reads r = reads_at(a_slot(p2), wn ? b_high(p3) : b_low(p2));
-      if (kFirst && done >= 0) {
-        load_all(o);
-        epilogue(done);
-        read_all(r);
-      } else {
-        read_with_loads(r, o);
-      }
-      barrier_sync();
-      compute(first_c);
-      wait_vmcnt<0>();
-      barrier_sync();
-      p2 ^= 1;
-      p3 = next3(p3);
-      advance(a, a_{});
-      advance(b, b_{});
-    };
+    compute(first_c);
+    if constexpr (decltype(group0_c)::value) wait_vmcnt<LA>();  // the scales and B low have landed
+    barrier_sync();
+  };
+  auto run = [&](auto group0_c) SPT_INLINE {
     for (int t = u0; units_left > 0; --units_left, t += args.grid) {
-      step(std::true_type{});
-      for (int u = 1; u < KT; ++u) step(std::false_type{});
+      step(std::true_type{}, group0_c);
+      for (int u = 1; u < KT; ++u) step(std::false_type{}, group0_c);
       done = t;
     }
-    if (done >= 0) epilogue(done);  // beside group 1's last compute phase
+    if (done >= 0) epilogue(done);  // group 0's beside group 1's last compute phase
+  };
+
+  auto first_loads = [&](int a, int b) SPT_INLINE {
+    load_all(st, prepare(st, a, b));
+    ++st.u;
+    ++st.kt;
+    enter(st);
+    valid(st);
+  };
+  if (grp == 0) {
+    first_loads(a_high(0), b_low(0));
+    wait_vmcnt<0>();
+    barrier_sync();
+    plan();
+    run(std::true_type{});
     barrier_sync();
   } else {
-    Stream a = begin(a_{}), b = begin(b_{});
-    load_all(prepare(a, b, a_slot(0), b_high(0)));
-    advance(a, a_{});
-    advance(b, b_{});
-    {  // B high (1); its A half belongs to K-tile 1 too and is loaded again in phase 1
-      load_all(prepare(a, b, a_slot(1), b_high(1)));
-      advance(b, b_{});
-    }
+    first_loads(a_low(0), b_high(0));
+    first_loads(a_low(1), b_high(1));
     wait_vmcnt<0>();
     barrier_sync();
     barrier_sync();  // phase 0
-    auto step = [&](auto first_c) SPT_INLINE {
-      constexpr bool kFirst = decltype(first_c)::value;
-      const Loads o = prepare(a, b, a_slot(p2 + 1), b_high(next3(next3(p3))));
-      const Reads r = reads_at(a_slot(p2), wn ? b_high(p3) : b_low(p2));
-      if (kFirst && done >= 0) {
-        load_all(o);
-        epilogue(done);
-        read_all(r);
-      } else {
-        read_with_loads(r, o);
-      }
-      barrier_sync();
-      compute(first_c);
-      wait_vmcnt<0>();
-      barrier_sync();
-      p2 ^= 1;
-      p3 = next3(p3);
-      advance(a, a_{});
-      advance(b, b_{});
-    };
-    for (int t = u0; units_left > 0; --units_left, t += args.grid) {
-      step(std::true_type{});
-      for (int u = 1; u < KT; ++u) step(std::false_type{});
-      done = t;
-    }
-    if (done >= 0) epilogue(done);
+    plan();
+    run(std::false_type{});
   }
+  wait_vmcnt<0>();  // no load to LDS outlives the workgroup
 }
 
 template <int FA, int FB>
