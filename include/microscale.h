@@ -68,7 +68,7 @@ gemm_status_t mx_pack(const void* codes, int64_t ldc, const void* scales, int64_
  * bf16 numbers, which all but those with scales under 2^-117 or over 2^119 are.
  *   Few output tiles with a long sum are cut over workgroups into fp32 planes in the workspace, which a second kernel
  * adds in their order: results do not change from run to run.
- * Errors: as above; GEMM_ERR_UNSUPPORTED (4 x 8; ldc of 2^20 or more; more than 2^24 tiles of 64 x 64).
+ * Errors: as above; GEMM_ERR_UNSUPPORTED (4 x 8; ldc of 2^20 or more; more than 2^24 tiles of 32 x 64).
  */
 typedef struct {
   int64_t m, n, k;

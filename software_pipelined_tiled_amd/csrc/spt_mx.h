@@ -105,13 +105,12 @@ const void* norm_parts_fn();
 
 struct MxEntry {
   const void* fn;
-  int bm, bn, threads, ksteps, per_cu;  // k-steps of a K-tile
+  int bm, bn, threads, ksteps;  // k-steps of a K-tile
 };
 // fa, fb: bits; exact: products through bf16
-MxEntry mx_tile_entry(int fa, int fb, bool exact, int bm, int per_cu);  // bm: 32, 64, 128
+MxEntry mx_tile_entry(int fa, int fb, bool exact, int bm);  // bm: 32, 64, 128
 // out: 0 f16, 1 bf16, 2 f32
 MxEntry mx_pp_entry(int fa, int fb, int out);
-// mt, nf: blocks of 16 rows and of 16 columns of a workgroup (1, 2, 4)
-MxEntry mx_skinny_entry(int fa, int fb, bool exact, int mt, int nf);
+MxEntry mx_skinny_entry(int fa, int fb, bool exact, int mt);  // mt: blocks of 16 rows (1, 2)
 
 }  // namespace spt

@@ -14,7 +14,7 @@ constexpr int64_t kMaxRows = kMax32 - 63;             // their number rounded up
 constexpr int64_t kMaxK = (int64_t)1 << 22;           // 256 rows of it stay inside a buffer's 32-bit offsets
 constexpr int64_t kMaxNorm = (int64_t)1 << 24;
 constexpr int64_t kMaxLdc = (int64_t)1 << 20;
-constexpr int64_t kMaxTiles = (int64_t)1 << 24;       // of 64 x 64
+constexpr int64_t kMaxTiles = (int64_t)1 << 24;       // of 32 x 64, the smallest tile's half
 
 bool on16(const void* p) { return (uintptr_t)p % 16 == 0; }
 
@@ -37,11 +37,81 @@ Units mx_units(int64_t rows, int64_t blocks) {
 }
 
 // ---------------------------------------------------------------------------------- products
+enum MxKernel { kSkinny16, kSkinny32, kTile32, kTile64, kTile128, kTwoGroup, kMxKernels };
+
 struct MxShape {
+  MxKernel kernel;
   MxEntry entry;
-  bool exact, pp;  // pp: the two-group kernel, which walks over its tiles
-  int64_t tiles_m, tiles_n, ktiles, splits, per, ws;
+  bool exact;
+  int64_t tiles_m, tiles_n, splits, per, ws;  // per: K-tiles of one part of a sum
 };
+
+MxEntry mx_entry(MxKernel kernel, const gemm_mx_t* p, bool exact, bool planes) {
+  const int fa = p->a_bits, fb = p->b_bits;
+  switch (kernel) {
+    case kSkinny16: return mx_skinny_entry(fa, fb, exact, 1);
+    case kSkinny32: return mx_skinny_entry(fa, fb, exact, 2);
+    case kTile32: return mx_tile_entry(fa, fb, exact, 32);
+    case kTile64: return mx_tile_entry(fa, fb, exact, 64);
+    case kTile128: return mx_tile_entry(fa, fb, exact, 128);
+    default: return mx_pp_entry(fa, fb, planes ? (int)GEMM_F32 : (int)p->out_dtype);
+  }
+}
+
+// The kernel and the parts of a sum: the least time by this model, in us. A start; the longer of the workgroups' rounds over the
+// compute units (k-steps times what one takes, and the tile's own start and end) and the bytes; and, with parts, the second pass
+// over their planes. Tiles run two to a compute unit, and a workgroup alone on its own takes its k-steps faster. The constants are
+// a fit to 3300 measured shapes (1 .. 16384 rows, N 64 .. 28672, K 100 .. 14336); on 1800 of them the choice takes 2.8 % longer
+// than the best kernel of each shape, 82 % at worst (1386 x 11469 x 650, 4 x 4 in fp32: 34 us against 18), where rules on the
+// numbers of rows and tiles took 25 %.
+void mx_choose(const gemm_mx_t* p, MxShape* s) {
+  // by format: 4 x 4, 8 x 4, 8 x 8, and the last two exact
+  struct Cost {
+    double start, solo[5], pair[5], tile[3], out;
+  };
+  static const Cost costs[kMxKernels] = {
+      {2.8, {.60, .60, 1.05, .63, 1.14}, {}, {}, .3},
+      {2.4, {.90, 1.35, 1.56, .98, 1.60}, {}, {}, .3},
+      {3.0, {.20, .235, .306, .485, .56}, {.385, .54, .59, .80, .915}, {}, .45},
+      {3.7, {.22, .34, .42, .665, .72}, {.405, .565, .65, 1.0, 1.11}, {}, .4},
+      {5.0, {.345, .50, .63, .97, 1.07}, {.50, .725, .90, 1.46, 1.70}, {}, .35},
+      {5.0, {}, {.66, .90, .98}, {3.2, 3.3, 4.8}, .24}};
+  static const int parts[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  const int f = (p->a_bits == 4 ? 0 : p->b_bits == 4 ? 1 : 2) + (s->exact ? 2 : 0);
+  const int64_t ksteps = mx_blocks(p->k) / 4;
+  const double operands = ((double)p->n * p->b_bits + (double)p->m * p->a_bits) * (double)p->k / 8e6;
+  const double plane = (double)p->m * (double)p->n * 4e-6;
+  double least = 0;
+  bool any = false;
+  for (int i = 0; i < kMxKernels; ++i) {
+    const MxKernel kernel = (MxKernel)i;
+    const bool skinny = kernel <= kSkinny32, pp = kernel == kTwoGroup;
+    // a workgroup of the skinny kernel has all rows, and as many columns as keep it the only one on its compute unit
+    if (skinny && (p->m > (kernel == kSkinny16 ? 16 : 32) || p->n > 16 * kCus)) continue;
+    if (pp && s->exact) continue;
+    const MxEntry e = mx_entry(kernel, p, s->exact, false);
+    const Cost& c = costs[i];
+    const int64_t tm = ceil_div(p->m, e.bm), tn = ceil_div(p->n, e.bn), kt = ceil_div(ksteps, e.ksteps);
+    for (int sp : parts) {
+      const int64_t units = tm * tn * sp, per = ceil_div(kt, sp);
+      if (sp > 1 && (skinny || units > 4 * kCus || kt < 2 * sp)) break;
+      if (pp && per < 2) break;
+      double work;
+      if (skinny) work = c.solo[f] * (double)ceil_div(ksteps, 8);
+      else if (pp) work = (double)ceil_div(units, kCus) * (c.pair[f] * (double)(per * e.ksteps) + c.tile[f]);
+      else work = (units <= kCus ? c.solo[f] : (double)ceil_div(units, 2 * kCus) * c.pair[f]) * (double)(per * e.ksteps);
+      const double out = sp > 1 ? plane * sp : plane * (p->out_dtype == GEMM_F32 ? 1 : .5);
+      const double bytes = .2 * operands + c.out * out;
+      const double us = c.start + (work > bytes ? work : bytes) + (sp > 1 ? 3.2 + .45 * out : 0);
+      if (any && us >= least) continue;
+      any = true;
+      least = us;
+      s->kernel = kernel;
+      s->splits = kt > 0 ? ceil_div(kt, per) : 1;
+      s->per = per;
+    }
+  }
+}
 
 gemm_status_t mx_shape(const gemm_mx_t* p, MxShape* s) {
   if (!p || !is_dtype(p->out_dtype) || p->ldc < p->n) return GEMM_ERR_INVALID;
@@ -49,39 +119,16 @@ gemm_status_t mx_shape(const gemm_mx_t* p, MxShape* s) {
   if (st == GEMM_OK) st = check_mx(p->n, p->k, p->b_bits);
   if (st != GEMM_OK) return st;
   if ((p->a_bits == 4 && p->b_bits == 8) || p->ldc >= kMaxLdc) return GEMM_ERR_UNSUPPORTED;
-  const int64_t small = ceil_div(p->m, 64) * ceil_div(p->n, 64);
-  if (small > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
-  s->pp = false;
+  if (ceil_div(p->m, 32) * ceil_div(p->n, 64) > kMaxTiles) return GEMM_ERR_UNSUPPORTED;
   s->exact = p->out_dtype == GEMM_F32 && p->a_bits == 8;
-  const int64_t ksteps = mx_blocks(p->k) / 4;
-  int64_t shortest;  // k-steps that a part of a sum has at least, in K-tiles
-  if (p->m <= 64) {
-    const int mt = p->m <= 16 ? 1 : p->m <= 32 ? 2 : 4;
-    const int nf = p->n >= 64 * kCus ? 4 : p->n >= 32 * kCus ? 2 : 1;
-    s->entry = mx_skinny_entry(p->a_bits, p->b_bits, s->exact, mt, nf);
-    shortest = 16;
-  } else if (!s->exact && ceil_div(p->m, 256) * ceil_div(p->n, 256) >= kCus / 2) {
-    s->pp = true;
-    shortest = 8;
-  } else {
-    s->entry = mx_tile_entry(p->a_bits, p->b_bits, s->exact, 128, 2);
-    shortest = 4;
-  }
-  if (s->pp) s->entry = mx_pp_entry(p->a_bits, p->b_bits, (int)p->out_dtype);
+  s->kernel = kTile32;
+  s->splits = 1;
+  s->per = 0;
+  mx_choose(p, s);
+  s->entry = mx_entry(s->kernel, p, s->exact, s->splits > 1);
   s->tiles_m = ceil_div(p->m, s->entry.bm);
   s->tiles_n = ceil_div(p->n, s->entry.bn);
-  s->ktiles = ceil_div(ksteps, s->entry.ksteps);
-  const int64_t tiles = s->tiles_m * s->tiles_n;
-  s->splits = 1;
-  if (tiles > 0 && tiles < kCus) {
-    const int64_t fit = kCus / tiles, most = s->ktiles / shortest;
-    s->splits = fit < most ? fit : most;
-    if (s->splits < 1) s->splits = 1;
-  }
-  s->per = ceil_div(s->ktiles, s->splits);
-  s->splits = s->per > 0 ? ceil_div(s->ktiles, s->per) : 1;
   s->ws = s->splits > 1 ? s->splits * p->m * p->n * 4 : 0;
-  if (s->pp && s->splits > 1) s->entry = mx_pp_entry(p->a_bits, p->b_bits, (int)GEMM_F32);
   return GEMM_OK;
 }
 
@@ -266,8 +313,9 @@ gemm_status_t gemm_mx_run(const gemm_mx_t* p, const void* a_codes, const void* a
   a.per = (int)s.per;
   a.plane = s.splits > 1 ? p->m * p->n : 0;
   a.units = (int)(s.tiles_m * s.tiles_n * s.splits);
-  a.grid = s.pp && a.units > cu ? cu : a.units;
-  a.nt = s.splits == 1;
+  a.grid = s.kernel == kTwoGroup && a.units > cu ? cu : a.units;  // it walks over its tiles
+  // 16-bit stores write whole lines, and past the caches they are taken faster; fp32 ones are not (2236 x 24448 x 448: 115 us, 61)
+  a.nt = s.splits == 1 && p->out_dtype != GEMM_F32;
   st = launch(s.entry.fn, dim3((unsigned)a.grid), s.entry.threads, 0, &a, stream);
   if (st != GEMM_OK || s.splits == 1) return st;
   return add_planes((const float*)workspace, C, nullptr, 0, p->ldc, p->m, p->n, s.splits, (int)p->out_dtype, stream);

@@ -1,13 +1,14 @@
-// Products of microscaled operands in 128 x 128 tiles: C = A . B^T through a ring of LDS stages.
+// Products of microscaled operands in tiles of 32, 64 or 128 rows by 128 columns: C = A . B^T through a ring of LDS stages.
 //
-// Four waves, 2 x 2, of 64 x 64 outputs each: 4 x 4 blocks of v_mfma_scale_f32_16x16x128_f8f6f4. A K-tile is 128 values
-// of k, 256 where both operands have 4 bits, so that its rows are 128 bytes of each operand (64 of a 4-bit one
-// beside an 8-bit one). The layout in LDS is the dense kernels': rows of eight (four) 16-byte chunks, chunk c of row r at
-// c XOR (r mod 8) (at c XOR ((r / 2) mod 4) in 64-byte rows), which the direct global->LDS loads make by choosing
-// each lane's source.
+// Four waves, 2 x 2, of 16 FM x 64 outputs each (FM = 1, 2, 4): FM x 4 blocks of v_mfma_scale_f32_16x16x128_f8f6f4. A K-tile is
+// 128 values of k, 256 where both operands have 4 bits, so that its rows are 128 bytes of each operand (64 of a 4-bit
+// one beside an 8-bit one). The layout in LDS is the dense kernels': rows of eight (four) 16-byte chunks, chunk c of row r
+// at c XOR (r mod 8) (at c XOR ((r / 2) mod 4) in 64-byte rows), which the direct global->LDS loads make by choosing each lane's
+// source. Two workgroups to a compute unit with half of its LDS each, so that one's products hide the other's reads and
+// waits (1024 x 8192^2 8 x 8: 75 us, 91 with one and twice the stages; 51 x 9280 x 1152 8 x 4, 32 rows: 6 us against 8).
 //
-// Rows are staged permuted: row r of fragment f is operand row 4r + f of the wave's 64. A lane's four fragments are
-// then four neighbouring rows, whose scales of one block are one aligned word in memory (hence scales in blocks of
+// Rows are staged permuted: row r of fragment f is row 4r + f of the wave's 64 B rows (FM r + f of its A rows). A lane's fragments
+// are then neighbouring rows, whose scales of one block are one aligned word in memory (hence scales in blocks of
 // 64 rows); the instruction's operand select picks the fragment's byte, so no instruction unpacks scales. And a
 // lane's results are four neighbouring columns, a quarter-wave's 128 bytes or more of a row.
 //
@@ -22,13 +23,13 @@ namespace spt {
 template <int F, int KS>
 constexpr int mx_lds_row() { return F == 8 || KS == 2 ? 128 : 64; }
 
-template <int FA, int FB, bool EXACT, int FM, int PC>
-__global__ void __launch_bounds__(256, PC) mx_tile_kernel(MxGemmArgs args) {
+template <int FA, int FB, bool EXACT, int FM>
+__global__ void __launch_bounds__(256, 2) mx_tile_kernel(MxGemmArgs args) {
   constexpr int KS = FA == 4 && FB == 4 ? 2 : 1;  // k-steps of a K-tile
   constexpr int RA = mx_lds_row<FA, KS>(), RB = mx_lds_row<FB, KS>();
   constexpr int BM = 32 * FM, A_BYTES = BM * RA, B_BYTES = 128 * RB, SC = KS * 256;  // SC: scales of 64 rows
   constexpr int STAGE = A_BYTES + B_BYTES + 4 * SC;
-  constexpr int FIT = 160 * 1024 / PC / STAGE, S = FIT < 8 ? FIT : 8;  // stages
+  constexpr int S = 80 * 1024 / STAGE;  // stages: two workgroups share a compute unit's LDS
   constexpr int LA = A_BYTES / 4096, LB = B_BYTES / 4096, LW = LA + LB + 1;  // loads of a wave
   static_assert(S >= 2 && LW * (S - 1) < 64, "ring");
   __shared__ __attribute__((aligned(1024))) char smem[S * STAGE];
@@ -87,8 +88,7 @@ __global__ void __launch_bounds__(256, PC) mx_tile_kernel(MxGemmArgs args) {
 #pragma unroll
     for (int j = 0; j < LB; ++j) {
       const int i = LB * wave + j;
-      if constexpr (FM < 4 && PC == 3) dma16_unseen_stream(rb, base + A_BYTES + i * 1024, vb == kOOB ? kOOB : vb + (unsigned)(instr_row(RB, 4, i) * ldb), (unsigned)kb);
-      else dma16_unseen(rb, base + A_BYTES + i * 1024, vb == kOOB ? kOOB : vb + (unsigned)(instr_row(RB, 4, i) * ldb), (unsigned)kb);
+      dma16_unseen(rb, base + A_BYTES + i * 1024, vb == kOOB ? kOOB : vb + (unsigned)(instr_row(RB, 4, i) * ldb), (unsigned)kb);
     }
     // 64 rows by 4 KS blocks lie together: 256 KS bytes by a quarter or half of the lanes
     if (lane < 16 * KS) {
@@ -206,15 +206,14 @@ __global__ void __launch_bounds__(256, PC) mx_tile_kernel(MxGemmArgs args) {
 }
 
 template <int FA, int FB, bool EXACT>
-static const void* tile_pick(int bm, int per_cu) {
-  if (per_cu == 3) return bm == 64 ? (const void*)&mx_tile_kernel<FA, FB, EXACT, 2, 3> : (const void*)&mx_tile_kernel<FA, FB, EXACT, 1, 3>;
-  return bm == 128 ? (const void*)&mx_tile_kernel<FA, FB, EXACT, 4, 2> : bm == 64 ? (const void*)&mx_tile_kernel<FA, FB, EXACT, 2, 2> : (const void*)&mx_tile_kernel<FA, FB, EXACT, 1, 2>;
+static const void* tile_pick(int bm) {
+  return bm == 128 ? (const void*)&mx_tile_kernel<FA, FB, EXACT, 4> : bm == 64 ? (const void*)&mx_tile_kernel<FA, FB, EXACT, 2> : (const void*)&mx_tile_kernel<FA, FB, EXACT, 1>;
 }
-MxEntry mx_tile_entry(int fa, int fb, bool exact, int bm, int per_cu) {
-  MxEntry e{nullptr, bm, 128, 256, fa == 4 ? 2 : 1, per_cu};
-  if (fa == 4) e.fn = tile_pick<4, 4, false>(bm, per_cu);
-  else if (fb == 4) e.fn = exact ? tile_pick<8, 4, true>(bm, per_cu) : tile_pick<8, 4, false>(bm, per_cu);
-  else e.fn = exact ? tile_pick<8, 8, true>(bm, per_cu) : tile_pick<8, 8, false>(bm, per_cu);
+MxEntry mx_tile_entry(int fa, int fb, bool exact, int bm) {
+  MxEntry e{nullptr, bm, 128, 256, fa == 4 ? 2 : 1};
+  if (fa == 4) e.fn = tile_pick<4, 4, false>(bm);
+  else if (fb == 4) e.fn = exact ? tile_pick<8, 4, true>(bm) : tile_pick<8, 4, false>(bm);
+  else e.fn = exact ? tile_pick<8, 8, true>(bm) : tile_pick<8, 8, false>(bm);
   return e;
 }
 

@@ -323,7 +323,7 @@ static const void* pp_pick(int out) {
   return out == 0 ? (const void*)&mx_pp_kernel<FA, FB, 0> : out == 1 ? (const void*)&mx_pp_kernel<FA, FB, 1> : (const void*)&mx_pp_kernel<FA, FB, 2>;
 }
 MxEntry mx_pp_entry(int fa, int fb, int out) {
-  MxEntry e{nullptr, 256, 256, 512, fa == 4 ? 2 : 1, 1};
+  MxEntry e{nullptr, 256, 256, 512, fa == 4 ? 2 : 1};
   e.fn = fa == 4 ? pp_pick<4, 4>(out) : fb == 4 ? pp_pick<8, 4>(out) : pp_pick<8, 8>(out);
   return e;
 }

@@ -20,9 +20,9 @@ __device__ __forceinline__ unsigned load_bytes(__amdgpu_buffer_rsrc_t r, unsigne
   else return (unsigned)__builtin_amdgcn_raw_buffer_load_b32(r, voffset, soffset, 0);
 }
 
-template <int FA, int FB, bool EXACT, int MT, int NF>
+template <int FA, int FB, bool EXACT, int MT>
 __global__ void __launch_bounds__(64 * kSkinnyWaves) mx_skinny_kernel(MxGemmArgs args) {
-  constexpr int W = kSkinnyWaves;
+  constexpr int W = kSkinnyWaves, NF = 1;
   // Pieces (k-steps) in flight: what about 128 registers hold, 2 to 8.
   constexpr int REGS = MT * FA + NF * FB + 2, D = 128 / REGS < 2 ? 2 : 128 / REGS > 8 ? 8 : 128 / REGS;
   __shared__ float red[W][MT * NF * 4][64];
@@ -155,20 +155,15 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) mx_skinny_kernel(MxGemmArgs
   }
 }
 
-template <int FA, int FB, bool EXACT, int MT>
-static const void* skinny_pick(int nf) {
-  return nf == 1 ? (const void*)&mx_skinny_kernel<FA, FB, EXACT, MT, 1> : nf == 2 ? (const void*)&mx_skinny_kernel<FA, FB, EXACT, MT, 2>
-                 : (const void*)&mx_skinny_kernel<FA, FB, EXACT, MT, 4>;
-}
 template <int FA, int FB, bool EXACT>
-static const void* skinny_rows(int mt, int nf) {
-  return mt == 1 ? skinny_pick<FA, FB, EXACT, 1>(nf) : mt == 2 ? skinny_pick<FA, FB, EXACT, 2>(nf) : skinny_pick<FA, FB, EXACT, 4>(nf);
+static const void* skinny_pick(int mt) {
+  return mt == 1 ? (const void*)&mx_skinny_kernel<FA, FB, EXACT, 1> : (const void*)&mx_skinny_kernel<FA, FB, EXACT, 2>;
 }
-MxEntry mx_skinny_entry(int fa, int fb, bool exact, int mt, int nf) {
-  MxEntry e{nullptr, 16 * mt, 16 * nf, 64 * kSkinnyWaves, 1, 1};
-  if (fa == 4) e.fn = skinny_rows<4, 4, false>(mt, nf);
-  else if (fb == 4) e.fn = exact ? skinny_rows<8, 4, true>(mt, nf) : skinny_rows<8, 4, false>(mt, nf);
-  else e.fn = exact ? skinny_rows<8, 8, true>(mt, nf) : skinny_rows<8, 8, false>(mt, nf);
+MxEntry mx_skinny_entry(int fa, int fb, bool exact, int mt) {
+  MxEntry e{nullptr, 16 * mt, 16, 64 * kSkinnyWaves, 1};
+  if (fa == 4) e.fn = skinny_pick<4, 4, false>(mt);
+  else if (fb == 4) e.fn = exact ? skinny_pick<8, 4, true>(mt) : skinny_pick<8, 4, false>(mt);
+  else e.fn = exact ? skinny_pick<8, 8, true>(mt) : skinny_pick<8, 8, false>(mt);
   return e;
 }
 
