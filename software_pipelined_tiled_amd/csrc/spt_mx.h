@@ -74,6 +74,7 @@ struct NormArgs {
   int n, blocks, wtype;
   float eps;
   int64_t per;          // rows of a workgroup
+  int lanes;
 };
 struct NormGradArgs {
   const char* dy;
@@ -86,6 +87,7 @@ struct NormGradArgs {
   int n, wtype;
   float eps;
   int64_t per;
+  int lanes;
 };
 struct NormPartsArgs {
   const float* parts;
@@ -96,9 +98,8 @@ struct NormPartsArgs {
 const void* mx_quantize_fn(int dtype, int bits);
 const void* mx_values_fn(int dtype, int bits);
 const void* mx_pack_fn();
-constexpr int kNormThreads = 512;
-// out: 0 the input's type, else bits; c: pieces of eight values a thread keeps in registers (1, 2, 4, and 8 without
-// gradients), 0: rows of any length
+// out: 0 the input's type, else bits; c: pieces of eight values to a thread (1, 2, and the 16-bit norms 4; up to 1024 threads), -1:
+// rows of `lanes` threads of 256, 0: rows of any length, 512 threads, -2: gradients with 32 bytes of LDS to a piece, 1024 threads
 const void* norm_fn(int dtype, int out, int c);
 const void* norm_grad_fn(int dtype, int c);
 const void* norm_parts_fn();

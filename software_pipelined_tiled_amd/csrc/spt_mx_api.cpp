@@ -133,19 +133,41 @@ gemm_status_t mx_shape(const gemm_mx_t* p, MxShape* s) {
 }
 
 // ---------------------------------------------------------------------------------- norm
-// Pieces of eight values a thread keeps, and threads of a workgroup. 0 pieces: a row too long for registers.
+// Pieces of eight values a thread keeps (0: a row too long for registers; -1: a row is a part of a wave's; -2: gradients of
+// long rows with dweight's sums in LDS), threads of a row and of a workgroup, bytes of LDS, rows of a workgroup.
+constexpr int64_t kGradLdsPieces = 4992;  // 156 KB of the 160
 struct NormShape {
-  int c, threads;
+  int c, lanes, threads, lds;
   int64_t per, grid;
 };
-NormShape norm_shape(int64_t rows, int64_t n, int most, int per_cu) {
-  NormShape s;
-  const int64_t pieces = ceil_div(n, 8);
-  s.c = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 4;
-  if (pieces > s.c * kNormThreads) s.c = most == 8 && pieces <= 8 * kNormThreads ? 8 : 0;
-  s.threads = s.c ? (int)round_up(ceil_div(pieces, s.c), 64) : kNormThreads;
-  const int64_t fit = (int64_t)kCus * per_cu;
+// A thread has as few pieces as 1024 threads allow (with the residual: 300 rows of 4096 bf16 4.0 us, 4.3 with two pieces to half the
+// threads; 1003 rows of 4097 fp32 12.8, 14.1), and a workgroup neighbouring rows, so that all workgroups are on the compute units at once
+// (6 waves to a SIMD, for the gradients' registers 5: 8192 rows of 4096 bf16 60 us, 65 with 6).
+NormShape norm_shape(int64_t rows, int64_t n, gemm_dtype_t dtype, bool mx, bool grad) {
+  NormShape s{};
+  const int64_t pieces = mx ? mx_blocks(n) * (kMxBlock / 8) : ceil_div(n, 8);
+  int64_t per_cu;
+  if (pieces <= 64) {
+    s.c = -1;
+    s.threads = 256;
+    for (s.lanes = mx ? 16 : 4; s.lanes < pieces;) s.lanes *= 2;
+    per_cu = grad ? 3 : 6;
+  } else {
+    if (pieces <= 1024) s.c = 1;
+    else if (pieces <= 2048) s.c = 2;
+    else if (grad) s.c = pieces <= kGradLdsPieces ? -2 : 0;
+    else s.c = pieces <= 4096 && dtype != GEMM_F32 ? 4 : 0;
+    s.threads = s.c > 0 ? (int)round_up(ceil_div(pieces, s.c), 64) : s.c < 0 ? 1024 : 512;
+    if (s.c == -2) s.lds = (int)pieces * 32;
+    s.lanes = s.threads;
+    per_cu = s.threads > 512 ? 1 : (grad ? 1280 : 1536) / s.threads;
+  }
+  const int64_t together = s.c == -1 ? s.threads / s.lanes : 1;  // rows of a workgroup at once
+  const int64_t fit = kCus * per_cu;
   s.per = ceil_div(rows, fit);
+  // every workgroup leaves a plane of dweight: at least eight rows to one, as long as all compute units have one
+  if (grad && s.per < 8) s.per = ceil_div(rows, kCus) < 8 ? ceil_div(rows, kCus) : 8;
+  s.per = round_up(s.per, together);
   s.grid = s.per > 0 ? ceil_div(rows, s.per) : 0;
   return s;
 }
@@ -180,8 +202,9 @@ gemm_status_t run_norm(const norm_rms_t* p, int out, const void* x, const void* 
   a.blocks = (int)mx_blocks(p->n);
   a.wtype = (int)p->weight_dtype;
   a.eps = p->eps;
-  const NormShape s = norm_shape(p->rows, out ? mx_blocks(p->n) * kMxBlock : p->n, 8, 8);
+  const NormShape s = norm_shape(p->rows, p->n, p->dtype, out != 0, false);
   a.per = s.per;
+  a.lanes = s.lanes;
   return launch(norm_fn((int)p->dtype, out, s.c), dim3((unsigned)s.grid), s.threads, 0, &a, stream);
 }
 
@@ -191,7 +214,7 @@ gemm_status_t check_grad(const norm_rms_grad_t* p) {
   f.rows = p->rows; f.n = p->n; f.dtype = p->dtype; f.weight_dtype = p->weight_dtype; f.eps = p->eps;
   return check_norm(&f);
 }
-NormShape grad_shape(const norm_rms_grad_t* p) { return norm_shape(p->rows, p->n, 4, 4); }
+NormShape grad_shape(const norm_rms_grad_t* p) { return norm_shape(p->rows, p->n, p->dtype, false, true); }
 
 }  // namespace
 
@@ -365,7 +388,8 @@ gemm_status_t norm_rms_grad_run(const norm_rms_grad_t* p, const void* dy, const 
     a.wtype = (int)p->weight_dtype;
     a.eps = p->eps;
     a.per = s.per;
-    st = launch(norm_grad_fn((int)p->dtype, s.c), dim3((unsigned)s.grid), s.threads, 0, &a, stream);
+    a.lanes = s.lanes;
+    st = launch(norm_grad_fn((int)p->dtype, s.c), dim3((unsigned)s.grid), s.threads, s.lds, &a, stream);
     if (st != GEMM_OK || !dweight) return st;
   }
   if (!dweight) return GEMM_OK;

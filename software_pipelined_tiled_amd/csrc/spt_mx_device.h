@@ -13,75 +13,86 @@ typedef short s16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kTypeSize[3] = {2, 2, 4};  // f16, bf16, f32
 
-template <int T>
-__device__ __forceinline__ float to_float(unsigned short v) {
-  if constexpr (T == 0) return (float)__builtin_bit_cast(_Float16, v);
-  else return __builtin_bit_cast(float, (unsigned)v << 16);
-}
-
-// The float nearest to `v` among type T's.
-template <int T>
-__device__ __forceinline__ float round_to(float v) {
-  if constexpr (T == 2) return v;
-  else if constexpr (T == 0) return (float)(_Float16)v;
-  else return (float)(__bf16)v;
-}
-
 // 16 bytes at any element's alignment: the memory path takes dwords off their own size (1003 rows of 4097 fp32 through the
 // norm and its gradients: 26 us, 86 with an element at a time).
 typedef unsigned u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
+// Eight values of type T as they lie in memory.
+template <int T>
+struct Raw8 {
+  u32x4 q[T == 2 ? 2 : 1];
+};
+
 // Eight values at `p`, of which `left` are there; the others become zeros.
 template <int T>
-__device__ __forceinline__ void load8(const char* p, int left, float (&v)[8]) {
+__device__ __forceinline__ Raw8<T> load_raw(const char* p, int left) {
+  Raw8<T> r;
   if (left >= 8) {
-    if constexpr (T == 2) {
-      const f32x4 a = __builtin_bit_cast(f32x4, (u32x4) * (const u32x4_any*)p), b = __builtin_bit_cast(f32x4, (u32x4) * (const u32x4_any*)(p + 16));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = a[e], v[4 + e] = b[e];
-    } else {
-      const u32x4 q = *(const u32x4_any*)p;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = to_float<T>((unsigned short)(q[e] & 0xFFFFu));
-        v[2 * e + 1] = to_float<T>((unsigned short)(q[e] >> 16));
-      }
-    }
-    return;
+    r.q[0] = *(const u32x4_any*)p;
+    if constexpr (T == 2) r.q[1] = *(const u32x4_any*)(p + 16);
+    return r;
   }
+  r.q[0] = u32x4{0, 0, 0, 0};
+  if constexpr (T == 2) r.q[1] = r.q[0];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    v[e] = 0.f;
+  for (int e = 0; e < 8; ++e)
     if (e < left) {
-      if constexpr (T == 2) v[e] = ((const float*)p)[e];
-      else v[e] = to_float<T>(((const unsigned short*)p)[e]);
+      if constexpr (T == 2) r.q[e >> 2][e & 3] = ((const unsigned*)p)[e];
+      else r.q[0][e >> 1] |= (unsigned)((const unsigned short*)p)[e] << (16 * (e & 1));
     }
-  }
+  return r;
 }
 
 template <int T>
-__device__ __forceinline__ void put8(char* p, int left, const float (&v)[8]) {
-  if constexpr (T == 2) {
-    if (left >= 8) {
-      *(u32x4_any*)p = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
-      *(u32x4_any*)(p + 16) = __builtin_bit_cast(u32x4, f32x4{v[4], v[5], v[6], v[7]});
-      return;
-    }
+__device__ __forceinline__ void unpack(const Raw8<T>& r, float (&v)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) ((float*)p)[e] = v[e];
-  } else {
-    u32x4 q;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = T == 1 ? pack_bf16(v[2 * e], v[2 * e + 1]) : pack_f16(v[2 * e], v[2 * e + 1]);
-    if (left >= 8) {
-      *(u32x4_any*)p = q;
-      return;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < left) ((unsigned short*)p)[e] = (unsigned short)(q[e >> 1] >> (16 * (e & 1)));
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (T == 2) {
+      const unsigned word = r.q[e >> 2][e & 3];  // (a bit_cast of the element itself would take the vector's first)
+      v[e] = __builtin_bit_cast(float, word);
+    } else if constexpr (T == 1) v[e] = __builtin_bit_cast(float, (e & 1) ? r.q[0][e >> 1] & 0xFFFF0000u : r.q[0][e >> 1] << 16);
+    else v[e] = (float)__builtin_bit_cast(_Float16, (unsigned short)(r.q[0][e >> 1] >> (16 * (e & 1))));
   }
+}
+
+// Eight floats rounded to type T.
+template <int T>
+__device__ __forceinline__ Raw8<T> pack(const float (&v)[8]) {
+  Raw8<T> r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (T == 2) {
+      r.q[0][e] = __builtin_bit_cast(unsigned, v[e]);
+      r.q[1][e] = __builtin_bit_cast(unsigned, v[4 + e]);
+    } else {
+      r.q[0][e] = T == 1 ? pack_bf16(v[2 * e], v[2 * e + 1]) : pack_f16(v[2 * e], v[2 * e + 1]);
+    }
+  }
+  return r;
+}
+
+template <int T>
+__device__ __forceinline__ void put_raw(char* p, int left, const Raw8<T>& r) {
+  if (left >= 8) {
+    *(u32x4_any*)p = r.q[0];
+    if constexpr (T == 2) *(u32x4_any*)(p + 16) = r.q[1];
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < left) {
+      if constexpr (T == 2) ((unsigned*)p)[e] = r.q[e >> 2][e & 3];
+      else ((unsigned short*)p)[e] = (unsigned short)(r.q[0][e >> 1] >> (16 * (e & 1)));
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void load8(const char* p, int left, float (&v)[8]) {
+  unpack<T>(load_raw<T>(p, left), v);
+}
+template <int T>
+__device__ __forceinline__ void put8(char* p, int left, const float (&v)[8]) {
+  put_raw<T>(p, left, pack<T>(v));
 }
 
 // Eight values of any type (a weight's): the type is the launch's, so the branch is the same for all lanes.

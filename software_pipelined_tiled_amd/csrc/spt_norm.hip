@@ -1,80 +1,117 @@
 // Root-mean-square norm with the residual's addition, its microscaled form, and its gradients.
 //
-// What bounds them: bytes. A row is read once and stays in registers between the sum of its squares and the result
-// (up to 32 values a thread: rows of 32768), so x, the residual, h and y cross memory once each; longer rows are read a
-// second time. A workgroup takes neighbouring rows and keeps its columns' weights (and its sums of dweight)
-// in registers from row to row. h is rounded to the tensors' type before the statistics: what is normalised is the h that the
+// What bounds them: bytes. A row is read once and stays in registers, as it lies in memory, between the sum of its squares and
+// the result, so x, the residual, h and y cross memory once each; rows of more than 32768 16-bit or 16384 fp32 values
+// are read a second time. h is rounded to the tensors' type before the statistics: what is normalised is the h that the
 // caller gets, as where the addition is an operator of its own. Statistics and products are fp32, y and dx are rounded once.
 //
+// A workgroup has a row at a time, and takes several neighbouring rows, the next one's loads in flight while it adds up the
+// squares; rows of up to 512 values are a wave's or a part of one, several to a workgroup (30000 rows of 200: 9.8 us, 26 with a
+// wave to a row). Weights stay in registers from row to row where rows are short enough, and else come from the L2. With the
+// residual, at the rate of a large copy (5.16 TB/s) in brackets: 8191 rows of 8192 fp16 105 us (104), as 8-bit MX 98 (92), 2000
+// rows of 28672 bf16 106 (89), 1003 rows of 4097 fp32 12.7 (12.8: part of it stays in the last cache).
+//
 // Gradients: sum h^2 and sum g h come out of one pass, so that r need not be kept by the forward. dweight's sums run
-// over a workgroup's rows in registers, leave as one fp32 plane a workgroup, and are added in the planes' order by a second
-// kernel: no atomics, the same bits on every run.
+// over a workgroup's rows in registers, for rows of more than 16384 values in LDS, and in its plane in memory for those that the
+// LDS does not hold either; they leave as one fp32 plane a workgroup, and are added in the planes' order by a second
+// kernel: no atomics, the same bits on every run. With dh: 8191 rows of 8192 fp16 116 us (104), 2000 of 28672 bf16 141 (89; 185
+// with the sums in registers, which did not fit), 1000 of 40960 fp16 186 (64), 300 rows of 4096 10 (1.9: two launches).
 #include "spt_mx_device.h"
 
 namespace spt {
 
-// The sum of N values over a workgroup, to all its threads, in a fixed order. `red` holds two sets of N x 16 floats used in
-// turn (`turn`), so that one barrier a call is enough.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* red, int turn) {
-  float* r = red + turn * N * 16;
-  const int waves = blockDim.x >> 6;
+constexpr int kShort = -1;  // C of rows that a part of a wave holds
+constexpr int kLds = -2;    // gradients: C of long rows with dweight's sums in LDS
+
+// The sum of N values over the `lanes` threads of a row (a power of two up to 64, or all the workgroup's), to all of them, in a fixed
+// order. `red` holds two sets of N x 16 floats used in turn (`turn`), so that one barrier a call is enough.
+template <int N, bool SHORT>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int turn, int lanes) {
+  if constexpr (SHORT) {
+    for (int d = lanes >> 1; d >= 1; d >>= 1) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d);
+    }
+  } else {
+    float* r = red + turn * N * 16;
+    const int waves = blockDim.x >> 6;
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v[i] += __shfl_xor(v[i], d);
-  }
-  if (waves == 1) return;
-  if ((threadIdx.x & 63) == 0) {
+    for (int i = 0; i < N; ++i) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) r[i * 16 + (threadIdx.x >> 6)] = v[i];
-  }
-  __syncthreads();
+      for (int d = 32; d >= 1; d >>= 1) v[i] += __shfl_xor(v[i], d);
+    }
+    if (waves == 1) return;
+    if ((threadIdx.x & 63) == 0) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float t = 0.f;
-    for (int w = 0; w < waves; ++w) t += r[i * 16 + w];
-    v[i] = t;
+      for (int i = 0; i < N; ++i) r[i * 16 + (threadIdx.x >> 6)] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float t = 0.f;
+      for (int w = 0; w < waves; ++w) t += r[i * 16 + w];
+      v[i] = t;
+    }
   }
 }
 
-// C: pieces of eight values a thread holds of a row (0: rows of any length, in two passes). OUT: 0 y in type T, 4 or 8: MX.
+__device__ __forceinline__ void load_weight(const char* w, int type, int col, int n, float (&o)[8]) {
+  if (w) {
+    load8_any(w, type, col, n - col, o);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 1.f;
+  }
+}
+
+// C: pieces of eight values a thread holds of a row (kShort: one, rows of part of a wave; 0: rows of any length, in two passes).
+// OUT: 0 y in type T, 4 or 8: MX.
 template <int T, int OUT, int C>
-__global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
+__global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_kernel(NormArgs a) {
   __shared__ float red[2 * 16];
-  constexpr int ES = kTypeSize[T], KEEP = C ? C : 1;
-  const int nt = blockDim.x, n = a.n;
+  constexpr bool SHORT = C == kShort;
+  constexpr int ES = kTypeSize[T], P = SHORT ? 1 : C, KEEP = P ? P : 1;
+  constexpr bool W_KEPT = P == 1 || P == 2;
+  const int n = a.n, lanes = SHORT ? a.lanes : blockDim.x, at = threadIdx.x & (SHORT ? lanes - 1 : 1023);
   const int pieces = OUT ? a.blocks * (kMxBlock / 8) : (n + 7) / 8;  // an MX row's padding is written too
-  const int64_t first = (int64_t)blockIdx.x * a.per, last = first + a.per < a.rows ? first + a.per : a.rows;
+  // this thread's first row, the last row of its workgroup, and from row to row
+  const int step = SHORT ? blockDim.x / lanes : 1;
+  const int64_t first = (int64_t)blockIdx.x * a.per + (SHORT ? threadIdx.x / lanes : 0);
+  const int64_t last = ((int64_t)blockIdx.x + 1) * a.per < a.rows ? ((int64_t)blockIdx.x + 1) * a.per : a.rows;
   const float inv_n = 1.f / (float)n;
 
-  float w[KEEP][8];
-  auto weight = [&](int col, float (&o)[8]) SPT_INLINE {
-    if (a.w) {
-      load8_any(a.w, a.wtype, col, n - col, o);
-    } else {
+  auto col_of = [&](int c) SPT_INLINE { return (c * lanes + at) * 8; };
+  float w[W_KEPT ? KEEP : 1][8];
+  if constexpr (W_KEPT) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = 1.f;
-    }
-  };
-  // h's eight values at `col`, written where a residual is added
-  auto h_at = [&](int64_t row, int col, float (&o)[8]) SPT_INLINE {
-    load8<T>(a.x + (row * a.ldx + col) * ES, n - col, o);
-    if (a.r) {
-      float r[8];
-      load8<T>(a.r + (row * a.ldr + col) * ES, n - col, r);
+    for (int c = 0; c < P; ++c) load_weight(a.w, a.wtype, col_of(c), n, w[c]);
+  }
+  // h's eight values at `col` from x's and the residual's
+  auto sum_of = [&](int64_t row, int col, const Raw8<T>& x, const Raw8<T>& r) SPT_INLINE {
+    if (!a.r) return x;
+    float u[8], v[8];
+    unpack<T>(x, u);
+    unpack<T>(r, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = round_to<T>(o[e] + r[e]);
-      put8<T>(a.h + (row * a.ldh + col) * ES, n - col, o);
-    }
+    for (int e = 0; e < 8; ++e) u[e] += v[e];
+    const Raw8<T> h = pack<T>(u);
+    put_raw<T>(a.h + row * a.ldh * ES + (unsigned)(col * ES), n - col, h);
+    return h;
   };
-  auto result = [&](int64_t row, int piece, const float (&h)[8], const float (&wt)[8], float rstd) SPT_INLINE {
+  auto square = [&](const Raw8<T>& h, float& s) SPT_INLINE {
+    float v[8];
+    unpack<T>(h, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(v[e], v[e], s);
+  };
+  auto result = [&](int64_t row, int piece, const Raw8<T>& h, const float (&wt)[8], float rstd) SPT_INLINE {
     const int col = piece * 8;
     float y[8];
+    unpack<T>(h, y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = h[e] * rstd * wt[e];
+    for (int e = 0; e < 8; ++e) y[e] = y[e] * rstd * wt[e];
     if constexpr (OUT == 0) {
-      put8<T>(a.y + (row * a.ldy + col) * ES, n - col, y);
+      put8<T>(a.y + row * a.ldy * ES + (unsigned)(col * ES), n - col, y);
     } else {
       // columns behind n have to be zeros also where the row's factor is not finite
 #pragma unroll
@@ -94,146 +131,212 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(NormArgs a) {
     }
   };
 
-  if constexpr (C > 0) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) weight((c * nt + (int)threadIdx.x) * 8, w[c]);
-  }
   int turn = 0;
-  for (int64_t row = first; row < last; ++row, turn ^= 1) {
-    float h[KEEP][8], sum[1] = {0.f};
-    if constexpr (C > 0) {
+  if constexpr (P > 0) {
+    constexpr bool AHEAD = P <= 2;  // the next row's loads before this row's sum
+    Raw8<T> x[KEEP], r[KEEP];
+    auto fetch = [&](int64_t row) SPT_INLINE {
 #pragma unroll
-      for (int c = 0; c < C; ++c) h_at(row, (c * nt + (int)threadIdx.x) * 8, h[c]);
+      for (int c = 0; c < P; ++c) {
+        const int col = col_of(c);
+        x[c] = load_raw<T>(a.x + row * a.ldx * ES + (unsigned)(col * ES), n - col);
+        if (a.r) r[c] = load_raw<T>(a.r + row * a.ldr * ES + (unsigned)(col * ES), n - col);
+      }
+    };
+    if (AHEAD && first < last) fetch(first);
+    for (int64_t row = first; row < last; row += step, turn ^= 1) {
+      if (!AHEAD) fetch(row);
+      Raw8<T> h[KEEP];
+      float sum[1] = {0.f};
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+      for (int c = 0; c < P; ++c) {
+        h[c] = sum_of(row, col_of(c), x[c], r[c]);
+        square(h[c], sum[0]);
+      }
+      if (AHEAD && row + step < last) fetch(row + step);
+      row_sum<1, SHORT>(sum, red, turn, lanes);
+      const char* wp = a.w;
+      if constexpr (!W_KEPT) asm volatile("" : "+s"(wp));  // loaded for each row: out of the loop they would be kept all the same
+      const float rstd = 1.f / __builtin_sqrtf(sum[0] * inv_n + a.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[0] = __builtin_fmaf(h[c][e], h[c][e], sum[0]);
-    } else {
-      for (int p = threadIdx.x; p * 8 < n; p += nt) {
-        h_at(row, p * 8, h[0]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[0] = __builtin_fmaf(h[0][e], h[0][e], sum[0]);
+      for (int c = 0; c < P; ++c) {
+        const int piece = c * lanes + at;
+        if (piece >= pieces) continue;
+        if constexpr (W_KEPT) {
+          result(row, piece, h[c], w[c], rstd);
+        } else {
+          load_weight(wp, a.wtype, piece * 8, n, w[0]);
+          result(row, piece, h[c], w[0], rstd);
+        }
       }
     }
-    block_sum<1>(sum, red, turn);
-    const float rstd = 1.f / __builtin_sqrtf(sum[0] * inv_n + a.eps);
-    if constexpr (C > 0) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int p = c * nt + (int)threadIdx.x;
-        if (p < pieces) result(row, p, h[c], w[c], rstd);
+  } else {
+    for (int64_t row = first; row < last; ++row, turn ^= 1) {
+      float sum[1] = {0.f};
+      for (int p = threadIdx.x; p * 8 < n; p += lanes) {
+        const int col = p * 8;
+        const Raw8<T> x = load_raw<T>(a.x + row * a.ldx * ES + (unsigned)(col * ES), n - col);
+        square(sum_of(row, col, x, a.r ? load_raw<T>(a.r + row * a.ldr * ES + (unsigned)(col * ES), n - col) : x), sum[0]);
       }
-    } else {
+      row_sum<1, false>(sum, red, turn, lanes);
+      const float rstd = 1.f / __builtin_sqrtf(sum[0] * inv_n + a.eps);
       // what this thread wrote to h, or read from x, a pass before
       const char* src = a.r ? a.h : a.x;
       const int64_t ld = a.r ? a.ldh : a.ldx;
-      for (int p = threadIdx.x; p < pieces; p += nt) {
-        load8<T>(src + (row * ld + p * 8) * ES, n - p * 8, h[0]);
-        weight(p * 8, w[0]);
-        result(row, p, h[0], w[0], rstd);
+      for (int p = threadIdx.x; p < pieces; p += lanes) {
+        const Raw8<T> h = load_raw<T>(src + row * ld * ES + (unsigned)((p * 8) * ES), n - p * 8);
+        load_weight(a.w, a.wtype, p * 8, n, w[0]);
+        result(row, p, h, w[0], rstd);
       }
     }
   }
 }
 
+// C as above, and kLds.
 template <int T, int C>
-__global__ void __launch_bounds__(kNormThreads) norm_grad_kernel(NormGradArgs a) {
+__global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_grad_kernel(NormGradArgs a) {
   __shared__ float red[2 * 2 * 16];
-  constexpr int ES = kTypeSize[T], KEEP = C ? C : 1;
-  const int nt = blockDim.x, n = a.n;
-  const int64_t first = (int64_t)blockIdx.x * a.per, last = first + a.per < a.rows ? first + a.per : a.rows;
+  constexpr bool SHORT = C == kShort;
+  constexpr int ES = kTypeSize[T], P = SHORT ? 1 : C == kLds ? 0 : C, KEEP = P ? P : 1;
+  constexpr bool W_KEPT = P == 1;
+  const int n = a.n, lanes = SHORT ? a.lanes : blockDim.x, at = threadIdx.x & (SHORT ? lanes - 1 : 1023);
+  const int step = SHORT ? blockDim.x / lanes : 1;
+  const int64_t first = (int64_t)blockIdx.x * a.per + (SHORT ? threadIdx.x / lanes : 0);
+  const int64_t last = ((int64_t)blockIdx.x + 1) * a.per < a.rows ? ((int64_t)blockIdx.x + 1) * a.per : a.rows;
   const float inv_n = 1.f / (float)n;
   float* plane = a.parts ? a.parts + (int64_t)blockIdx.x * n : nullptr;
 
-  auto weight = [&](int col, float (&o)[8]) SPT_INLINE {
-    if (a.w) {
-      load8_any(a.w, a.wtype, col, n - col, o);
-    } else {
+  auto col_of = [&](int c) SPT_INLINE { return (c * lanes + at) * 8; };
+  float w[1][8];
+  if constexpr (W_KEPT) load_weight(a.w, a.wtype, col_of(0), n, w[0]);
+  auto add = [&](const Raw8<T>& dy, const Raw8<T>& h, const float (&wt)[8], float (&sum)[2]) SPT_INLINE {
+    float u[8], v[8];
+    unpack<T>(dy, u);
+    unpack<T>(h, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = 1.f;
+    for (int e = 0; e < 8; ++e) {
+      sum[0] = __builtin_fmaf(v[e], v[e], sum[0]);
+      sum[1] = __builtin_fmaf(u[e] * wt[e], v[e], sum[1]);
     }
   };
-  float w[KEEP][8], dw[KEEP][8];
-  if constexpr (C > 0) {
+  // dx's eight values at `col`, with f = r^2 mean(g h)
+  auto grad = [&](int64_t row, int col, const Raw8<T>& dy, const Raw8<T>& h, const Raw8<T>& dh, const float (&wt)[8], float rstd,
+                  float f) SPT_INLINE {
+    float u[8], v[8], d[8];
+    unpack<T>(dy, u);
+    unpack<T>(h, v);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      weight((c * nt + (int)threadIdx.x) * 8, w[c]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dw[c][e] = 0.f;
-    }
-  }
-  // dx's eight values at `col`; t = h r^3 mean(g h) / .. as one factor
-  auto grad = [&](int64_t row, int col, const float (&dy)[8], const float (&h)[8], const float (&wt)[8], float rstd, float f) SPT_INLINE {
-    float d[8];
+    for (int e = 0; e < 8; ++e) u[e] = rstd * (u[e] * wt[e] - v[e] * f);
     if (a.dh) {
-      load8<T>(a.dh + (row * a.lddh + col) * ES, n - col, d);
+      unpack<T>(dh, d);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] += rstd * (dy[e] * wt[e] - h[e] * f);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = rstd * (dy[e] * wt[e] - h[e] * f);
+      for (int e = 0; e < 8; ++e) u[e] += d[e];
     }
-    put8<T>(a.dx + (row * a.lddx + col) * ES, n - col, d);
+    put8<T>(a.dx + row * a.lddx * ES + (unsigned)(col * ES), n - col, u);
   };
   int turn = 0;
-  for (int64_t row = first; row < last; ++row, turn ^= 1) {
-    float dy[KEEP][8], h[KEEP][8], sum[2] = {0.f, 0.f};
-    auto add = [&](const float (&u)[8], const float (&v)[8], const float (&wt)[8]) SPT_INLINE {
+  if constexpr (P > 0) {
+    float dw[KEEP][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum[0] = __builtin_fmaf(v[e], v[e], sum[0]);
-        sum[1] = __builtin_fmaf(u[e] * wt[e], v[e], sum[1]);
-      }
+    for (int c = 0; c < P; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dw[c][e] = 0.f;
+    constexpr bool AHEAD = P == 1;  // the next row's loads before this row's sum
+    Raw8<T> dy[KEEP], h[KEEP], dh[KEEP], u, v;
+    auto fetch = [&](int64_t row, int c, Raw8<T>& p, Raw8<T>& q) SPT_INLINE {
+      const int col = col_of(c);
+      p = load_raw<T>(a.dy + row * a.lddy * ES + (unsigned)(col * ES), n - col);
+      q = load_raw<T>(a.h + row * a.ldh * ES + (unsigned)(col * ES), n - col);
     };
-    if constexpr (C > 0) {
+    if (AHEAD && first < last) fetch(first, 0, dy[0], h[0]);
+    for (int64_t row = first; row < last; row += step, turn ^= 1) {
+      float sum[2] = {0.f, 0.f};
+      const char* wp = a.w;
+      if constexpr (!W_KEPT) asm volatile("" : "+s"(wp));  // loaded for each row: out of the loop they would be kept all the same
+      if constexpr (!AHEAD) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = (c * nt + (int)threadIdx.x) * 8;
-        load8<T>(a.dy + (row * a.lddy + col) * ES, n - col, dy[c]);
-        load8<T>(a.h + (row * a.ldh + col) * ES, n - col, h[c]);
+        for (int c = 0; c < P; ++c) fetch(row, c, dy[c], h[c]);
       }
 #pragma unroll
-      for (int c = 0; c < C; ++c) add(dy[c], h[c], w[c]);
-    } else {
-      for (int p = threadIdx.x; p * 8 < n; p += nt) {
-        load8<T>(a.dy + (row * a.lddy + p * 8) * ES, n - p * 8, dy[0]);
-        load8<T>(a.h + (row * a.ldh + p * 8) * ES, n - p * 8, h[0]);
-        weight(p * 8, w[0]);
-        add(dy[0], h[0], w[0]);
+      for (int c = 0; c < P; ++c) {
+        const int col = col_of(c);
+        if (a.dh) dh[c] = load_raw<T>(a.dh + row * a.lddh * ES + (unsigned)(col * ES), n - col);
+        if constexpr (!W_KEPT) load_weight(wp, a.wtype, col, n, w[0]);
+        add(dy[c], h[c], w[0], sum);
       }
+      if (AHEAD && row + step < last) fetch(row + step, 0, u, v);
+      row_sum<2, SHORT>(sum, red, turn, lanes);
+      const float rstd = 1.f / __builtin_sqrtf(sum[0] * inv_n + a.eps);
+      const float f = rstd * rstd * (sum[1] * inv_n);
+#pragma unroll
+      for (int c = 0; c < P; ++c) {
+        const int col = col_of(c);
+        if constexpr (!W_KEPT) load_weight(wp, a.wtype, col, n, w[0]);
+        if (a.dx && col < n) grad(row, col, dy[c], h[c], dh[c], w[0], rstd, f);
+        float p[8], q[8];
+        unpack<T>(dy[c], p);
+        unpack<T>(h[c], q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[c][e] = __builtin_fmaf(p[e], q[e] * rstd, dw[c][e]);
+      }
+      if constexpr (AHEAD) dy[0] = u, h[0] = v;
     }
-    block_sum<2>(sum, red, turn);
-    const float rstd = 1.f / __builtin_sqrtf(sum[0] * inv_n + a.eps);
-    const float f = rstd * rstd * (sum[1] * inv_n);
-    if constexpr (C > 0) {
+    if constexpr (SHORT) {  // the rows' parts of the workgroup, in their order
+      __shared__ float part[256 * 8];
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = (c * nt + (int)threadIdx.x) * 8;
-        if (a.dx && col < n) grad(row, col, dy[c], h[c], w[c], rstd, f);
+      for (int e = 0; e < 8; ++e) part[threadIdx.x * 8 + e] = dw[0][e];
+      __syncthreads();
+      if (plane && (int)threadIdx.x < lanes) {
+        for (int s = 1; s < step; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[c][e] = __builtin_fmaf(dy[c][e], h[c][e] * rstd, dw[c][e]);
+          for (int e = 0; e < 8; ++e) dw[0][e] += part[(s * lanes + at) * 8 + e];
+        put8<2>((char*)(plane + at * 8), n - at * 8, dw[0]);
       }
-    } else {
-      for (int p = threadIdx.x; p * 8 < n; p += nt) {
+    } else if (plane) {
+#pragma unroll
+      for (int c = 0; c < P; ++c) put8<2>((char*)(plane + col_of(c)), n - col_of(c), dw[c]);
+    }
+  } else {
+    extern __shared__ u32x4 sums[];  // kLds: two to a piece, the first ones of all pieces before the second ones
+    const int pieces = (n + 7) / 8;
+    for (int64_t row = first; row < last; ++row, turn ^= 1) {
+      float sum[2] = {0.f, 0.f};
+      auto piece = [&](int col, Raw8<T>& u, Raw8<T>& v) SPT_INLINE {
+        u = load_raw<T>(a.dy + row * a.lddy * ES + (unsigned)(col * ES), n - col);
+        v = load_raw<T>(a.h + row * a.ldh * ES + (unsigned)(col * ES), n - col);
+        load_weight(a.w, a.wtype, col, n, w[0]);
+      };
+      Raw8<T> u, v;
+      for (int p = threadIdx.x; p * 8 < n; p += lanes) {
+        piece(p * 8, u, v);
+        add(u, v, w[0], sum);
+      }
+      row_sum<2, false>(sum, red, turn, lanes);
+      const float rstd = 1.f / __builtin_sqrtf(sum[0] * inv_n + a.eps);
+      const float f = rstd * rstd * (sum[1] * inv_n);
+      for (int p = threadIdx.x; p * 8 < n; p += lanes) {
         const int col = p * 8;
-        load8<T>(a.dy + (row * a.lddy + col) * ES, n - col, dy[0]);
-        load8<T>(a.h + (row * a.ldh + col) * ES, n - col, h[0]);
-        weight(col, w[0]);
-        if (a.dx) grad(row, col, dy[0], h[0], w[0], rstd, f);
-        if (plane) {  // the plane's columns are this thread's alone
+        piece(col, u, v);
+        // dx may be dy's own memory: dweight's part is taken from what was read
+        if (a.dx) grad(row, col, u, v, a.dh ? load_raw<T>(a.dh + row * a.lddh * ES + (unsigned)(col * ES), n - col) : u, w[0], rstd, f);
+        if (plane) {  // a piece's sums are this thread's alone
+          float p8[8], q8[8], s8[8];
+          unpack<T>(u, p8);
+          unpack<T>(v, q8);
+          if (row > first) {
+            if constexpr (C == kLds) unpack<2>(Raw8<2>{sums[p], sums[pieces + p]}, s8);
+            else load8<2>((const char*)(plane + col), n - col, s8);
+          }
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (col + e < n) plane[col + e] = __builtin_fmaf(dy[0][e], h[0][e] * rstd, row == first ? 0.f : plane[col + e]);
+          for (int e = 0; e < 8; ++e) s8[e] = __builtin_fmaf(p8[e], q8[e] * rstd, row > first ? s8[e] : 0.f);
+          if (C == kLds && row + 1 < last) {
+            const Raw8<2> r8 = pack<2>(s8);
+            sums[p] = r8.q[0];
+            sums[pieces + p] = r8.q[1];
+          } else {
+            put8<2>((char*)(plane + col), n - col, s8);
+          }
         }
-      }
-    }
-  }
-  if constexpr (C > 0) {
-    if (plane) {
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const int col = (c * nt + (int)threadIdx.x) * 8;
-        put8<2>((char*)(plane + col), n - col, dw[c]);
       }
     }
   }
@@ -246,13 +349,15 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(NormPartsArgs a) {
   const int c = threadIdx.x & 3, p0 = threadIdx.x >> 2;
   const int col = blockIdx.x * 16 + c * 4;
   float s[4] = {0.f, 0.f, 0.f, 0.f};
-  const bool vec = a.n % 4 == 0 && col + 4 <= a.n;
   for (int p = p0; p < a.count; p += 64) {
     const float* src = a.parts + (int64_t)p * a.n + col;
-    if (vec) {
-      const f32x4 v = *(const f32x4*)src;
+    if (col + 4 <= a.n) {
+      const u32x4 v = *(const u32x4_any*)src;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] += v[e];
+      for (int e = 0; e < 4; ++e) {
+        const unsigned word = v[e];
+        s[e] += __builtin_bit_cast(float, word);
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -273,8 +378,14 @@ __global__ void __launch_bounds__(256) norm_parts_kernel(NormPartsArgs a) {
 
 template <int T, int OUT>
 static const void* norm_pick(int c) {
-  return c == 1 ? (const void*)&norm_kernel<T, OUT, 1> : c == 2 ? (const void*)&norm_kernel<T, OUT, 2>
-       : c == 4 ? (const void*)&norm_kernel<T, OUT, 4> : c == 8 ? (const void*)&norm_kernel<T, OUT, 8> : (const void*)&norm_kernel<T, OUT, 0>;
+  if constexpr (T != 2)
+    if (c == 4) return (const void*)&norm_kernel<T, OUT, 4>;
+  switch (c) {
+    case kShort: return (const void*)&norm_kernel<T, OUT, kShort>;
+    case 1: return (const void*)&norm_kernel<T, OUT, 1>;
+    case 2: return (const void*)&norm_kernel<T, OUT, 2>;
+    default: return (const void*)&norm_kernel<T, OUT, 0>;
+  }
 }
 template <int T>
 static const void* norm_pick_out(int out, int c) {
@@ -285,8 +396,13 @@ const void* norm_fn(int dtype, int out, int c) {
 }
 template <int T>
 static const void* norm_grad_pick(int c) {
-  return c == 1 ? (const void*)&norm_grad_kernel<T, 1> : c == 2 ? (const void*)&norm_grad_kernel<T, 2>
-       : c == 4 ? (const void*)&norm_grad_kernel<T, 4> : (const void*)&norm_grad_kernel<T, 0>;
+  switch (c) {
+    case kShort: return (const void*)&norm_grad_kernel<T, kShort>;
+    case 1: return (const void*)&norm_grad_kernel<T, 1>;
+    case 2: return (const void*)&norm_grad_kernel<T, 2>;
+    case kLds: return (const void*)&norm_grad_kernel<T, kLds>;
+    default: return (const void*)&norm_grad_kernel<T, 0>;
+  }
 }
 const void* norm_grad_fn(int dtype, int c) {
   return dtype == 0 ? norm_grad_pick<0>(c) : dtype == 1 ? norm_grad_pick<1>(c) : norm_grad_pick<2>(c);

@@ -13,16 +13,13 @@ a forward-mode tangent.
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
-
 import torch
 from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 from torch.autograd.graph import increment_version
 
 from . import _lib
-from .experts import (_16BIT, _CODES, _FLOATS, _enqueue, _matrix, _need, _on_device, _out, _ptr, _result_type, _rows_apart,
-                      _type, _workspace)
+from .experts import (_16BIT, _CODES, _FLOATS, _enqueue, _matrix, _need, _on_device, _out, _ptr, _rows_apart, _type, _workspace)
 
 
 def _wants_grad(*tensors) -> bool:
@@ -46,35 +43,44 @@ def _no_grad(call: str, *tensors) -> None:
 
 # ------------------------------------------------------------------------------- microscaled tensors
 
-@dataclass(frozen=True)
+_MX_ROWS, _MX_K = 2**31 - 64, 2**22  # the library's limits
+
 class MXTensor:
     """A microscaled tensor [rows, k] (made by ``quantize_mx``, ``pack_mx`` or ``rms_norm_mx``). bits: 8 (e4m3) or 4
     (e2m1). codes [rows, bytes], rows of whole 128 values, and scales [ceil(rows / 64), blocks, 64], the exponents of the
     scales with a bias of 127 (255: NaN). dtype: what it was made from, the products' default result."""
-    codes: torch.Tensor
-    scales: torch.Tensor
-    bits: int
-    rows: int
-    k: int
-    dtype: torch.dtype
+    __slots__ = ("bits", "rows", "k", "dtype", "device", "codes_ptr", "scales_ptr", "_data", "_codes", "_scales")
 
-    def __post_init__(self):
-        _lib.mx_bytes(self.rows, self.k, self.bits)
-        codes, scales = _shapes(self.rows, self.k, self.bits)
-        for name, t, shape in (("codes", self.codes, codes), ("scales", self.scales, scales)):
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bits: int, rows: int, k: int, dtype: torch.dtype):
+        _lib.mx_bytes(rows, k, bits)
+        for name, t, shape in zip(("codes", "scales"), (codes, scales), _shapes(rows, k, bits)):
             if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous() or t.data_ptr() % 16:
                 raise ValueError(f"{name} must be contiguous bytes {shape} on 16 bytes")
-        _need(self.codes.device == self.scales.device, "codes and scales must be on one device")
-        if self.dtype not in _FLOATS:
-            raise TypeError(f"unsupported dtype {self.dtype}")
+        _on_device("codes scales", codes, scales)
+        if dtype not in _FLOATS:
+            raise TypeError(f"unsupported dtype {dtype}")
+        self.bits, self.rows, self.k, self.dtype, self.device = bits, rows, k, dtype, codes.device
+        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+        self._data, self._codes, self._scales = None, codes, scales
 
     @property
     def shape(self) -> tuple[int, int]:
         return self.rows, self.k
 
     @property
-    def device(self) -> torch.device:
-        return self.codes.device
+    def codes(self) -> torch.Tensor:
+        if self._codes is None:  # views of the one allocation, made when somebody asks for them
+            self._codes = self._data[: self.scales_ptr - self.codes_ptr].view(_shapes(self.rows, self.k, self.bits)[0])
+        return self._codes
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._data[self.scales_ptr - self.codes_ptr:].view(_shapes(self.rows, self.k, self.bits)[1])
+        return self._scales
+
+    def __repr__(self) -> str:
+        return f"MXTensor({self.rows} x {self.k}, {self.bits} bits, {self.device})"
 
 
 def _shapes(rows: int, k: int, bits: int):
@@ -82,12 +88,23 @@ def _shapes(rows: int, k: int, bits: int):
     return (rows, blocks * 4 * bits), ((rows + 63) // 64, blocks, 64)
 
 
+def _mx_bytes(rows: int, k: int, bits: int) -> tuple[int, int]:
+    """Bytes of the codes, a multiple of 16, and of the scales."""
+    blocks = (k + 127) // 128 * 4
+    return rows * blocks * 4 * bits, ((rows + 63) // 64) * blocks * 64
+
+
 def _new_mx(rows: int, k: int, bits: int, dtype, device) -> MXTensor:
-    """Without the checks: made to the layout here."""
-    codes, scales = _shapes(rows, k, bits)
+    """Without the checks: made to the layout here, in one allocation."""
+    if rows > _MX_ROWS or k > _MX_K:
+        _lib.mx_bytes(rows, k, bits)  # refuses it
+    codes, scales = _mx_bytes(rows, k, bits)
     q = MXTensor.__new__(MXTensor)
-    q.__dict__.update(codes=torch.empty(codes, dtype=torch.uint8, device=device),
-                      scales=torch.empty(scales, dtype=torch.uint8, device=device), bits=bits, rows=rows, k=k, dtype=dtype)
+    q._data = data = torch.empty(codes + scales, dtype=torch.uint8, device=device)
+    q.bits, q.rows, q.k, q.dtype, q.device = bits, rows, k, dtype, device
+    q.codes_ptr = data.data_ptr()
+    q.scales_ptr = q.codes_ptr + codes
+    q._codes = q._scales = None
     return q
 
 
@@ -107,18 +124,19 @@ def quantize_mx(x: torch.Tensor, bits: int = 8) -> MXTensor:
     ldx = _matrix("x", x)
     rows, k = x.shape
     q = _new_mx(rows, k, bits, x.dtype, x.device)
-    _enqueue(x.device, "mx_quantize", x.data_ptr(), code, rows, k, ldx, bits, q.codes.data_ptr(), q.scales.data_ptr())
+    _enqueue(x.device, "mx_quantize", x.data_ptr(), code, rows, k, ldx, bits, q.codes_ptr, q.scales_ptr)
     return q
 
 
 def dequantize_mx(q: MXTensor, dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values of ``q``, [rows, k] in fp16, bf16 or fp32 (default: what it was made from), rounded once."""
-    dtype = _result_type(dtype, out, q.dtype)
-    _on_device("q", q.codes, q.scales)
-    _no_grad("dequantize_mx", out)
+    dtype = dtype or (q.dtype if out is None else out.dtype)
+    code = _result_code(dtype)
+    if out is not None:
+        _no_grad("dequantize_mx", out)
     out, ldo, fresh = _out(out, q.rows, q.k, dtype, q.device)
-    _enqueue(q.device, "mx_dequantize", q.codes.data_ptr(), q.scales.data_ptr(), q.bits, q.rows, q.k, out.data_ptr(),
-             _CODES[dtype], ldo)
+    _enqueue(q.device, "mx_dequantize", q.codes_ptr, q.scales_ptr, q.bits, q.rows, q.k, out.data_ptr(),
+             code, ldo)
     if not fresh:
         increment_version(out)
     return out
@@ -142,10 +160,9 @@ def pack_mx(codes: torch.Tensor, scales: torch.Tensor, bits: int, k: int | None 
     k = codes.shape[1] * 8 // bits if k is None else int(k)
     _need(k >= 0 and codes.shape[1] == -(-k * bits // 8), f"codes must have {-(-k * bits // 8)} bytes a row")
     lds = _matrix("scales", scales, rows, -(-k // 32))
-    _lib.mx_bytes(rows, k, bits)
     q = _new_mx(rows, k, bits, dtype, codes.device)
-    _enqueue(codes.device, "mx_pack", codes.data_ptr(), ldc, scales.data_ptr(), lds, bits, rows, k, q.codes.data_ptr(),
-             q.scales.data_ptr())
+    _enqueue(codes.device, "mx_pack", codes.data_ptr(), ldc, scales.data_ptr(), lds, bits, rows, k, q.codes_ptr,
+             q.scales_ptr)
     return q
 
 
@@ -155,30 +172,58 @@ def mx_matmul(a: MXTensor, b: MXTensor, out_dtype: torch.dtype | None = None, ou
     8-bit operands keep 13 bits below the largest of the products they add at a time, far below the result's rounding; fp32
     results of 8-bit operands go through bf16 instructions, whose sums keep all of fp32, at less than half the rate. No
     gradient."""
-    _need(a.k == b.k, f"a has rows of {a.k}, b of {b.k}")
-    _on_device("a b", a.codes, b.codes)
+    dev = a.device
+    if a.k != b.k:
+        raise ValueError(f"a has rows of {a.k}, b of {b.k}")
+    if b.device != dev:
+        raise ValueError(f"b is on {b.device}, a on {dev}")
     _need(a.bits == 8 or b.bits == 4, "a 4-bit a goes with a 4-bit b")
-    _no_grad("mx_matmul", out)
-    dtype = _result_type(out_dtype, out, a.dtype)
-    out, ldc, fresh = _out(out, a.rows, b.rows, dtype, a.device)
-    p = _lib.GemmMx(a.rows, b.rows, a.k, a.bits, b.bits, _CODES[dtype], ldc)
+    if out is not None:
+        _no_grad("mx_matmul", out)
+    dtype = out_dtype or (a.dtype if out is None else out.dtype)
+    code = _result_code(dtype)
+    out, ldc, fresh = _out(out, a.rows, b.rows, dtype, dev)
+    p = _lib.GemmMx(a.rows, b.rows, a.k, a.bits, b.bits, code, ldc)
     ws_bytes = _lib.gemm_mx_workspace_bytes(p)
-    ws = _workspace(ws_bytes, a.device)
-    _enqueue(a.device, "gemm_mx_run", p, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(), b.scales.data_ptr(),
-             out.data_ptr(), _ptr(ws), ws_bytes)
+    ws = _workspace(ws_bytes, dev)
+    _enqueue(dev, "gemm_mx_run", p, a.codes_ptr, a.scales_ptr, b.codes_ptr, b.scales_ptr, out.data_ptr(), _ptr(ws), ws_bytes)
     if not fresh:
         increment_version(out)
     return out
 
 
+def _result_code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
+
+
 def mx_linear(x: torch.Tensor, w: MXTensor, bits: int = 8, out_dtype: torch.dtype | None = None,
               out: torch.Tensor | None = None) -> torch.Tensor:
     """x [rows, k] quantised to ``bits`` and multiplied with the weight w [n, k]: [rows, n] in x's type or ``out_dtype``.
-    A 4-bit weight takes rows of 8 bits or 4, an 8-bit one rows of 8. No gradient."""
+    The same as ``mx_matmul(quantize_mx(x, bits), w)``, with one workspace. A 4-bit weight takes rows of 8 bits or 4, an
+    8-bit one rows of 8. No gradient."""
+    code, bits, dev = _type("x", x, _FLOATS), _bits(bits), x.device
+    _need(bits == 8 or w.bits == 4, "rows of 4 bits go with a 4-bit weight")
+    if not x.is_cuda or w.device != dev:
+        _on_device("x w", x, w.codes)
     _no_grad("mx_linear", x, out)
-    _need(_bits(bits) == 8 or w.bits == 4, "rows of 4 bits go with a 4-bit weight")
-    _need(x.dim() == 2 and x.shape[1] == w.k, f"x must be [rows, {w.k}]")
-    return mx_matmul(quantize_mx(x, bits), w, out_dtype, out)
+    ldx = _matrix("x", x, None, w.k)
+    rows, k = x.shape
+    dtype = out_dtype or (x.dtype if out is None else out.dtype)
+    out_code = _result_code(dtype)
+    out, ldc, fresh = _out(out, rows, w.rows, dtype, dev)
+    p = _lib.GemmMx(rows, w.rows, k, bits, w.bits, out_code, ldc)
+    ws_bytes = _lib.gemm_mx_workspace_bytes(p)
+    codes, scales = _mx_bytes(rows, k, bits)
+    ws = torch.empty(codes + scales + ws_bytes, dtype=torch.uint8, device=dev)  # each part a multiple of 16 bytes long
+    at = ws.data_ptr()
+    _enqueue(dev, "mx_quantize", x.data_ptr(), code, rows, k, ldx, bits, at, at + codes)
+    _enqueue(dev, "gemm_mx_run", p, at, at + codes, w.codes_ptr, w.scales_ptr, out.data_ptr(), at + codes + scales, ws_bytes)
+    if not fresh:
+        increment_version(out)
+    return out
 
 
 # ------------------------------------------------------------------------------- norm
@@ -314,8 +359,8 @@ def rms_norm_mx(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float 
     _no_grad("rms_norm_mx", x, weight, residual, residual_out)
     p, weight, h, h_fresh = _norm_args(x, weight, residual, eps, residual_out)
     q = _new_mx(p.rows, p.n, bits, x.dtype, x.device)
-    _enqueue(x.device, "norm_rms_mx_run", p, bits, x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(h), q.codes.data_ptr(),
-             q.scales.data_ptr())
+    _enqueue(x.device, "norm_rms_mx_run", p, bits, x.data_ptr(), _ptr(residual), _ptr(weight), _ptr(h), q.codes_ptr,
+             q.scales_ptr)
     if not h_fresh:
         increment_version(h)
     return q if residual is None else (q, h)

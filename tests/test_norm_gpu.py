@@ -112,6 +112,26 @@ def test_gradients(rows, n, dtype, wtype):
             within(dw, rw, tw)
 
 
+@pytest.mark.parametrize("rows,n", [(9001, 33), (3500, 1001), (1300, 9001), (700, 17001), (530, 39936), (600, 39937)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_rows(rows, n, dtype):
+    """Several rows to a workgroup: what is kept from row to row, and the sums over rows, of rows of every length."""
+    h, dy, dh, w = rand((rows, n), dtype, 3), rand((rows, n), dtype, 4), rand((rows, n), dtype, 5), weights(n, F32, 6)
+    dx, dw = spt.rms_norm_grad(dy, h, w, 1e-5, dh=dh)
+    rx, tx, rw, tw = grad_reference(dy, h, w, 1e-5, dh)
+    within(dx, rx, tx)
+    within(dw, rw, tw)
+    del dx, rx, tx
+    y, s = spt.rms_norm(dy, w, 1e-5, residual=dh)
+    check_y(y, s, w, 1e-5)
+    # each row's result is its own: rows in another order and number give the same bits
+    pick = torch.arange(rows - 1, -1, -3, device="cuda")
+    assert torch.equal(spt.rms_norm(dy[pick], w, 1e-5, residual=dh[pick])[0], y[pick])
+    q = spt.rms_norm_mx(s, w, 1e-5, bits=8)
+    few = spt.rms_norm_mx(s[pick], w, 1e-5, bits=8)
+    assert torch.equal(spt.dequantize_mx(q, dtype)[pick], spt.dequantize_mx(few, dtype))
+
+
 def test_gradients_against_differences():
     """Central differences in 64 bits of the definition against the kernel's fp32 gradients: with steps of 2^-10 the cubic term
     of a function of unit scale is below 2^-18."""
