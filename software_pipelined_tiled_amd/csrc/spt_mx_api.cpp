@@ -95,7 +95,7 @@ void mx_choose(const gemm_mx_t* p, MxShape* s) {
     for (int sp : parts) {
       const int64_t units = tm * tn * sp, per = ceil_div(kt, sp);
       if (sp > 1 && (skinny || units > 4 * kCus || kt < 2 * sp)) break;
-      if (pp && per < 2) break;
+      if (pp && (kt < 2 || kt - (kt - 1) / per * per < 2)) continue;  // its pipeline has at least two K-tiles, those of the last part too
       double work;
       if (skinny) work = c.solo[f] * (double)ceil_div(ksteps, 8);
       else if (pp) work = (double)ceil_div(units, kCus) * (c.pair[f] * (double)(per * e.ksteps) + c.tile[f]);

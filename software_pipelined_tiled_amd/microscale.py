@@ -330,6 +330,7 @@ class _Norm(torch.autograd.Function):
         want_x, want_w, _, want_r = ctx.needs_input_grad
         if dy is None:  # y was not used: what reached h passes on
             return dh if want_x else None, None, None, dh if want_r else None
+        _wants_grad(dy, dh)  # refuses tangents
         dx, dw = _norm_grad(_rows_apart(dy), h, weight, ctx.eps, None if dh is None else _rows_apart(dh), want_x or want_r,
                             want_w)
         return dx if want_x else None, dw, None, dx if want_r else None

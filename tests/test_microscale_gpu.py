@@ -259,6 +259,22 @@ def test_matmul_exact(m, n, k, fa, fb):
         assert torch.equal(spt.mx_matmul(a, b, out), ref.to(F32).to(out)), out
 
 
+# By format and type these take, between them, every kernel with its sum whole and in parts, parts whose last one is a single step, more
+# tiles than compute units, and 4-bit rows that end in half of a step. Sums stay below 2^24 units of 2^-2.
+@pytest.mark.parametrize("fa,fb", FORMATS)
+@pytest.mark.parametrize("m,n,k", [(4668, 4694, 288), (2, 26, 7190), (605, 308, 21172), (1, 20, 161), (4447, 390, 214), (5874, 153, 8434),
+                                   (582, 3899, 2602), (1398, 403, 33096), (1, 25, 1074), (20, 22, 419), (562, 577, 30747),
+                                   (1, 21, 10692), (2461, 1707, 462), (1140, 3736, 16071), (5005, 971, 15845), (129, 5531, 20453)])
+def test_matmul_every_kernel(m, n, k, fa, fb):
+    a, b = int_operand(m, k, fa, m + k, spread=1), int_operand(n, k, fb, n + k + 1, spread=1)
+    ref, _ = reference(a, b)
+    for out in (F32, BF16, F16):
+        buf = torch.full((m, n + 8), 7.0, dtype=out, device="cuda")  # what lies beside the result stays as it is
+        spt.mx_matmul(a, b, out=buf[:, :n])
+        assert torch.equal(buf[:, :n], ref.to(F32).to(out)), out
+        assert (buf[:, n:] == 7.0).all()
+
+
 def close(got, ref, total, k, dtype, fa):
     u = torch.finfo(dtype).eps / 2
     err = (k * 2.0**-23 + (2.0**-9 if fa == 8 and dtype != F32 else 0.0)) * total
