@@ -8,6 +8,7 @@ namespace spt {
 // ------------------------------------------------------------------------------ layout
 constexpr int kMxBlock = 32;      // values that share a scale
 constexpr int kMxScaleRows = 64;  // rows whose scales of one block lie together
+constexpr int kMxUnitRows = 16;  // rows that a workgroup of the streams takes
 
 SPT_HD int64_t mx_blocks(int64_t k) { return (k + 127) / 128 * 4; }  // of a row, with those behind k
 SPT_HD int64_t mx_row_bytes(int64_t k, int bits) { return mx_blocks(k) * (4 * bits); }
@@ -22,7 +23,7 @@ struct MxQuantArgs {
   unsigned char* scales;
   int64_t rows, ldx;
   int k, blocks;        // blocks of a row
-  int64_t units;        // 64 rows by 512 columns
+  int64_t units;        // of 16 rows by 512 columns
 };
 struct MxValuesArgs {
   const unsigned char* codes;

@@ -1,81 +1,83 @@
 // Microscaled tensors: quantisation, the values back, and the layout of a checkpoint's codes and scales.
 //
-// All three are streams: 2 (4) bytes read and 0.53 or 1.03 written per value, or the reverse. A unit is 64 rows by 512
+// All three are streams: 2 (4) bytes read and 0.53 or 1.03 written per value, or the reverse. A unit is 16 rows by 512
 // columns of one workgroup: a wave takes rows w, w + 4, .., a lane eight neighbouring values (16 bytes of fp16 or bf16),
 // four lanes a block of 32, so a row's piece is one 1 KiB load and its largest magnitudes two DPP steps. The scales of
-// 64 rows by 16 blocks lie together in memory and are collected in LDS, so that they leave in one piece of 1 KiB: written
+// 16 rows of a block lie together in memory and are collected in LDS, so that they leave 16 bytes at a time: written
 // row by row each would be a byte in a line of its own.
+//   8192 x 8192 bf16 to 4 bits: 28.9 us (32.5 at the rate of a large copy; part of it stays in the last cache), 28672 x 8192 to 8 bits
+// 119 (137), 301 x 8190 fp32 to 8 bits 5.0 (2.4); units of 64 rows, whose scales leave in whole lines, took 34.8, 143 and 9.6. The
+// values of the same 8192 x 8192: 32.5, with 64 rows 31.1, but 115 against 118 at 28672 rows and 5.1 against 9.8 at 1024 x 4096.
 #include "spt_mx_device.h"
 
 namespace spt {
 
 constexpr int kUnitCols = 512;  // 16 blocks
+constexpr int kScaleBytes = 16 * kMxUnitRows;  // of a unit
 
-// Copies the unit's 16 x 64 scale bytes out of LDS.
-__device__ __forceinline__ void put_scales(const unsigned* sc, unsigned char* scales, int64_t rb, int cg, int blocks) {
-  const int first = cg * 16, count = blocks - first < 16 ? blocks - first : 16;
-  unsigned* dst = (unsigned*)(scales + (rb * blocks + first) * kMxScaleRows);
-  if ((int)threadIdx.x < count * 16) dst[threadIdx.x] = sc[threadIdx.x];
+// Word t of a unit's scales, 16 blocks of 16 rows: its place in the tensor, and whether the row has the block.
+__device__ __forceinline__ int64_t scale_word(int64_t row0, int cg, int blocks, int t) {
+  return (row0 / kMxScaleRows * blocks + cg * 16 + t / 4) * (kMxScaleRows / 4) + row0 % kMxScaleRows / 4 + t % 4;
+}
+__device__ __forceinline__ bool has_scale_word(int cg, int blocks, int t) { return t < kScaleBytes / 4 && t < (blocks - cg * 16) * 4; }
+__device__ __forceinline__ void put_scales(const unsigned* sc, unsigned char* scales, int64_t row0, int cg, int blocks) {
+  if (has_scale_word(cg, blocks, threadIdx.x)) ((unsigned*)scales)[scale_word(row0, cg, blocks, threadIdx.x)] = sc[threadIdx.x];
 }
 
 template <int T, int BITS>
 __global__ void __launch_bounds__(256) mx_quantize_kernel(MxQuantArgs a) {
-  __shared__ __attribute__((aligned(16))) unsigned char sc[16 * kMxScaleRows];
+  __shared__ __attribute__((aligned(16))) unsigned char sc[kScaleBytes];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int groups = (a.blocks + 15) / 16;
   const int64_t row_bytes = (int64_t)a.blocks * (4 * BITS);
   for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
     const int64_t rb = u / groups;
     const int cg = (int)(u - rb * groups);
-    const int64_t row0 = rb * kMxScaleRows;
-    const int rows = a.rows - row0 < kMxScaleRows ? (int)(a.rows - row0) : kMxScaleRows;
+    const int64_t row0 = rb * kMxUnitRows;
+    const int rows = a.rows - row0 >= kMxUnitRows ? kMxUnitRows : a.rows > row0 ? (int)(a.rows - row0) : 0;
     const int col = cg * kUnitCols + lane * 8;
     const bool held = col < a.blocks * kMxBlock;  // the row's padding is written too
-    if (rows < kMxScaleRows) {                     // rows behind the last: zeros
-      ((unsigned*)sc)[threadIdx.x] = 0;
+    if (rows < kMxUnitRows) {                      // rows behind the last: zeros
+      if (threadIdx.x < kScaleBytes / 4) ((unsigned*)sc)[threadIdx.x] = 0;
       __syncthreads();
     }
-    for (int base = wave; base < rows; base += 16) {  // four rows' loads before the first is used
-      float v[4][8];
+    float v[4][8];  // the wave's four rows
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = base + 4 * j;
-        load8<T>(a.x + ((row0 + i) * a.ldx + col) * kTypeSize[T], i < rows ? a.k - col : 0, v[j]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int i = wave + 4 * j;
+      load8<T>(a.x + ((row0 + i) * a.ldx + col) * kTypeSize[T], i < rows ? a.k - col : 0, v[j]);
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = base + 4 * j;
-        if (i >= rows) break;
-        const unsigned s = mx_scale_of<BITS>(v[j]);
-        const u32x2 q = mx_codes<BITS>(v[j], s);
-        if (held) {
-          unsigned char* p = a.codes + (row0 + i) * row_bytes + (int64_t)col * BITS / 8;
-          if constexpr (BITS == 8) *(u32x2*)p = q;
-          else *(unsigned*)p = q[0];
-        }
-        if ((lane & 3) == 0) sc[(lane >> 2) * kMxScaleRows + i] = (unsigned char)s;
+    for (int j = 0; j < 4; ++j) {
+      const int i = wave + 4 * j;
+      if (i >= rows) break;
+      const unsigned s = mx_scale_of<BITS>(v[j]);
+      const u32x2 q = mx_codes<BITS>(v[j], s);
+      if (held) {
+        unsigned char* p = a.codes + (row0 + i) * row_bytes + (int64_t)col * BITS / 8;
+        if constexpr (BITS == 8) *(u32x2*)p = q;
+        else *(unsigned*)p = q[0];
       }
+      if ((lane & 3) == 0) sc[(lane >> 2) * kMxUnitRows + i] = (unsigned char)s;
     }
     __syncthreads();
-    put_scales((const unsigned*)sc, a.scales, rb, cg, a.blocks);
+    put_scales((const unsigned*)sc, a.scales, row0, cg, a.blocks);
     __syncthreads();
   }
 }
 
 template <int T, int BITS>
 __global__ void __launch_bounds__(256) mx_values_kernel(MxValuesArgs a) {
-  __shared__ __attribute__((aligned(16))) unsigned char sc[16 * kMxScaleRows];
+  __shared__ __attribute__((aligned(16))) unsigned char sc[kScaleBytes];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int groups = (a.blocks + 15) / 16;
   const int64_t row_bytes = (int64_t)a.blocks * (4 * BITS);
   for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
     const int64_t rb = u / groups;
     const int cg = (int)(u - rb * groups);
-    const int64_t row0 = rb * kMxScaleRows;
-    const int rows = a.rows - row0 < kMxScaleRows ? (int)(a.rows - row0) : kMxScaleRows;
-    const int first = cg * 16, count = a.blocks - first < 16 ? a.blocks - first : 16;
-    const unsigned* src = (const unsigned*)(a.scales + (rb * a.blocks + first) * kMxScaleRows);
-    if ((int)threadIdx.x < count * 16) ((unsigned*)sc)[threadIdx.x] = src[threadIdx.x];
+    const int64_t row0 = rb * kMxUnitRows;
+    const int rows = a.rows - row0 >= kMxUnitRows ? kMxUnitRows : a.rows > row0 ? (int)(a.rows - row0) : 0;
+    if (has_scale_word(cg, a.blocks, threadIdx.x)) ((unsigned*)sc)[threadIdx.x] = ((const unsigned*)a.scales)[scale_word(row0, cg, a.blocks, threadIdx.x)];
     __syncthreads();
     const int col = cg * kUnitCols + lane * 8;
     if (col < a.k) {
@@ -86,7 +88,7 @@ __global__ void __launch_bounds__(256) mx_values_kernel(MxValuesArgs a) {
         if constexpr (BITS == 8) q = *(const u32x2*)p;
         else q[0] = *(const unsigned*)p;
         float v[8];
-        mx_values<BITS>(q, sc[(lane >> 2) * kMxScaleRows + i], v);
+        mx_values<BITS>(q, sc[(lane >> 2) * kMxUnitRows + i], v);
         put8<T>(a.out + ((row0 + i) * a.ldo + col) * kTypeSize[T], a.k - col, v);
       }
     }
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(256) mx_values_kernel(MxValuesArgs a) {
 
 // Once per weight: byte loads, so that a checkpoint's rows may begin anywhere.
 __global__ void __launch_bounds__(256) mx_pack_kernel(MxPackArgs a) {
-  __shared__ __attribute__((aligned(16))) unsigned char sc[16 * kMxScaleRows];
+  __shared__ __attribute__((aligned(16))) unsigned char sc[kScaleBytes];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int groups = (a.blocks + 15) / 16;
   const int row_bytes = a.blocks * 4 * a.bits;
@@ -105,8 +107,8 @@ __global__ void __launch_bounds__(256) mx_pack_kernel(MxPackArgs a) {
   for (int64_t u = blockIdx.x; u < a.units; u += gridDim.x) {
     const int64_t rb = u / groups;
     const int cg = (int)(u - rb * groups);
-    const int64_t row0 = rb * kMxScaleRows;
-    const int rows = a.rows - row0 < kMxScaleRows ? (int)(a.rows - row0) : kMxScaleRows;
+    const int64_t row0 = rb * kMxUnitRows;
+    const int rows = a.rows - row0 >= kMxUnitRows ? kMxUnitRows : a.rows > row0 ? (int)(a.rows - row0) : 0;
     const int at = (cg * kUnitCols + lane * 8) * a.bits / 8;  // the lane's 4 or 8 bytes
     for (int i = wave; i < rows; i += 4) {
       const unsigned char* p = a.codes + (row0 + i) * a.ldc;
@@ -123,12 +125,10 @@ __global__ void __launch_bounds__(256) mx_pack_kernel(MxPackArgs a) {
         if (a.bits == 8) o[1] = q[1];
       }
     }
-    for (int t = threadIdx.x; t < 16 * kMxScaleRows; t += 256) {
-      const int i = t >> 4, b = cg * 16 + (t & 15);
-      sc[(t & 15) * kMxScaleRows + i] = i < rows && b < plain ? a.scales[(row0 + i) * a.lds + b] : 0;
-    }
+    const int i = threadIdx.x >> 4, b = cg * 16 + (threadIdx.x & 15);  // a scale of each thread's
+    sc[(threadIdx.x & 15) * kMxUnitRows + i] = i < rows && b < plain ? a.scales[(row0 + i) * a.lds + b] : 0;
     __syncthreads();
-    put_scales((const unsigned*)sc, a.out_scales, rb, cg, a.blocks);
+    put_scales((const unsigned*)sc, a.out_scales, row0, cg, a.blocks);
     __syncthreads();
   }
 }

@@ -24,14 +24,15 @@ gemm_status_t check_mx(int64_t rows, int64_t k, int bits) {
   return GEMM_OK;
 }
 
-// Units of 64 rows by 512 columns, and the workgroups that walk over them.
+// Units of 16 rows by 512 columns, and the workgroups that walk over them. The last 64 rows have all theirs: rows behind the last
+// one have scales, zeros.
 struct Units {
   int64_t units;
   unsigned grid;
 };
 Units mx_units(int64_t rows, int64_t blocks) {
   Units u;
-  u.units = ceil_div(rows, kMxScaleRows) * ceil_div(blocks, 16);
+  u.units = round_up(rows, kMxScaleRows) / kMxUnitRows * ceil_div(blocks, 16);
   u.grid = (unsigned)(u.units < 65536 ? u.units : 65536);
   return u;
 }

@@ -140,7 +140,7 @@ def _out(out, rows: int, cols: int, dtype, device) -> tuple[torch.Tensor, int, b
     """The output, its row stride, and whether it is new (then the rows nobody computes are zeroed). One that is not
     new was written behind torch's back, which ``increment_version`` tells autograd: it may have been saved."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols, True
+        return torch.empty(rows, cols, dtype=dtype, device=device), cols, True
     if out.device != device:
         raise ValueError(f"out is on {out.device}, the operands on {device}")
     if out.dtype != dtype:

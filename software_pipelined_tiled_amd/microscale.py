@@ -282,7 +282,7 @@ def _norm_grad(dy, h, weight, eps, dh, want_dx=True, want_dw=True):
     lddy = _matrix("dy", dy, rows, n)
     lddh = _matrix("dh", dh, rows, n) if dh is not None else 0
     weight, wcode = _norm_weight(weight, h)
-    dx = torch.empty((rows, n), dtype=h.dtype, device=h.device) if want_dx else None
+    dx = torch.empty(rows, n, dtype=h.dtype, device=h.device) if want_dx else None
     dw = torch.empty(n, dtype=weight.dtype, device=h.device) if want_dw and weight is not None else None
     p = _lib.NormRmsGrad(rows, n, code, wcode, _eps(eps), lddy, ldh, lddh, n)
     ws_bytes = _lib.norm_rms_grad_workspace_bytes(p, dw is not None)
