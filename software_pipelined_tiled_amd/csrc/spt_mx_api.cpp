@@ -161,7 +161,7 @@ NormShape norm_shape(int64_t rows, int64_t n, gemm_dtype_t dtype, bool mx, bool 
     s.threads = s.c > 0 ? (int)round_up(ceil_div(pieces, s.c), 64) : s.c < 0 ? 1024 : 512;
     if (s.c == -2) s.lds = (int)pieces * 32;
     s.lanes = s.threads;
-    per_cu = s.threads > 512 ? 1 : (grad ? 1280 : 1536) / s.threads;
+    per_cu = (grad ? 1280 : 1536) / s.threads;
   }
   const int64_t together = s.c == -1 ? s.threads / s.lanes : 1;  // rows of a workgroup at once
   const int64_t fit = kCus * per_cu;
