@@ -252,6 +252,23 @@ def check_near(q, h, w, eps):
         assert not q.scales[-1, :, rows % 64:].any()
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("rows,n", [(13001, 1001), (12290, 4096), (2603, 9001), (1030, 8192), (2570, 17001), (5001, 600)])
+def test_mx_of_many_rows(rows, n, bits):
+    """Codes and scales of workgroups with several rows, from any row of four on, are those of few rows at a time, the zeros behind the
+    last row too."""
+    x, w = rand((rows, n), BF16, 1), weights(n, BF16, 2)
+    q = spt.rms_norm_mx(x, w, bits=bits)
+    for at in range(0, rows, 64 * 41):
+        part = spt.rms_norm_mx(x[at: at + 128], w, bits=bits)
+        blocks = part.scales.shape[0]
+        assert torch.equal(q.codes[at: at + 128], part.codes)
+        assert torch.equal(q.scales[at // 64: at // 64 + blocks], part.scales)
+    at = rows // 64 * 64 - 64
+    part = spt.rms_norm_mx(x[at:], w, bits=bits)
+    assert torch.equal(q.scales[at // 64:], part.scales) and (part.scales[-1, :, (rows - 1) % 64 + 1:] == 0).all()
+
+
 def test_mx_feeds_the_product():
     """A layer: norm in 8 bits, product with a 4-bit weight; against the norm in fp32 quantised by itself."""
     x, r, w = rand((50, 1000), F32, 1), rand((50, 1000), F32, 2), weights(1000, F32, 3)
