@@ -61,8 +61,9 @@ MxEntry mx_entry(MxKernel kernel, const gemm_mx_t* p, bool exact, bool planes) {
 
 // The kernel and the parts of a sum: the least time by this model, in us. A start; the longer of the workgroups' rounds over the
 // compute units (k-steps times what one takes, and the tile's own start and end) and the bytes; and, with parts, the second pass
-// over their planes. Tiles run two to a compute unit, and a workgroup alone on its own takes its k-steps faster. The constants are
-// a fit to 3300 measured shapes (1 .. 16384 rows, N 64 .. 28672, K 100 .. 14336); on 1800 of them the choice takes 2.8 % longer
+// over their planes. Tiles run two to a compute unit, and a workgroup alone on its own takes its k-steps faster. A workgroup draws only
+// so many bytes at once, so that fewer than 170 tiles do not fill the memory (1 x 8192 x 8192, 8 x 8: 16.9 us in four parts of 64 tiles,
+// 23.6 in two). The constants are a fit to 3400 measured shapes (1 .. 16384 rows, N 64 .. 28672, K 100 .. 14336); on 1800 of them the choice takes 2.3 % longer
 // than the best kernel of each shape, 82 % at worst (1386 x 11469 x 650, 4 x 4 in fp32: 34 us against 18), where rules on the
 // numbers of rows and tiles took 25 %.
 void mx_choose(const gemm_mx_t* p, MxShape* s) {
@@ -102,8 +103,9 @@ void mx_choose(const gemm_mx_t* p, MxShape* s) {
       else if (pp) work = (double)ceil_div(units, kCus) * (c.pair[f] * (double)(per * e.ksteps) + c.tile[f]);
       else work = (units <= kCus ? c.solo[f] : (double)ceil_div(units, 2 * kCus) * c.pair[f]) * (double)(per * e.ksteps);
       const double out = sp > 1 ? plane * sp : plane * (p->out_dtype == GEMM_F32 ? 1 : .5);
-      const double bytes = .2 * operands + c.out * out;
-      const double us = c.start + (work > bytes ? work : bytes) + (sp > 1 ? 3.2 + .45 * out : 0);
+      const double drawn = skinny ? .2 : pp || units > 166 ? .18 : 30. / (double)units;  // us for a megabyte
+      const double bytes = drawn * operands + c.out * out;
+      const double us = c.start + (work > bytes ? work : bytes) + (sp > 1 ? 2.7 + .4 * out : 0);
       if (any && us >= least) continue;
       any = true;
       least = us;
