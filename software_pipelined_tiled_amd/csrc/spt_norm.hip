@@ -8,14 +8,15 @@
 // A workgroup has a row at a time, and takes several neighbouring rows, the next one's loads in flight while it adds up the
 // squares; rows of up to 512 values are a wave's or a part of one, several to a workgroup (30000 rows of 200: 9.8 us, 26 with a
 // wave to a row). Weights stay in registers from row to row where rows are short enough, and else come from the L2. With the
-// residual, at the rate of a large copy (5.16 TB/s) in brackets: 8191 rows of 8192 fp16 105 us (104), as 8-bit MX 98 (92), 2000
-// rows of 28672 bf16 106 (89), 1003 rows of 4097 fp32 12.7 (12.8: part of it stays in the last cache).
+// residual, at the rate of a large copy (5.16 TB/s) in brackets: 8191 rows of 8192 fp16 104 us (104), as 8-bit MX 97 (92), 2000
+// rows of 28672 bf16 101 (89; 105 without the loads ahead), as MX 106 (78: its registers have no room for them), 1003 rows of 4097
+// fp32 13.0 (12.8: part of it stays in the last cache), 1000 rows of 38400 fp16 in two passes 73 (60).
 //
 // Gradients: sum h^2 and sum g h come out of one pass, so that r need not be kept by the forward. dweight's sums run
 // over a workgroup's rows in registers, for rows of more than 16384 values in LDS, and in its plane in memory for those that the
 // LDS does not hold either; they leave as one fp32 plane a workgroup, and are added in the planes' order by a second
-// kernel: no atomics, the same bits on every run. With dh: 8191 rows of 8192 fp16 116 us (104), 2000 of 28672 bf16 141 (89; 185
-// with the sums in registers, which did not fit), 1000 of 40960 fp16 186 (64), 300 rows of 4096 10 (1.9: two launches).
+// kernel: no atomics, the same bits on every run. With dh: 8191 rows of 8192 fp16 116 us (104), 8192 of 4096 bf16 60 (52), 2000 of
+// 28672 bf16 138 (89; 185 with the sums in registers, which did not fit), 300 rows of 4096 10 (1.9: two launches).
 #include "spt_mx_device.h"
 
 namespace spt {
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_kernel(NormArgs a) {
 
   int turn = 0;
   if constexpr (P > 0) {
-    constexpr bool AHEAD = P <= 2;  // the next row's loads before this row's sum
+    constexpr bool AHEAD = P <= 2 || OUT == 0;  // the next row's loads before this row's sum (the MX form of four pieces has no registers for it)
     Raw8<T> x[KEEP], r[KEEP];
     auto fetch = [&](int64_t row) SPT_INLINE {
 #pragma unroll
@@ -191,8 +192,13 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_kernel(NormArgs a) {
       float sum[1] = {0.f};
       for (int p = threadIdx.x; p * 8 < n; p += lanes) {
         const int col = p * 8;
-        const Raw8<T> x = load_raw<T>(a.x + row * a.ldx * ES + (unsigned)(col * ES), n - col);
-        square(sum_of(row, col, x, a.r ? load_raw<T>(a.r + row * a.ldr * ES + (unsigned)(col * ES), n - col) : x), sum[0]);
+        Raw8<T> x = load_ahead<T>(a.x + row * a.ldx * ES, col, n), r = x;
+        if (a.r) {
+          r = load_ahead<T>(a.r + row * a.ldr * ES, col, n);
+          settle<T>(r, col, n);
+        }
+        settle<T>(x, col, n);
+        square(sum_of(row, col, x, r), sum[0]);
       }
       row_sum<1, false>(sum, red, turn, lanes);
       const float rstd = 1.f / __builtin_sqrtf(sum[0] * inv_n + a.eps);
@@ -323,9 +329,11 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_grad_kernel(NormGrad
     for (int64_t row = first; row < last; ++row, turn ^= 1) {
       float sum[2] = {0.f, 0.f};
       auto piece = [&](int col, Raw8<T>& u, Raw8<T>& v) SPT_INLINE {
-        u = load_raw<T>(a.dy + row * a.lddy * ES + (unsigned)(col * ES), n - col);
-        v = load_raw<T>(a.h + row * a.ldh * ES + (unsigned)(col * ES), n - col);
+        u = load_ahead<T>(a.dy + row * a.lddy * ES, col, n);
+        v = load_ahead<T>(a.h + row * a.ldh * ES, col, n);
         load_weight(a.w, a.wtype, col, n, w[0]);
+        settle<T>(u, col, n);
+        settle<T>(v, col, n);
       };
       Raw8<T> u, v;
       for (int p = threadIdx.x; p * 8 < n; p += lanes) {
@@ -339,7 +347,12 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_grad_kernel(NormGrad
         const int col = p * 8;
         piece(col, u, v);
         // dx may be dy's own memory: dweight's part is taken from what was read
-        if (a.dx) grad(row, col, u, v, a.dh ? load_raw<T>(a.dh + row * a.lddh * ES + (unsigned)(col * ES), n - col) : u, w[0], rstd, f);
+        Raw8<T> d = u;
+        if (a.dh) {
+          d = load_ahead<T>(a.dh + row * a.lddh * ES, col, n);
+          settle<T>(d, col, n);
+        }
+        if (a.dx) grad(row, col, u, v, d, w[0], rstd, f);
         if (plane) {  // a piece's sums are this thread's alone
           float p8[8], q8[8], s8[8];
           unpack<T>(u, p8);
