@@ -58,7 +58,7 @@ struct MxGemmArgs {
   int group_m;
   int units;            // output tiles times parts of the sum
   int splits;
-  int per;              // K-tiles (k-steps of the skinny kernel) of one part
+  int per;              // K-tiles of one part (the skinny kernel has one)
   int64_t plane;        // elements between planes
   int grid;
   int nt;               // non-temporal stores

@@ -1,10 +1,11 @@
 // Products of microscaled operands with few rows: what bounds them is reading B once.
 //
-// A workgroup has up to 16 MT rows and 16 NF columns, and its eight waves share out k: each streams its k-steps of B (and
-// of A, which lies in the L2) from memory to registers in the matrix instruction's own order, with no LDS on the way,
-// several k-steps of it in flight. The waves' sums meet in LDS once at the end. Row r of fragment f is operand row
-// NF r + f (MT r + f): a lane's NF scale bytes are neighbours, one load that the instruction's operand select takes apart,
-// and its results NF neighbouring columns.
+// A workgroup has up to 16 MT rows and 16 NF columns (NF = 1: over 172 shapes 32 columns took 21 % longer and 64 50 %, for
+// want of workgroups), and its eight waves share out k: each streams its k-steps of B (and of A, which lies in the L2) from
+// memory to registers in the matrix instruction's own order, with no LDS on the way, several k-steps of it in flight. The
+// waves' sums meet in LDS once at the end. Row r of fragment f is operand row MT r + f: a lane's MT scale bytes are
+// neighbours, one load that the instruction's operand select takes apart. 32 rows of 4096 x 4096 8 x 4: 8.8 us, the tile kernel in
+// four parts 9.2; where there are more columns than compute units have workgroups, it loses (6144 x 4096: 15.8 against 9.9).
 //   B goes by with the non-temporal hint: nobody reads it again.
 #include "spt_mx_device.h"
 
@@ -29,8 +30,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) mx_skinny_kernel(MxGemmArgs
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
-  const int nb = blockIdx.x / args.splits, part = blockIdx.x - nb * args.splits;
-  const int col0 = nb * (16 * NF);
+  const int col0 = blockIdx.x * (16 * NF);
   const int lda = args.blocks * (4 * FA), ldb = args.blocks * (4 * FB);
   const __amdgpu_buffer_rsrc_t ra = make_rsrc(args.a, (uint64_t)args.m * lda);
   const __amdgpu_buffer_rsrc_t rb = make_rsrc(args.b + (int64_t)col0 * ldb, (uint64_t)(args.n - col0) * ldb);
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) mx_skinny_kernel(MxGemmArgs
     u32x4 a[MT][FA / 4], b[NF][FB / 4];
     unsigned sa, sb;
   };
-  const int ks0 = part * args.per, ks1 = ks0 + args.per < args.ksteps ? ks0 + args.per : args.ksteps;
+  const int ks1 = args.ksteps;
   auto load = [&](Piece& p, int ks) SPT_INLINE {
     const unsigned past = ks < ks1 ? 0u : kOOB;  // set, it moves an offset beyond the descriptor's end
     const unsigned ka = (unsigned)(ks * (16 * FA)), kb = (unsigned)(ks * (16 * FB)), kc = (unsigned)(ks * 256);
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) mx_skinny_kernel(MxGemmArgs
   // Pieces wave, wave + W, ..: neighbouring waves read neighbouring parts of a row's lines. One past the end reads zeros.
   {
     Piece p[D];
-    int ks = ks0 + wave;
+    int ks = wave;
 #pragma unroll
     for (int d = 0; d < D; ++d) load(p[d], ks + d * W);
     for (; ks < ks1; ks += D * W) {
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(64 * kSkinnyWaves) mx_skinny_kernel(MxGemmArgs
   __syncthreads();
 
   // An item is one lane's NF neighbouring columns of row MT (4 q4 + e) + f, the waves' sums added in their order.
-  char* out = args.c + part * args.plane * 4;
+  char* out = args.c;
   for (int t = threadIdx.x; t < MT * 256; t += 64 * W) {
     const int l = t & 63, e = (t >> 6) & 3, f = t >> 8;
     const int row = MT * (4 * (l >> 4) + e) + f, col = col0 + NF * (l & 15);
