@@ -45,6 +45,7 @@ def _no_grad(call: str, *tensors) -> None:
 
 _MX_ROWS, _MX_K = 2**31 - 64, 2**22  # the library's limits
 
+
 class MXTensor:
     """A microscaled tensor [rows, k] (made by ``quantize_mx``, ``pack_mx`` or ``rms_norm_mx``). bits: 8 (e4m3) or 4
     (e2m1). codes [rows, bytes], rows of whole 128 values, and scales [ceil(rows / 64), blocks, 64], the exponents of the
@@ -78,6 +79,9 @@ class MXTensor:
         if self._scales is None:
             self._scales = self._data[self.scales_ptr - self.codes_ptr:].view(_shapes(self.rows, self.k, self.bits)[1])
         return self._scales
+
+    def __reduce__(self):  # a copy's addresses are its own tensors'
+        return MXTensor, (self.codes, self.scales, self.bits, self.rows, self.k, self.dtype)
 
     def __repr__(self) -> str:
         return f"MXTensor({self.rows} x {self.k}, {self.bits} bits, {self.device})"

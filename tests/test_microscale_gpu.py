@@ -8,6 +8,9 @@
   cut what lies 13 bits below the largest of the up to 16 products added at a time: each of those loses less than 2^-13
   of that largest one, so 16 of them less than 16 * 2^-13 of the 16's total magnitude: 2^-9 T.
 """
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -358,6 +361,19 @@ def test_same_bits_every_run(fa, fb):
         first = spt.mx_matmul(a, b, out)
         for _ in range(5):
             assert torch.equal(spt.mx_matmul(a, b, out), first)
+
+
+def test_copies_have_memory_of_their_own():
+    for q in (spt.quantize_mx(wide((70, 300), 1).to(BF16), 4), int_operand(70, 300, 8, 1)):
+        want = spt.dequantize_mx(q, F32)
+        others = [copy.copy(q), copy.deepcopy(q), pickle.loads(pickle.dumps(q))]
+        for other in others[1:]:
+            assert other.codes_ptr != q.codes_ptr and other.codes_ptr == other.codes.data_ptr() and other.scales_ptr == other.scales.data_ptr()
+        q.codes.zero_()
+        assert torch.equal(spt.dequantize_mx(others[0], F32), torch.zeros_like(want))  # a shallow copy shares it
+        for other in others[1:]:
+            assert (other.bits, other.shape, other.dtype) == (q.bits, q.shape, q.dtype)
+            assert torch.equal(spt.dequantize_mx(other, F32), want)
 
 
 def test_streams():

@@ -16,6 +16,7 @@ if not torch.cuda.is_available():  # collected on CPU-only hosts, never run ther
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import software_pipelined_tiled_amd as spt  # noqa: E402
+from software_pipelined_tiled_amd import _lib  # noqa: E402
 from test_microscale_gpu import check_quantized, codes_of, gen, scale_bytes, values  # noqa: E402
 
 F16, BF16, F32, F64 = torch.float16, torch.bfloat16, torch.float32, torch.float64
@@ -186,7 +187,7 @@ def test_strides(dtype, extra, offset):
         assert torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales)
 
 
-@pytest.mark.parametrize("n", [100, 4096, 40000])
+@pytest.mark.parametrize("n", [1, 7, 100, 201, 4096, 8191, 20531, 40000, 40003])
 def test_in_place(n):
     """The residual's stream kept in one tensor, as a decoding loop does."""
     x, r, w = rand((5, n), BF16, 1), rand((5, n), BF16, 2), weights(n, BF16, 3)
@@ -206,6 +207,23 @@ def test_in_place(n):
     q, h1 = spt.rms_norm_mx(x, w, residual=keep, residual_out=keep)
     p, _ = spt.rms_norm_mx(x, w, residual=r)
     assert torch.equal(keep, h) and torch.equal(p.codes, q.codes) and torch.equal(p.scales, q.scales)
+
+
+@pytest.mark.parametrize("n", [3, 201, 1001, 9001, 20531, 40003])
+@pytest.mark.parametrize("over", ["dy", "dh"])
+def test_gradient_over_its_operand(n, over):
+    """dx in dy's or dh's own memory, as the C interface allows."""
+    rows = 300
+    h, w = rand((rows, n), BF16, 1), weights(n, F32, 2)
+    t = {"dy": rand((rows, n), BF16, 3), "dh": rand((rows, n), BF16, 4)}
+    want_dx, want_dw = spt.rms_norm_grad(t["dy"], h, w, 1e-6, dh=t["dh"])
+    dw = torch.empty_like(w)
+    p = _lib.NormRmsGrad(rows, n, spt.GEMM_BF16, spt.GEMM_F32, 1e-6, n, n, n, n)
+    size = _lib.norm_rms_grad_workspace_bytes(p, True)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    assert spt.lib().norm_rms_grad_run(p, t["dy"].data_ptr(), h.data_ptr(), w.data_ptr(), t["dh"].data_ptr(), t[over].data_ptr(),
+                                       dw.data_ptr(), ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(t[over], want_dx) and torch.equal(dw, want_dw)
 
 
 @pytest.mark.parametrize("bits", [4, 8])
