@@ -100,7 +100,8 @@ const void* mx_quantize_fn(int dtype, int bits);
 const void* mx_values_fn(int dtype, int bits);
 const void* mx_pack_fn();
 // out: 0 the input's type, else bits; c: pieces of eight values to a thread (1, 2, and the 16-bit norms 4; up to 1024 threads), -1:
-// rows of `lanes` threads of 256, 0: rows of any length, 512 threads, -2: gradients with 32 bytes of LDS to a piece, 1024 threads
+// rows of `lanes` threads of 256, 0: rows of any length, 512 threads, -2: gradients with 32 bytes of LDS to a piece, 1024 threads, -3:
+// gradients with rows of `lanes` threads, whole waves, side by side
 const void* norm_fn(int dtype, int out, int c);
 const void* norm_grad_fn(int dtype, int c);
 const void* norm_parts_fn();

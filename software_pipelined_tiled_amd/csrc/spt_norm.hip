@@ -15,7 +15,8 @@
 // Gradients: sum h^2 and sum g h come out of one pass, so that r need not be kept by the forward. dweight's sums run
 // over a workgroup's rows in registers, for rows of more than 16384 values in LDS, and in its plane in memory for those that the
 // LDS does not hold either; they leave as one fp32 plane a workgroup, and are added in the planes' order by a second
-// kernel: no atomics, the same bits on every run. With dh: 8191 rows of 8192 fp16 116 us (104), 8192 of 4096 bf16 60 (52), 2000 of
+// kernel: no atomics, the same bits on every run. A workgroup has eight rows or more, so that the planes are few, with few rows side
+// by side. With dh: 8191 rows of 8192 fp16 116 us (104), 8192 of 4096 bf16 60 (52), 2000 of
 // 28672 bf16 138 (89; 185 with the sums in registers, which did not fit), 300 rows of 4096 10 (1.9: two launches).
 #include "spt_mx_device.h"
 
@@ -23,11 +24,12 @@ namespace spt {
 
 constexpr int kShort = -1;  // C of rows that a part of a wave holds
 constexpr int kLds = -2;    // gradients: C of long rows with dweight's sums in LDS
+constexpr int kSide = -3;   // gradients: C of rows of several waves, with several of them side by side in a workgroup
 
 // The sum of N values over the `lanes` threads of a row (a power of two up to 64, or all the workgroup's), to all of them, in a fixed
-// order. `red` holds two sets of N x 16 floats used in turn (`turn`), so that one barrier a call is enough.
+// order. `red` holds two sets of N x 16 floats used in turn (`turn`), so that one barrier a call is enough. `wave0`: the row's first wave.
 template <int N, bool SHORT>
-__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int turn, int lanes) {
+__device__ __forceinline__ void row_sum(float (&v)[N], float* red, int turn, int lanes, int wave0 = 0) {
   if constexpr (SHORT) {
     for (int d = lanes >> 1; d >= 1; d >>= 1) {
 #pragma unroll
@@ -35,13 +37,13 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int turn, int
     }
   } else {
     float* r = red + turn * N * 16;
-    const int waves = blockDim.x >> 6;
+    const int waves = lanes >> 6;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
 #pragma unroll
       for (int d = 32; d >= 1; d >>= 1) v[i] += __shfl_xor(v[i], d);
     }
-    if (waves == 1) return;
+    if (blockDim.x == 64) return;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) r[i * 16 + (threadIdx.x >> 6)] = v[i];
@@ -50,7 +52,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int turn, int
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float t = 0.f;
-      for (int w = 0; w < waves; ++w) t += r[i * 16 + w];
+      for (int w = 0; w < waves; ++w) t += r[i * 16 + wave0 + w];
       v[i] = t;
     }
   }
@@ -214,16 +216,18 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_kernel(NormArgs a) {
   }
 }
 
-// C as above, and kLds.
+// C as above, kLds and kSide.
 template <int T, int C>
 __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_grad_kernel(NormGradArgs a) {
   __shared__ float red[2 * 2 * 16];
-  constexpr bool SHORT = C == kShort;
-  constexpr int ES = kTypeSize[T], P = SHORT ? 1 : C == kLds ? 0 : C, KEEP = P ? P : 1;
+  constexpr bool SHORT = C == kShort, SIDE = C == kSide, SEVERAL = SHORT || SIDE;
+  constexpr int ES = kTypeSize[T], P = SEVERAL ? 1 : C == kLds ? 0 : C, KEEP = P ? P : 1;
   constexpr bool W_KEPT = P == 1;
-  const int n = a.n, lanes = SHORT ? a.lanes : blockDim.x, at = threadIdx.x & (SHORT ? lanes - 1 : 1023);
-  const int step = SHORT ? blockDim.x / lanes : 1;
-  const int64_t first = (int64_t)blockIdx.x * a.per + (SHORT ? threadIdx.x / lanes : 0);
+  const int n = a.n, lanes = SEVERAL ? a.lanes : blockDim.x;
+  const int place = SHORT ? threadIdx.x / lanes : SIDE ? __builtin_amdgcn_readfirstlane(threadIdx.x / lanes) : 0;  // among the rows side by side
+  const int at = threadIdx.x - place * lanes;
+  const int step = SEVERAL ? blockDim.x / lanes : 1;
+  const int64_t first = (int64_t)blockIdx.x * a.per + place;
   const int64_t last = ((int64_t)blockIdx.x + 1) * a.per < a.rows ? ((int64_t)blockIdx.x + 1) * a.per : a.rows;
   const float inv_n = 1.f / (float)n;
   float* plane = a.parts ? a.parts + (int64_t)blockIdx.x * n : nullptr;
@@ -271,7 +275,9 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_grad_kernel(NormGrad
       q = load_ahead<T>(a.h + row * a.ldh * ES, col, n);
     };
     if (AHEAD && first < last) fetch(first, 0, dy[0], h[0]);
-    for (int64_t row = first; row < last; row += step, turn ^= 1) {
+    // rows of several waves side by side meet at barriers: all go on to the workgroup's last row
+    for (int64_t row = first; (SIDE ? row - place : row) < last; row += step, turn ^= 1) {
+      const bool live = !SIDE || row < last;
       float sum[2] = {0.f, 0.f};
       const char* wp = a.w;
       if constexpr (!W_KEPT) asm volatile("" : "+s"(wp));  // loaded for each row: out of the loop they would be kept all the same
@@ -281,6 +287,7 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_grad_kernel(NormGrad
       }
 #pragma unroll
       for (int c = 0; c < P; ++c) {
+        if (!live) break;
         const int col = col_of(c);
         if (a.dh) dh[c] = load_ahead<T>(a.dh + row * a.lddh * ES, col, n);
         settle<T>(dy[c], col, n);
@@ -289,7 +296,8 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_grad_kernel(NormGrad
         add(dy[c], h[c], w[0], sum);
       }
       if (AHEAD && row + step < last) fetch(row + step, 0, u, v);
-      row_sum<2, SHORT>(sum, red, turn, lanes);
+      row_sum<2, SHORT>(sum, red, turn, lanes, SIDE ? place * (lanes >> 6) : 0);
+      if (!live) continue;
       const float rstd = 1.f / __builtin_sqrtf(sum[0] * inv_n + a.eps);
       const float f = rstd * rstd * (sum[1] * inv_n);
 #pragma unroll
@@ -308,8 +316,8 @@ __global__ void __launch_bounds__(C == 0 ? 512 : 1024) norm_grad_kernel(NormGrad
       }
       if constexpr (AHEAD) dy[0] = u, h[0] = v;
     }
-    if constexpr (SHORT) {  // the rows' parts of the workgroup, in their order
-      __shared__ float part[256 * 8];
+    if constexpr (SEVERAL) {  // the rows' parts of the workgroup, in their order
+      __shared__ float part[(SIDE ? 1024 : 256) * 8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) part[threadIdx.x * 8 + e] = dw[0][e];
       __syncthreads();
@@ -435,6 +443,7 @@ static const void* norm_grad_pick(int c) {
     case 1: return (const void*)&norm_grad_kernel<T, 1>;
     case 2: return (const void*)&norm_grad_kernel<T, 2>;
     case kLds: return (const void*)&norm_grad_kernel<T, kLds>;
+    case kSide: return (const void*)&norm_grad_kernel<T, kSide>;
     default: return (const void*)&norm_grad_kernel<T, 0>;
   }
 }

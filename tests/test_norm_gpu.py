@@ -113,7 +113,7 @@ def test_gradients(rows, n, dtype, wtype):
             within(dw, rw, tw)
 
 
-@pytest.mark.parametrize("rows,n", [(9001, 33), (3500, 1001), (1300, 9001), (700, 17001), (530, 39936), (600, 39937)])
+@pytest.mark.parametrize("rows,n", [(9001, 33), (3500, 1001), (2049, 1500), (20000, 1000), (9, 2560), (257, 3001), (1300, 9001), (700, 17001), (530, 39936), (600, 39937)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_many_rows(rows, n, dtype):
     """Several rows to a workgroup: what is kept from row to row, and the sums over rows, of rows of every length."""
