@@ -22,7 +22,7 @@ def violations(instructions):
     return bad
 
 
-def test_the_checker_flags_each_kind_of_mistake():
+def test_violations_of_each_kind_are_found():
     good = ["s_mov_b32 m0, s2", "s_nop 0", "buffer_load_dword v1, s[8:11], s3 offen lds", "s_mov_b32 m0, s2", "s_nop 0",
             "buffer_load_dwordx4 v1, s[8:11], s3 offen nt lds", "s_endpgm"]
     assert violations(good) == []
