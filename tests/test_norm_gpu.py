@@ -360,9 +360,9 @@ def test_autograd():
     assert torch.equal(torch.autograd.grad(y, x, dy.t().contiguous().t())[0], first[0])
 
 
-def test_captured_step():
+@pytest.mark.parametrize("rows,n", [(300, 1000), (600, 20001), (3, 60)])
+def test_captured_step(rows, n):
     """Forward and both gradients by plain calls in one graph, replayed on new values."""
-    rows, n = 300, 1000
     x, r, w = rand((rows, n), BF16, 1), rand((rows, n), BF16, 2), weights(n, F32, 3)
     dy, dh = rand((rows, n), BF16, 4), rand((rows, n), BF16, 5)
 
