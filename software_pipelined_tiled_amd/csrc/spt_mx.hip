@@ -79,6 +79,35 @@ __global__ void __launch_bounds__(256) mx_values_kernel(MxValuesArgs a) {
     const int rows = a.rows - row0 >= kMxUnitRows ? kMxUnitRows : a.rows > row0 ? (int)(a.rows - row0) : 0;
     if (has_scale_word(cg, a.blocks, threadIdx.x)) ((unsigned*)sc)[threadIdx.x] = ((const unsigned*)a.scales)[scale_word(row0, cg, a.blocks, threadIdx.x)];
     __syncthreads();
+    if constexpr (T == 2) {
+      // fp32 leaves in two pieces of 1 KiB a row, four neighbouring values a lane in each (8192 x 8192 from 4 bits: 72 us, 85 with
+      // eight neighbours a lane, whose 16-byte stores leave gaps)
+      const int col = cg * kUnitCols + lane * 4;
+#pragma unroll 4
+      for (int i = wave; i < rows; i += 4) {
+        const unsigned char* p = a.codes + (row0 + i) * row_bytes + (int64_t)col * BITS / 8;
+        u32x2 q = {0, 0};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (col + 256 * h < a.k) {
+            if constexpr (BITS == 8) q[h] = *(const unsigned*)(p + 256 * h);
+            else q[0] |= (unsigned)*(const unsigned short*)(p + 128 * h) << (16 * h);
+          }
+        float v[2][8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mx_values<BITS>(q, sc[(8 * h + (lane >> 3)) * kMxUnitRows + i], v[h]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int left = a.k - (col + 256 * h);
+          float* o = (float*)a.out + (row0 + i) * a.ldo + col + 256 * h;
+          if (left >= 4) *(u32x4_any*)o = __builtin_bit_cast(u32x4, f32x4{v[h][4 * h], v[h][4 * h + 1], v[h][4 * h + 2], v[h][4 * h + 3]});
+          else
+            for (int e = 0; e < left; ++e) o[e] = e == 0 ? v[h][4 * h] : e == 1 ? v[h][4 * h + 1] : v[h][4 * h + 2];
+        }
+      }
+      __syncthreads();
+      continue;
+    }
     const int col = cg * kUnitCols + lane * 8;
     if (col < a.k) {
 #pragma unroll 4

@@ -208,6 +208,20 @@ def test_dequantize_every_code_and_scale(bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("dtype", [F16, BF16, F32])
+@pytest.mark.parametrize("rows,k", [(1, 1), (2, 3), (17, 259), (65, 510), (33, 513), (5, 770), (70, 1023)])
+def test_dequantize_out(rows, k, dtype, bits):
+    """Rows apart and off their size's alignment: the values, and nothing beside them."""
+    q = int_operand(rows, k, bits, rows + k)
+    buf = torch.full((rows * (k + 5) + 3,), 7.0, dtype=dtype, device="cuda")
+    out = buf[3:].view(rows, k + 5)[:, :k]
+    assert spt.dequantize_mx(q, out=out) is out
+    want = values(q)[:, :k].to(F32).to(dtype)
+    assert torch.equal(out, want) and torch.equal(spt.dequantize_mx(q, dtype), want)
+    assert (buf[:3] == 7.0).all() and (buf[3:].view(rows, k + 5)[:, k:] == 7.0).all()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("rows,k", [(1, 1), (3, 32), (64, 128), (65, 95), (130, 500), (7, 1025)])
 def test_pack(rows, k, bits):
     g = gen(rows + k)
