@@ -39,7 +39,7 @@ struct MxPackArgs {
   unsigned char* out_codes;
   unsigned char* out_scales;
   int64_t rows, ldc, lds;
-  int k, blocks, bits;
+  int k, blocks;
   int64_t units;
 };
 
@@ -98,7 +98,7 @@ struct NormPartsArgs {
 
 const void* mx_quantize_fn(int dtype, int bits);
 const void* mx_values_fn(int dtype, int bits);
-const void* mx_pack_fn();
+const void* mx_pack_fn(int bits);
 // out: 0 the input's type, else bits; c: pieces of eight values to a thread (1, 2, and the 16-bit norms 4; up to 1024 threads), -1:
 // rows of `lanes` threads of 256, 0: rows of any length, 512 threads, -2: gradients with 32 bytes of LDS to a piece, 1024 threads, -3:
 // gradients with rows of `lanes` threads, whole waves, side by side

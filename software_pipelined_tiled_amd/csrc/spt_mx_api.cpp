@@ -300,10 +300,9 @@ gemm_status_t mx_pack(const void* codes, int64_t ldc, const void* scales, int64_
   a.rows = rows; a.ldc = ldc; a.lds = lds;
   a.k = (int)k;
   a.blocks = (int)mx_blocks(k);
-  a.bits = bits;
   const Units u = mx_units(rows, a.blocks);
   a.units = u.units;
-  return launch(mx_pack_fn(), dim3(u.grid), 256, 0, &a, stream);
+  return launch(mx_pack_fn(bits), dim3(u.grid), 256, 0, &a, stream);
 }
 
 gemm_status_t gemm_mx_workspace_bytes(const gemm_mx_t* p, int64_t* out) {
