@@ -86,8 +86,10 @@ gemm_status_t gemm_mx_run(const gemm_mx_t* p, const void* a_codes, const void* a
  * h = x + residual, rounded to `dtype` (x itself without a residual), and y = h / sqrt(mean(h^2) + eps) * weight over
  * rows of n: the statistics in fp32, y rounded once. dtype F16, BF16 or F32 for x, residual, h and y; weight [n] F16,
  * BF16 or F32, or NULL for ones. The sum of a row's squares has to stay inside fp32's range.
- *   h is written where `residual` is given, and may be x's or residual's own memory (the same rows), y x's.
- * Errors: as above; GEMM_ERR_INVALID (eps negative or not finite), GEMM_ERR_UNSUPPORTED (rows beyond 2^31 - 64, n beyond 2^24).
+ *   h is written where `residual` is given, and may be x's or residual's own memory (the same rows), y x's; h and y need
+ * memory of their own.
+ * Errors: as above; GEMM_ERR_INVALID (eps negative or not finite, h and y in the same memory), GEMM_ERR_UNSUPPORTED (rows
+ * beyond 2^31 - 64, n beyond 2^24).
  */
 typedef struct {
   int64_t rows, n;

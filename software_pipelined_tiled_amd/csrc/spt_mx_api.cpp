@@ -188,6 +188,16 @@ gemm_status_t check_norm(const norm_rms_t* p) {
   return GEMM_OK;
 }
 
+// Whether rows of two results share memory: exact for one row and for rows of one stride; of two strides only a common first address.
+bool rows_meet(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t row_bytes, int es) {
+  const __int128 d = a < b ? (const char*)b - (const char*)a : (const char*)a - (const char*)b;
+  if (d == 0 || rows == 1 || lda != ldb) return d == 0 || (rows == 1 && d < row_bytes);
+  const __int128 step = (__int128)lda * es;
+  if (d >= step * rows) return false;
+  const int64_t before = (int64_t)(d / step), rest = (int64_t)(d - before * step);  // the lower one's last row that begins ahead of the upper one
+  return rest < row_bytes || (before + 1 < rows && step - rest < row_bytes);
+}
+
 gemm_status_t run_norm(const norm_rms_t* p, int out, const void* x, const void* residual, const void* weight, void* h,
                        void* y, void* scales, void* stream) {
   gemm_status_t st = check_norm(p);
@@ -196,6 +206,10 @@ gemm_status_t run_norm(const norm_rms_t* p, int out, const void* x, const void* 
   if (p->ldx < p->n || (residual && (p->ldr < p->n || p->ldh < p->n)) || (!out && p->ldy < p->n)) return GEMM_ERR_INVALID;
   if (p->rows == 0 || p->n == 0) return GEMM_OK;
   if (!x || !y || (residual && !h) || (out && (!scales || !on16(y) || !on16(scales)))) return GEMM_ERR_INVALID;
+  if (residual) {  // x's memory may take h or y, but not both
+    const int es = p->dtype == GEMM_F32 ? 4 : 2;
+    if (out ? y == h || scales == h : rows_meet(y, p->ldy, h, p->ldh, p->rows, p->n * es, es)) return GEMM_ERR_INVALID;
+  }
   int cu = 0;
   st = device_cus(&cu);
   if (st != GEMM_OK) return st;

@@ -345,9 +345,11 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor | None = None, eps: float = 1
     """y = h / sqrt(mean(h^2) + eps) * weight over the rows of x [rows, n] (fp16, bf16 or fp32), in x's type; h = x, and
     the result is y. With a ``residual`` of x's shape and type h = x + residual, rounded to that type, and the result is
     (y, h). weight [n] fp16, bf16 or fp32, or None for ones. Statistics and products are fp32, y is rounded once; the sum
-    of a row's squares has to stay inside fp32's range. ``out`` may be x, ``residual_out`` x or residual; with either the
-    call takes no part in autograd."""
+    of a row's squares has to stay inside fp32's range. ``out`` may be x, ``residual_out`` x or residual, and the two need
+    memory of their own; with either the call takes no part in autograd."""
     if out is not None or residual_out is not None:
+        _need(out is None or residual_out is None or out.data_ptr() != residual_out.data_ptr() or not out.numel(),
+              "out and residual_out need memory of their own")
         _need(not _wants_grad(x, weight, residual, out, residual_out),
               "out= and residual_out= take no part in autograd; call under torch.no_grad()")
     elif _wants_grad(x, weight, residual):
