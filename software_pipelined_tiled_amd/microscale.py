@@ -150,8 +150,9 @@ def pack_mx(codes: torch.Tensor, scales: torch.Tensor, bits: int, k: int | None 
             dtype: torch.dtype = torch.bfloat16) -> MXTensor:
     """Lay out a checkpoint's rows: codes [rows, ceil(k * bits / 8)] bytes (of two 4-bit values the first in the low
     half; 8-bit ones may be float8_e4m3fn), scales [rows, ceil(k / 32)] bytes, exponents with a bias of 127. k: by
-    default all that the codes hold. ``dtype``: the products' default result."""
+    default all that the codes hold. ``dtype``: the products' default result. No gradient."""
     bits = _bits(bits)
+    _no_grad("pack_mx", codes, scales)  # of the 8-bit types: a view as bytes drops out of the graph
     if bits == 8 and codes.dtype == torch.float8_e4m3fn:
         codes = codes.view(torch.uint8)
     if scales.dtype == torch.float8_e8m0fnu:
