@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(256) mx_values_kernel(MxValuesArgs a) {
 typedef unsigned u32_byte __attribute__((aligned(1)));  // the memory path takes dwords at any byte
 typedef unsigned u32x2_byte __attribute__((ext_vector_type(2), aligned(1)));
 
-// Once per weight: a checkpoint's rows may begin anywhere. 28672 x 8192 in 4 bits: 97 us (47 at the rate of a large copy), in 8 bits 199 (94).
+// Once per weight: a checkpoint's rows may begin anywhere. 28672 x 8192 in 4 bits, from memory: 50 us (48 at the rate of a large copy), in
+// 8 bits 89 (94); with each row's last 512 columns taken byte by byte, though all there, 134 and 203.
 template <int BITS>
 __global__ void __launch_bounds__(256) mx_pack_kernel(MxPackArgs a) {
   __shared__ __attribute__((aligned(16))) unsigned char sc[kScaleBytes];
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(256) mx_pack_kernel(MxPackArgs a) {
     const int si = threadIdx.x >> 4, sb = cg * 16 + (threadIdx.x & 15);  // and a scale of each thread's
     const unsigned char* from = a.codes + (row0 + wave) * a.ldc + at;
     unsigned char* to = a.out_codes + (row0 + wave) * row_bytes + at;
-    if (rows == kMxUnitRows && (cg + 1) * kUnitCols < a.k) {  // all there: the loads before the first is used
+    if (rows == kMxUnitRows && (cg + 1) * kUnitCols <= a.k) {  // all there: the loads before the first is used
       const unsigned char scale = a.scales[(row0 + si) * a.lds + sb];
       unsigned q[4][2];
 #pragma unroll
