@@ -274,7 +274,7 @@ __device__ __forceinline__ i32x8 mx_operand(u32x4 lo, u32x4 hi) {
 // `lo`.
 template <int F, int P>
 __device__ __forceinline__ u32x4 mx_bf16(u32x4 lo, u32x4 hi, unsigned byte) {
-  const float f = byte == 255 ? __builtin_bit_cast(float, 0x7FC00000u) : mx_scale(byte);
+  const float f = __builtin_bit_cast(float, byte << 23);  // the conversions take its exponent alone: 0 is 2^-127, 255 NaN
   u32x4 r;
   if constexpr (F == 8) {
     const unsigned w0 = P < 2 ? lo[2 * P % 4] : hi[2 * P % 4], w1 = P < 2 ? lo[2 * P % 4 + 1] : hi[2 * P % 4 + 1];
@@ -290,6 +290,72 @@ __device__ __forceinline__ u32x4 mx_bf16(u32x4 lo, u32x4 hi, unsigned byte) {
     r[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, f, 3));
   }
   return r;
+}
+
+// ------------------------------------------------------------------------------ products through bf16 at any scale
+// A value times its scale is a bf16 number while the scale byte is in 10 .. 246 (2^-9 2^-117 is the smallest normal one, 448 2^119 is
+// finite). Blocks beyond that are far, and k-steps with one take mx_far_products.
+
+// Of words of four scale bytes: whether one is outside 64 .. 191, whose two highest bits are alike. OR a byte that nobody reads with 0x7F.
+__device__ __forceinline__ bool mx_wide(unsigned wa, unsigned wb) { return (~((wa ^ (wa << 1)) & (wb ^ (wb << 1))) & 0x80808080u) != 0; }
+
+// 0: near (NaN is), 1: low, 2: high.
+__device__ __forceinline__ int mx_reach(unsigned byte) { return byte < 10 ? 1 : byte > 246 && byte < 255 ? 2 : 0; }
+
+// Nonzero if one of a lane's fragments (N of them, bytes of `w`) has a far scale and a value that is not zero.
+template <int F, int N>
+__device__ __forceinline__ unsigned mx_far(const u32x4 (&x)[N][F / 4], unsigned w) {
+  unsigned any = 0;
+  static_for<N>([&](auto f_c) SPT_INLINE {
+    constexpr int f = decltype(f_c)::value;
+    unsigned codes = 0;
+#pragma unroll
+    for (int h = 0; h < F / 4; ++h) codes |= x[f][h][0] | x[f][h][1] | x[f][h][2] | x[f][h][3];
+    const unsigned from = ((w >> (8 * f)) & 255u) - 10;  // 0 .. 236: near, 245: NaN
+    any |= (from > 236) & (from != 245) ? codes & (F == 8 ? 0x7F7F7F7Fu : 0x77777777u) : 0u;
+  });
+  return any;
+}
+
+// mx_bf16 of a block of reach `u`, moved by 2^64 into bf16's range; zeros of another reach.
+template <int F, int P>
+__device__ __forceinline__ u32x4 mx_bf16_of(u32x4 lo, u32x4 hi, unsigned byte, int u) {
+  const bool own = mx_reach(byte) == u;
+  const u32x4 r = mx_bf16<F, P>(lo, hi, own ? byte + (unsigned)(u == 1 ? 64 : u == 2 ? -64 : 0) : 127u);
+  return own ? r : u32x4{0, 0, 0, 0};
+}
+
+// acc += the products of a k-step with far blocks in it: those of each pair of reaches by themselves, and back by their power of two. A
+// result without far blocks gets the same bits as without this.
+template <int FA, int FB, int FM, int FN>
+__device__ __forceinline__ void mx_far_products(const u32x4 (&x)[FM][FA / 4], const u32x4 (&y)[FN][FB / 4], unsigned wa, unsigned wb, f32x4 (&acc)[FM][FN]) {
+#pragma unroll 1
+  for (int pair = 0; pair < 9; ++pair) {
+    const int u = pair / 3, v = pair - 3 * u;
+    if (u == 1 && v == 1) continue;  // below 2^-217: nothing in fp32
+    const int back = (u == 1 ? -64 : u == 2 ? 64 : 0) + (v == 1 ? -64 : v == 2 ? 64 : 0);
+    static_for<FM>([&](auto i_c) SPT_INLINE {
+      constexpr int i = decltype(i_c)::value;
+      // what derives from the scales is not kept from pair to pair: it has no registers
+      const unsigned sa = opaque_u32(wa), sb = opaque_u32(wb);
+      f32x4 d[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) d[j] = back == 0 ? acc[i][j] : f32x4{0.f, 0.f, 0.f, 0.f};
+      static_for<4>([&](auto p_c) SPT_INLINE {
+        constexpr int p = decltype(p_c)::value;
+        const u32x4 xb = mx_bf16_of<FA, p>(x[i][0], x[i][FA / 4 - 1], (sa >> (8 * i)) & 255u, u);
+        static_for<FN>([&](auto j_c) SPT_INLINE {
+          constexpr int j = decltype(j_c)::value;
+          d[j] = mfma16<__bf16>(xb, mx_bf16_of<FB, p>(y[j][0], y[j][FB / 4 - 1], (sb >> (8 * j)) & 255u, v), d[j]);
+        });
+      });
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = back == 0 ? d[j][e] : acc[i][j][e] + __builtin_ldexpf(d[j][e], back);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+  }
 }
 
 }  // namespace spt

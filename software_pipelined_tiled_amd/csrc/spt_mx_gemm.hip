@@ -13,7 +13,9 @@
 // lane's results are four neighbouring columns, a quarter-wave's 128 bytes or more of a row.
 //
 // EXACT (8-bit operands with fp32 results): a lane reads both chunks of one 32-block instead, converts them to bf16 with
-// their scale, and runs four 16x16x32 bf16 instructions, whose sums lose nothing.
+// their scale, and runs four 16x16x32 bf16 instructions, whose sums lose nothing. A wave that meets a scale which carries its values out
+// of bf16's range takes that k-step in pieces (mx_far_products); looking for such scales costs up to 3 % (300 x 8192^2 8 x 8: 70 us, 69;
+// 128 x 5000 x 6000 22.6, 21.9).
 //
 // Scales go through LDS too (1 KiB a stage; 2 with 256 values of k): each wave loads those of one 64-row block.
 //   What bounds it: with few rows reading B (16 rows of 28672 x 8192 8 x 4: 30 us, 24 at the rate of a large copy), else its K-tiles'
@@ -99,6 +101,15 @@ __global__ void __launch_bounds__(256, 2) mx_tile_kernel(MxGemmArgs args) {
     }
   };
 
+  // EXACT: 0x7F in the scale bytes of rows that are not there (theirs are 0, a far one) and where a lane has fewer than four
+  unsigned near_a = 0, near_b = 0;
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      if (f >= FM || row0 + 16 * FM * wm + FM * r16 + f >= args.m) near_a |= 0x7Fu << (8 * f);
+      if (col0 + 64 * wn + 4 * r16 + f >= args.n) near_b |= 0x7Fu << (8 * f);
+    }
+  }
   f32x4 acc[FM][4];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -111,7 +122,20 @@ __global__ void __launch_bounds__(256, 2) mx_tile_kernel(MxGemmArgs args) {
     const int at = rowbytes == 128 ? row * 128 + ((c ^ (r16 & 7)) << 4) : row * 64 + ((c ^ ((r16 >> 1) & 3)) << 4);
     return *(const u32x4*)(p + at);
   };
-  auto compute = [&](int slot) SPT_INLINE {
+  // This lane's scale bytes of a k-step, as `compute` takes them. EXACT looks at them first, and has them read before the loads go out.
+  struct Words {
+    unsigned a, b;
+  };
+  auto scale_words = [&](const char* st) SPT_INLINE {
+    const int arow = (row0 & 63) + wm * 16 * FM;
+    const char* sa = st + A_BYTES + B_BYTES + (arow >> 6) * SC + (arow & 63) + FM * r16;
+    const char* sb = st + A_BYTES + B_BYTES + (2 + wn) * SC;
+    Words w;
+    w.a = FM == 4 ? *(const unsigned*)(sa + q4 * 64) : FM == 2 ? *(const unsigned short*)(sa + q4 * 64) : *(const unsigned char*)(sa + q4 * 64);
+    w.b = *(const unsigned*)(sb + q4 * 64 + 4 * r16);
+    return w;
+  };
+  auto compute = [&](int slot, const Words& early) SPT_INLINE {
     const char* st = smem + opaque_s32(slot * STAGE);
     const char* pa = st + wm * 16 * FM * RA;
     const char* pb = st + A_BYTES + wn * 64 * RB;
@@ -120,8 +144,8 @@ __global__ void __launch_bounds__(256, 2) mx_tile_kernel(MxGemmArgs args) {
     const char* sb = st + A_BYTES + B_BYTES + (2 + wn) * SC;
     static_for<KS>([&](auto s_c) SPT_INLINE {
       constexpr int s = decltype(s_c)::value;
-      const unsigned wa = FM == 4 ? *(const unsigned*)(sa + (4 * s + q4) * 64) : FM == 2 ? *(const unsigned short*)(sa + (4 * s + q4) * 64) : *(const unsigned char*)(sa + (4 * s + q4) * 64);
-      const unsigned wb = *(const unsigned*)(sb + (4 * s + q4) * 64 + 4 * r16);
+      const unsigned wa = EXACT ? early.a : FM == 4 ? *(const unsigned*)(sa + (4 * s + q4) * 64) : FM == 2 ? *(const unsigned short*)(sa + (4 * s + q4) * 64) : *(const unsigned char*)(sa + (4 * s + q4) * 64);
+      const unsigned wb = EXACT ? early.b : *(const unsigned*)(sb + (4 * s + q4) * 64 + 4 * r16);
       constexpr int CA = FA / 4, CB = FB / 4;  // chunks of a lane
       u32x4 x[FM][CA], y[4][CB];
 #pragma unroll
@@ -154,6 +178,23 @@ __global__ void __launch_bounds__(256, 2) mx_tile_kernel(MxGemmArgs args) {
       }
     });
   };
+  // EXACT: whether the k-step has a far block of this wave's rows; then its products are done here.
+  auto far_step = [&](int slot, const Words& w) SPT_INLINE {
+    if (__builtin_expect(!__any(mx_wide(w.a | near_a, w.b | near_b)), 1)) return false;
+    const char* st = smem + opaque_s32(slot * STAGE);
+    u32x4 x[FM][FA / 4], y[4][FB / 4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int h = 0; h < FB / 4; ++h) y[f][h] = chunk(st + A_BYTES + wn * 64 * RB, RB, f, FB == 4 ? q4 : 2 * q4 + h);
+#pragma unroll
+    for (int f = 0; f < FM; ++f)
+#pragma unroll
+      for (int h = 0; h < FA / 4; ++h) x[f][h] = chunk(st + wm * 16 * FM * RA, RA, f, 2 * q4 + h);
+    if (!__any((mx_far<FA, FM>(x, w.a) | mx_far<FB, 4>(y, w.b)) != 0)) return false;
+    mx_far_products<FA, FB, FM, 4>(x, y, w.a, w.b, acc);
+    return true;
+  };
 
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) issue(kt0 + i, i);
@@ -161,8 +202,12 @@ __global__ void __launch_bounds__(256, 2) mx_tile_kernel(MxGemmArgs args) {
   for (int kt = kt0; kt < kt1; ++kt) {
     wait_vmcnt<LW * (S - 2)>();  // this wave's share of K-tile kt has landed
     barrier_sync();              // everyone's has, and everyone has read K-tile kt - 1
+    Words w{};
+    if constexpr (EXACT) w = scale_words(smem + opaque_s32(slot * STAGE));
     issue(kt + S - 1, slot == 0 ? S - 1 : slot - 1);
-    compute(slot);
+    bool done = false;
+    if constexpr (EXACT) done = far_step(slot, w);
+    if (!done) compute(slot, w);
     slot = slot + 1 == S ? 0 : slot + 1;
   }
   wait_vmcnt<0>();
