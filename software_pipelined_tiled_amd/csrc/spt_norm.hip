@@ -26,8 +26,14 @@ constexpr int kShort = -1;  // C of rows that a part of a wave holds
 constexpr int kLds = -2;    // gradients: C of long rows with dweight's sums in LDS
 constexpr int kSide = -3;   // gradients: C of rows of several waves, with several of them side by side in a workgroup
 
+template <int CTRL>
+__device__ __forceinline__ float lanes_moved(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+
 // The sum of N values over the `lanes` threads of a row (a power of two up to 64, or all the workgroup's), to all of them, in a fixed
-// order. `red` holds two sets of N x 16 floats used in turn (`turn`), so that one barrier a call is enough. `wave0`: the row's first wave.
+// order: in pairs, of the waves' sums too (one after the other they are off by 1.6 times as much in the mean). `red` holds two sets of
+// N x 16 floats used in turn (`turn`), so that one barrier a call is enough. `wave0`: the row's first wave.
 template <int N, bool SHORT>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int turn, int lanes, int wave0 = 0) {
   if constexpr (SHORT) {
@@ -49,11 +55,14 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int turn, int
       for (int i = 0; i < N; ++i) r[i * 16 + (threadIdx.x >> 6)] = v[i];
     }
     __syncthreads();
+    const int w = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float t = 0.f;
-      for (int w = 0; w < waves; ++w) t += r[i * 16 + wave0 + w];
-      v[i] = t;
+      float t = w < waves ? r[i * 16 + wave0 + w] : 0.f;
+      t += lanes_moved<0xB1>(t);         // lanes 1 0 3 2 of four
+      t += lanes_moved<0x4E>(t);         // lanes 2 3 0 1
+      t += lanes_moved<0x141>(t);        // eight lanes backwards: the other four's sum
+      v[i] = t + lanes_moved<0x140>(t);  // sixteen lanes backwards: the other eight's
     }
   }
 }
