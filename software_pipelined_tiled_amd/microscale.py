@@ -49,20 +49,36 @@ _MX_ROWS, _MX_K = 2**31 - 64, 2**22  # the library's limits
 class MXTensor:
     """A microscaled tensor [rows, k] (made by ``quantize_mx``, ``pack_mx`` or ``rms_norm_mx``). bits: 8 (e4m3) or 4
     (e2m1). codes [rows, bytes], rows of whole 128 values, and scales [ceil(rows / 64), blocks, 64], the exponents of the
-    scales with a bias of 127 (255: NaN). dtype: what it was made from, the products' default result."""
+    scales with a bias of 127 (255: NaN). Codes and scales given here must be zeros behind k, and scales behind the last row: the products
+    read them. dtype: what it was made from, the products' default result. It may be pickled, and loaded where there is
+    no GPU; every call needs it on one (``to``)."""
     __slots__ = ("bits", "rows", "k", "dtype", "device", "codes_ptr", "scales_ptr", "_data", "_codes", "_scales")
 
     def __init__(self, codes: torch.Tensor, scales: torch.Tensor, bits: int, rows: int, k: int, dtype: torch.dtype):
+        self._hold(codes, scales, bits, rows, k, dtype)
+        if codes.data_ptr() % 16 or scales.data_ptr() % 16:
+            raise ValueError("codes and scales must begin on 16 bytes")
+        _on_device("codes scales", codes, scales)
+
+    def _hold(self, codes, scales, bits, rows, k, dtype):
         _lib.mx_bytes(rows, k, bits)
         for name, t, shape in zip(("codes", "scales"), (codes, scales), _shapes(rows, k, bits)):
-            if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous() or t.data_ptr() % 16:
-                raise ValueError(f"{name} must be contiguous bytes {shape} on 16 bytes")
-        _on_device("codes scales", codes, scales)
+            if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous bytes {shape}")
         if dtype not in _FLOATS:
             raise TypeError(f"unsupported dtype {dtype}")
         self.bits, self.rows, self.k, self.dtype, self.device = bits, rows, k, dtype, codes.device
         self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
         self._data, self._codes, self._scales = None, codes, scales
+        return self
+
+    def to(self, device) -> MXTensor:
+        """Itself where it is on ``device``, else a copy there."""
+        codes = self.codes.to(device)
+        if codes.device == self.device:
+            return self
+        parts = codes, self.scales.to(device), self.bits, self.rows, self.k, self.dtype
+        return MXTensor(*parts) if codes.is_cuda else _loaded(*parts)
 
     @property
     def shape(self) -> tuple[int, int]:
@@ -81,10 +97,22 @@ class MXTensor:
         return self._scales
 
     def __reduce__(self):  # a copy's addresses are its own tensors'
-        return MXTensor, (self.codes, self.scales, self.bits, self.rows, self.k, self.dtype)
+        return _loaded, (self.codes, self.scales, self.bits, self.rows, self.k, self.dtype)
 
     def __repr__(self) -> str:
         return f"MXTensor({self.rows} x {self.k}, {self.bits} bits, {self.device})"
+
+
+def _loaded(codes, scales, bits, rows, k, dtype) -> MXTensor:
+    """One that may lie in host memory."""
+    if codes.is_cuda or scales.is_cuda:
+        return MXTensor(codes, scales, bits, rows, k, dtype)
+    return MXTensor.__new__(MXTensor)._hold(codes, scales, bits, rows, k, dtype)
+
+
+def _on_gpu(name: str, q: MXTensor) -> None:
+    if q.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor; {name}.to(device) moves it")
 
 
 def _shapes(rows: int, k: int, bits: int):
@@ -134,6 +162,7 @@ def quantize_mx(x: torch.Tensor, bits: int = 8) -> MXTensor:
 
 def dequantize_mx(q: MXTensor, dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """The values of ``q``, [rows, k] in fp16, bf16 or fp32 (default: what it was made from), rounded once."""
+    _on_gpu("q", q)
     dtype = dtype or (q.dtype if out is None else out.dtype)
     code = _result_code(dtype)
     if out is not None:
@@ -178,6 +207,7 @@ def mx_matmul(a: MXTensor, b: MXTensor, out_dtype: torch.dtype | None = None, ou
     results of 8-bit operands go through bf16 instructions, whose sums keep all of fp32, at less than half the rate. No
     gradient."""
     dev = a.device
+    _on_gpu("a", a)
     if a.k != b.k:
         raise ValueError(f"a has rows of {a.k}, b of {b.k}")
     if b.device != dev:
