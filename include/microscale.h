@@ -77,6 +77,18 @@ typedef struct {
   int64_t ldc;
 } gemm_mx_t;
 gemm_status_t gemm_mx_workspace_bytes(const gemm_mx_t* p, int64_t* out);
+
+/*
+ * The kernel that a product takes, chosen from the sizes, formats and result type alone: kernel 0 few rows (bm of them, k shared by a
+ * workgroup's waves), 1 tiles, 2 tiles by two groups of waves; the tile bm x bn; splits, the parts of a sum; k_per_part, the values of k
+ * of one part (the last may have fewer); through_bf16, whether fp32 results of 8-bit operands take bf16 instructions.
+ */
+typedef struct {
+  int kernel, bm, bn, splits;
+  int64_t k_per_part;
+  int through_bf16;
+} gemm_mx_config_t;
+gemm_status_t gemm_mx_describe(const gemm_mx_t* p, gemm_mx_config_t* out);
 gemm_status_t gemm_mx_run(const gemm_mx_t* p, const void* a_codes, const void* a_scales, const void* b_codes,
                           const void* b_scales, void* C, void* workspace, int64_t workspace_bytes, void* stream);
 

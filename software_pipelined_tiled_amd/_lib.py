@@ -28,7 +28,7 @@ EXPERT_EXPORTS = ("experts_sort_workspace_bytes", "experts_sort", "experts_gathe
                   "gemm_w4_workspace_bytes", "gemm_w4_run")
 
 # every entry point include/microscale.h declares
-MX_EXPORTS = ("mx_bytes", "mx_quantize", "mx_dequantize", "mx_pack", "gemm_mx_workspace_bytes", "gemm_mx_run", "norm_rms_run",
+MX_EXPORTS = ("mx_bytes", "mx_quantize", "mx_dequantize", "mx_pack", "gemm_mx_workspace_bytes", "gemm_mx_describe", "gemm_mx_run", "norm_rms_run",
               "norm_rms_mx_run", "norm_rms_grad_workspace_bytes", "norm_rms_grad_run")
 GEMM_GROUPED_FORWARD, GEMM_GROUPED_GRAD_A, GEMM_GROUPED_GRAD_B = 0, 1, 2
 
@@ -74,6 +74,11 @@ class GemmW4(ctypes.Structure):
 class GemmMx(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("a_bits", ctypes.c_int),
                 ("b_bits", ctypes.c_int), ("out_dtype", ctypes.c_int), ("ldc", ctypes.c_int64)]
+
+
+class GemmMxConfig(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int), ("bm", ctypes.c_int), ("bn", ctypes.c_int), ("splits", ctypes.c_int),
+                ("k_per_part", ctypes.c_int64), ("through_bf16", ctypes.c_int)]
 
 
 class NormRms(ctypes.Structure):
@@ -154,6 +159,7 @@ def lib() -> ctypes.CDLL:
             ("mx_dequantize", [vp, vp, i32, i64, i64, vp, i32, i64, vp]),
             ("mx_pack", [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp]),
             ("gemm_mx_workspace_bytes", [P(GemmMx), P(i64)]),
+            ("gemm_mx_describe", [P(GemmMx), P(GemmMxConfig)]),
             ("gemm_mx_run", [P(GemmMx), vp, vp, vp, vp, vp, vp, i64, vp]),
             ("norm_rms_run", [P(NormRms), vp, vp, vp, vp, vp, vp]),
             ("norm_rms_mx_run", [P(NormRms), i32, vp, vp, vp, vp, vp, vp, vp]),
@@ -338,6 +344,13 @@ def gemm_mx_workspace_bytes(p: GemmMx) -> int:
     n = ctypes.c_int64()
     _check(lib().gemm_mx_workspace_bytes(ctypes.byref(p), ctypes.byref(n)), "gemm_mx_workspace_bytes")
     return n.value
+
+
+def gemm_mx_describe(p: GemmMx) -> dict:
+    """The kernel that a product takes, its tile, the parts of its sum."""
+    c = GemmMxConfig()
+    _check(lib().gemm_mx_describe(ctypes.byref(p), ctypes.byref(c)), "gemm_mx_describe")
+    return {f: getattr(c, f) for f, _ in GemmMxConfig._fields_}
 
 
 def norm_rms_grad_workspace_bytes(p: NormRmsGrad, wants_dweight: bool) -> int:

@@ -327,6 +327,20 @@ gemm_status_t gemm_mx_workspace_bytes(const gemm_mx_t* p, int64_t* out) {
   return st;
 }
 
+gemm_status_t gemm_mx_describe(const gemm_mx_t* p, gemm_mx_config_t* out) {
+  if (!out) return GEMM_ERR_INVALID;
+  MxShape s;
+  const gemm_status_t st = mx_shape(p, &s);
+  if (st != GEMM_OK) return st;
+  out->kernel = s.kernel <= kSkinny32 ? 0 : s.kernel == kTwoGroup ? 2 : 1;
+  out->bm = s.entry.bm;
+  out->bn = s.entry.bn;
+  out->splits = (int)s.splits;
+  out->k_per_part = s.per * s.entry.ksteps * 128;
+  out->through_bf16 = s.exact;
+  return GEMM_OK;
+}
+
 gemm_status_t gemm_mx_run(const gemm_mx_t* p, const void* a_codes, const void* a_scales, const void* b_codes,
                           const void* b_scales, void* C, void* workspace, int64_t workspace_bytes, void* stream) {
   MxShape s;
