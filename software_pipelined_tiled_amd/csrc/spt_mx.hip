@@ -5,9 +5,11 @@
 // four lanes a block of 32, so a row's piece is one 1 KiB load and its largest magnitudes two DPP steps. The scales of
 // 16 rows of a block lie together in memory and are collected in LDS, so that they leave 16 bytes at a time: written
 // row by row each would be a byte in a line of its own.
-//   8192 x 8192 bf16 to 4 bits: 28.9 us (32.5 at the rate of a large copy; part of it stays in the last cache), 28672 x 8192 to 8 bits
-// 119 (137), 301 x 8190 fp32 to 8 bits 5.0 (2.4); units of 64 rows, whose scales leave in whole lines, took 34.8, 143 and 9.6. The
-// values of the same 8192 x 8192: 32.5, with 64 rows 31.1, but 115 against 118 at 28672 rows and 5.1 against 9.8 at 1024 x 4096.
+//   Operands from memory, at the rate of a large copy in brackets: 8192 x 8192 bf16 to 4 bits 29 us (33; the result stays in the last
+// cache), to 8 bits 35 (40), 28672 x 8192 to 8 bits 121 (138), 301 x 8190 fp32 to 8 bits 5.4 (2.4); the values of 8192 x 8192 in bf16 from 4
+// bits 38 (33), of 28672 x 8192 from 8 bits 123 (138). Units of 64 rows, whose scales leave in whole lines, took, the same operands
+// again and again, 34.8 for 28.9, 143 for 119 and 9.6 for 5.0; for values 31.1 and 32.5, but 118 and 115 at 28672 rows and 9.8 and
+// 5.1 at 1024 x 4096.
 #include "spt_mx_device.h"
 
 namespace spt {
@@ -80,8 +82,8 @@ __global__ void __launch_bounds__(256) mx_values_kernel(MxValuesArgs a) {
     if (has_scale_word(cg, a.blocks, threadIdx.x)) ((unsigned*)sc)[threadIdx.x] = ((const unsigned*)a.scales)[scale_word(row0, cg, a.blocks, threadIdx.x)];
     __syncthreads();
     if constexpr (T == 2) {
-      // fp32 leaves in two pieces of 1 KiB a row, four neighbouring values a lane in each (8192 x 8192 from 4 bits: 72 us, 85 with
-      // eight neighbours a lane, whose 16-byte stores leave gaps)
+      // fp32 leaves in two pieces of 1 KiB a row, four neighbouring values a lane in each (8192 x 8192 from 4 bits, the same codes again:
+      // 72 us, 85 with eight neighbours a lane, whose 16-byte stores leave gaps; from memory 80)
       const int col = cg * kUnitCols + lane * 4;
 #pragma unroll 4
       for (int i = wave; i < rows; i += 4) {
@@ -128,8 +130,8 @@ __global__ void __launch_bounds__(256) mx_values_kernel(MxValuesArgs a) {
 typedef unsigned u32_byte __attribute__((aligned(1)));  // the memory path takes dwords at any byte
 typedef unsigned u32x2_byte __attribute__((ext_vector_type(2), aligned(1)));
 
-// Once per weight: a checkpoint's rows may begin anywhere. 28672 x 8192 in 4 bits, from memory: 50 us (48 at the rate of a large copy), in
-// 8 bits 89 (94); with each row's last 512 columns taken byte by byte, though all there, 134 and 203.
+// Once per weight: a checkpoint's rows may begin anywhere. 28672 x 8192 in 4 bits, from memory: 45 us (48 at the rate of a large copy), in
+// 8 bits 85 (94); with each row's last 512 columns taken byte by byte, though all there, 134 and 203.
 template <int BITS>
 __global__ void __launch_bounds__(256) mx_pack_kernel(MxPackArgs a) {
   __shared__ __attribute__((aligned(16))) unsigned char sc[kScaleBytes];

@@ -63,9 +63,11 @@ MxEntry mx_entry(MxKernel kernel, const gemm_mx_t* p, bool exact, bool planes) {
 // compute units (k-steps times what one takes, and the tile's own start and end) and the bytes; and, with parts, the second pass
 // over their planes. Tiles run two to a compute unit, and a workgroup alone on its own takes its k-steps faster. A workgroup draws only
 // so many bytes at once, so that fewer than 170 tiles do not fill the memory (1 x 8192 x 8192, 8 x 8: 16.9 us in four parts of 64 tiles,
-// 23.6 in two). The constants are a fit to 3400 measured shapes (1 .. 16384 rows, N 64 .. 28672, K 100 .. 14336); on 1800 of them the choice takes 2.3 % longer
-// than the best kernel of each shape, 82 % at worst (1386 x 11469 x 650, 4 x 4 in fp32: 34 us against 18), where rules on the
-// numbers of rows and tiles took 25 %.
+// 23.6 in two). The constants are a fit to 3400 measured shapes (1 .. 16384 rows, N 64 .. 28672, K 100 .. 14336); on 1800 of them the choice
+// takes 2.3 % longer than the best kernel of each shape, 82 % at worst (1386 x 11469 x 650, 4 x 4 in fp32: 34 us against 18), where rules on
+// the numbers of rows and tiles took 25 %. On 2000 other shapes of the same ranges it takes 3.6 % longer, more than 10 % on 268 of them, 58 %
+// at worst (2442 x 5248 x 192, 4 x 4: 15.6 us against 9.9 with two groups); the worst have sums of 100 to 700. Where power holds the
+// matrix cores back its times are too short (8192^3 8 x 8: 275 us, 364 measured), for all kernels alike.
 void mx_choose(const gemm_mx_t* p, MxShape* s) {
   // by format: 4 x 4, 8 x 4, 8 x 8, and the last two exact
   struct Cost {
@@ -143,7 +145,7 @@ struct NormShape {
   int c, lanes, threads, lds;
   int64_t per, grid;
 };
-// A thread has as few pieces as 1024 threads allow (with the residual: 300 rows of 4096 bf16 4.0 us, 4.3 with two pieces to half the
+// Figures here: the same operands again and again. A thread has as few pieces as 1024 threads allow (with the residual: 300 rows of 4096 bf16 4.0 us, 4.3 with two pieces to half the
 // threads; 1003 rows of 4097 fp32 12.8, 14.1), and a workgroup neighbouring rows, so that all workgroups are on the compute units at once
 // (6 waves to a SIMD, for the gradients' registers 5: 8192 rows of 4096 bf16 60 us, 65 with 6).
 NormShape norm_shape(int64_t rows, int64_t n, gemm_dtype_t dtype, bool mx, bool grad) {
@@ -373,7 +375,7 @@ gemm_status_t gemm_mx_run(const gemm_mx_t* p, const void* a_codes, const void* a
   a.plane = s.splits > 1 ? p->m * p->n : 0;
   a.units = (int)(s.tiles_m * s.tiles_n * s.splits);
   a.grid = s.kernel == kTwoGroup && a.units > cu ? cu : a.units;  // it walks over its tiles
-  // 16-bit stores write whole lines, and past the caches they are taken faster; fp32 ones are not (2236 x 24448 x 448: 115 us, 61)
+  // 16-bit stores write whole lines, and past the caches they are taken faster; fp32 ones are not (2236 x 24448 x 448: 115 us, 63)
   a.nt = s.splits == 1 && p->out_dtype != GEMM_F32;
   st = launch(s.entry.fn, dim3((unsigned)a.grid), s.entry.threads, 0, &a, stream);
   if (st != GEMM_OK || s.splits == 1) return st;

@@ -18,8 +18,10 @@
 // 128 x 5000 x 6000 22.6, 21.9).
 //
 // Scales go through LDS too (1 KiB a stage; 2 with 256 values of k): each wave loads those of one 64-row block.
-//   What bounds it: with few rows reading B (16 rows of 28672 x 8192 8 x 4: 30 us, 24 at the rate of a large copy), else its K-tiles'
-// latency and reads; the exact form the conversions (301 x 1025 x 8190 8 x 8: 19 us and 4 for the planes' sum, with bf16 results 16 in all).
+//   What bounds it: with few rows reading B (16 rows of 28672 x 8192 8 x 4: 30 us with part of B in the last cache, 35 from memory, 24 at
+// the rate of a large copy), else its K-tiles' latency and reads (256, 512, 1024 rows of 8192^2 8 x 8: 36, 55 and 78 us; 15, 16 and 32 at
+// the instruction's rate); the exact form the conversions (301 x 1025 x 8190 8 x 8: 19 us and 4 for the planes' sum, with bf16 results
+// 16 in all; 8192^3 965, where the two-group kernel takes 364 for bf16 results).
 #include "spt_mx_device.h"
 
 namespace spt {

@@ -24,8 +24,8 @@
 // Rows are staged permuted, so that scales arrive as words and results as 8 neighbouring columns: row r of fragment f is row
 // 4r + f of a wave's 64 A rows and 8r + f of its 128 B rows (one word, two words of scales; 16 lanes store 256 or 512
 // bytes of a row).
-//   8192^3, bf16 results: 8 x 8 353 us (3.1 PFLOP/s), 8 x 4 335, 4 x 4 229 (4.8); with 128-row tiles 714, 437 for 8 x 8 and 4 x 4.
-// The 8-bit forms keep the matrix cores 0.87 busy (0.81 at 4096 x 8192 x 4096, where a tile has half the k) at 1.5 to 1.55 GHz
+//   8192^3, bf16 results: 8 x 8 364 us (3.0 PFLOP/s), 8 x 4 340, 4 x 4 236 (4.7); with 128-row tiles 714, 437 for 8 x 8 and 4 x 4.
+// The 8-bit forms keep the matrix cores 0.87 busy (0.82 at 4096 x 8192 x 4096, where a tile has half the k) at 1.5 to 1.55 GHz
 // and are held by power. The 4-bit form, 0.60 to 0.64 busy at 1.77 GHz, is held by its memory phases: a K-tile's reads and loads move
 // 260 KiB through LDS in the 2048 cycles of its products, which are half as long as the 8-bit ones for as many bytes.
 #include "spt_mx_device.h"

@@ -6,18 +6,20 @@
 // caller gets, as where the addition is an operator of its own. Statistics and products are fp32, y and dx are rounded once.
 //
 // A workgroup has a row at a time, and takes several neighbouring rows, the next one's loads in flight while it adds up the
-// squares; rows of up to 512 values are a wave's or a part of one, several to a workgroup (30000 rows of 200: 9.8 us, 26 with a
-// wave to a row). Weights stay in registers from row to row where rows are short enough, and else come from the L2. With the
-// residual, at the rate of a large copy (5.16 TB/s) in brackets: 8191 rows of 8192 fp16 104 us (104), as 8-bit MX 97 (92), 2000
-// rows of 28672 bf16 101 (89; 105 without the loads ahead), as MX 106 (78: its registers have no room for them), 1003 rows of 4097
-// fp32 13.0 (12.8: part of it stays in the last cache), 1000 rows of 38400 fp16 in two passes 73 (60).
+// squares; rows of up to 512 values are a wave's or a part of one, several to a workgroup (30000 rows of 200 from the last cache: 9.8
+// us, 26 with a wave to a row). Weights stay in registers from row to row where rows are short enough, and else come from the L2. With the
+// residual, operands from memory, at the rate of a large copy (5.16 TB/s) in brackets: 8191 rows of 8192 fp16 106 us (104), as MX of 8
+// bits 97 (92), of 4 bits 92 (85); 8192 rows of 4096 bf16 56, 47 and 46 (52, 46, 43); 2000 rows of 28672 bf16 99 (89; 4 us more without the
+// loads ahead), as MX of 8 bits 103 (78: its four pieces have no loads ahead, and the row ends' lane masks, kept over the rows, fill the
+// scalar registers: 128 are spilled); 1003 rows of 4097 fp32 17 (13); 1000 rows of 38400 fp16 in two passes 80 (60).
 //
 // Gradients: sum h^2 and sum g h come out of one pass, so that r need not be kept by the forward. dweight's sums run
 // over a workgroup's rows in registers, for rows of more than 16384 values in LDS, and in its plane in memory for those that the
 // LDS does not hold either; they leave as one fp32 plane a workgroup, and are added in the planes' order by a second
 // kernel: no atomics, the same bits on every run. A workgroup has eight rows or more, so that the planes are few, with few rows side
-// by side. With dh: 8191 rows of 8192 fp16 116 us (104), 8192 of 4096 bf16 60 (52), 2000 of
-// 28672 bf16 138 (89; 185 with the sums in registers, which did not fit), 300 rows of 4096 10 (1.9: two launches).
+// by side. With dh, from memory: 8191 rows of 8192 fp16 113 us (104), 8192 of 4096 bf16 59 (52), 2000 of 28672 bf16 138 (89: each row's dy
+// and h are read twice, with nothing in flight from one row to the next; 185 with the sums in registers, which did not fit), 300 rows
+// of 4096 10.5 (1.9: two launches).
 #include "spt_mx_device.h"
 
 namespace spt {
@@ -32,7 +34,7 @@ __device__ __forceinline__ float lanes_moved(float v) {
 }
 
 // The sum of N values over the `lanes` threads of a row (a power of two up to 64, or all the workgroup's), to all of them, in a fixed
-// order: in pairs, of the waves' sums too (one after the other they are off by 1.6 times as much in the mean). `red` holds two sets of
+// order: in pairs, of the waves' sums too (one after the other they are off by 1.5 times as much in the mean). `red` holds two sets of
 // N x 16 floats used in turn (`turn`), so that one barrier a call is enough. `wave0`: the row's first wave.
 template <int N, bool SHORT>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* red, int turn, int lanes, int wave0 = 0) {
