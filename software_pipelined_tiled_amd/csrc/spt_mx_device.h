@@ -302,19 +302,38 @@ __device__ __forceinline__ bool mx_wide(unsigned wa, unsigned wb) { return (~((w
 // 0: near (NaN is), 1: low, 2: high.
 __device__ __forceinline__ int mx_reach(unsigned byte) { return byte < 10 ? 1 : byte > 246 && byte < 255 ? 2 : 0; }
 
+// The values of fragment `f` in a lane that are not zero, as bits.
+template <int F, int N>
+__device__ __forceinline__ unsigned mx_numbers(const u32x4 (&x)[N][F / 4], int f) {
+  unsigned codes = 0;
+#pragma unroll
+  for (int h = 0; h < F / 4; ++h) codes |= x[f][h][0] | x[f][h][1] | x[f][h][2] | x[f][h][3];
+  return codes & (F == 8 ? 0x7F7F7F7Fu : 0x77777777u);
+}
+
 // Nonzero if one of a lane's fragments (N of them, bytes of `w`) has a far scale and a value that is not zero.
 template <int F, int N>
 __device__ __forceinline__ unsigned mx_far(const u32x4 (&x)[N][F / 4], unsigned w) {
   unsigned any = 0;
   static_for<N>([&](auto f_c) SPT_INLINE {
     constexpr int f = decltype(f_c)::value;
-    unsigned codes = 0;
-#pragma unroll
-    for (int h = 0; h < F / 4; ++h) codes |= x[f][h][0] | x[f][h][1] | x[f][h][2] | x[f][h][3];
     const unsigned from = ((w >> (8 * f)) & 255u) - 10;  // 0 .. 236: near, 245: NaN
-    any |= (from > 236) & (from != 245) ? codes & (F == 8 ? 0x7F7F7F7Fu : 0x77777777u) : 0u;
+    any |= (from > 236) & (from != 245) ? mx_numbers<F, N>(x, f) : 0u;
   });
   return any;
+}
+
+// The reaches of the wave's blocks that are not zero, one bit each; near always.
+template <int F, int N>
+__device__ __forceinline__ int mx_reaches(const u32x4 (&x)[N][F / 4], unsigned w) {
+  unsigned low = 0, high = 0;
+  static_for<N>([&](auto f_c) SPT_INLINE {
+    constexpr int f = decltype(f_c)::value;
+    const int u = mx_reach((w >> (8 * f)) & 255u);
+    low |= u == 1 ? mx_numbers<F, N>(x, f) : 0u;
+    high |= u == 2 ? mx_numbers<F, N>(x, f) : 0u;
+  });
+  return 1 | (__any(low != 0) ? 2 : 0) | (__any(high != 0) ? 4 : 0);
 }
 
 // mx_bf16 of a block of reach `u`, moved by 2^64 into bf16's range; zeros of another reach.
@@ -325,14 +344,15 @@ __device__ __forceinline__ u32x4 mx_bf16_of(u32x4 lo, u32x4 hi, unsigned byte, i
   return own ? r : u32x4{0, 0, 0, 0};
 }
 
-// acc += the products of a k-step with far blocks in it: those of each pair of reaches by themselves, and back by their power of two. A
-// result without far blocks gets the same bits as without this.
+// acc += the products of a k-step with far blocks in it: those of each pair of reaches that is there by themselves, and back by their
+// power of two. A result without far blocks gets the same bits as without this.
 template <int FA, int FB, int FM, int FN>
 __device__ __forceinline__ void mx_far_products(const u32x4 (&x)[FM][FA / 4], const u32x4 (&y)[FN][FB / 4], unsigned wa, unsigned wb, f32x4 (&acc)[FM][FN]) {
+  const int ra = mx_reaches<FA, FM>(x, wa), rb = mx_reaches<FB, FN>(y, wb);
 #pragma unroll 1
   for (int pair = 0; pair < 9; ++pair) {
     const int u = pair / 3, v = pair - 3 * u;
-    if (u == 1 && v == 1) continue;  // below 2^-217: nothing in fp32
+    if (!(ra >> u & 1) || !(rb >> v & 1) || (u == 1 && v == 1)) continue;  // two low ones are below 2^-217: nothing in fp32
     const int back = (u == 1 ? -64 : u == 2 ? 64 : 0) + (v == 1 ? -64 : v == 2 ? 64 : 0);
     static_for<FM>([&](auto i_c) SPT_INLINE {
       constexpr int i = decltype(i_c)::value;
