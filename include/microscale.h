@@ -63,9 +63,11 @@ gemm_status_t mx_pack(const void* codes, int64_t ldc, const void* scales, int64_
  * F32, row stride ldc, rounded once from an fp32 sum.
  *   16-bit results, and all of 4 x 4, come from the scaled matrix instructions. For operands of 8 bits these keep, of
  * the products that they add at a time, 13 bits below the largest (on Gaussian data 1.5e-5 of a result's size for 8 x 8
- * and 5e-6 for 8 x 4, a hundredth and less of a 16-bit rounding). With F32 results operands of 8 bits go through
- * bf16 matrix instructions instead, whose sums are fp32 throughout, at less than half the rate; blocks with scales under
- * 2^-117 or over 2^119, whose values are no bf16 numbers, are moved into their range and back (those k-steps take three to five times as long).
+ * and 5e-6 for 8 x 4, some times that where a few columns are far larger, and under 5e-4 for any terms of independent
+ * signs: 15 products lose less than 2^-13 of a largest one, which is itself a term; a 16-bit rounding is 2e-4 or 1.7e-3).
+ * With F32 results operands of 8 bits go through bf16 matrix instructions instead, whose sums are fp32 throughout, at less than
+ * half the rate; blocks with scales under 2^-117 or over 2^119, whose values are no bf16 numbers, are moved into their
+ * range and back (those k-steps take three to five times as long).
  *   Few output tiles with a long sum are cut over workgroups into fp32 planes in the workspace, which a second kernel
  * adds in their order: results do not change from run to run.
  * Errors: as above; GEMM_ERR_UNSUPPORTED (4 x 8; ldc of 2^20 or more; more than 2^24 tiles of 32 x 64).

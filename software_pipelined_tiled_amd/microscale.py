@@ -237,8 +237,8 @@ def _result_code(dtype) -> int:
 def mx_linear(x: torch.Tensor, w: MXTensor, bits: int = 8, out_dtype: torch.dtype | None = None,
               out: torch.Tensor | None = None) -> torch.Tensor:
     """x [rows, k] quantised to ``bits`` and multiplied with the weight w [n, k]: [rows, n] in x's type or ``out_dtype``.
-    The same as ``mx_matmul(quantize_mx(x, bits), w)``, with one workspace. A 4-bit weight takes rows of 8 bits or 4, an
-    8-bit one rows of 8. No gradient."""
+    The same as ``mx_matmul(quantize_mx(x, bits), w)``, with one workspace, and with its sums: ``out_dtype=torch.float32`` keeps all
+    of fp32 in those of 8-bit rows. A 4-bit weight takes rows of 8 bits or 4, an 8-bit one rows of 8. No gradient."""
     code, bits, dev = _type("x", x, _FLOATS), _bits(bits), x.device
     _need(bits == 8 or w.bits == 4, "rows of 4 bits go with a 4-bit weight")
     if not x.is_cuda or w.device != dev:
